@@ -123,49 +123,65 @@ def _need(t, name, dtype=None, device=True):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+class _PoolHandle:
+    """Destroys its pa_pool_t when nothing refers to it any more: the Pool, and
+    every tensor that views its memory."""
+
+    def __init__(self):
+        self.ptr = ctypes.c_void_p()
+
+    def destroy(self):
+        if self.ptr:
+            lib.pa_pool_destroy(self.ptr)
+            self.ptr = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
 class _CudaArray:
     """Exposes a raw device buffer through __cuda_array_interface__ so torch can
-    view it without copying."""
+    view it without copying; torch keeps this object, and with it the buffer's
+    owner, as long as a view lives."""
 
-    def __init__(self, ptr, shape, typestr):
+    def __init__(self, ptr, shape, typestr, owner):
+        self.owner = owner
         self.__cuda_array_interface__ = {"shape": tuple(shape), "typestr": typestr,
                                          "data": (ptr, False), "version": 3, "strides": None}
 
 
 class Pool:
-    """Owns one pa_pool_t: K and V arrays [num_blocks][n_kv_heads][16][128]."""
+    """Owns one pa_pool_t: K and V arrays [num_blocks][n_kv_heads][16][128].
+    close() releases the memory at once (views of k and v must not be used
+    after it); a pool that is only dropped lives on as long as its views."""
 
     def __init__(self, num_blocks, n_kv_heads, dtype=torch.bfloat16, block_size=BLOCK_SIZE,
                  d_head=HEAD_DIM):
-        self._h = ctypes.c_void_p()
+        self._h = _PoolHandle()
         code = lib.pa_pool_create(num_blocks, block_size, n_kv_heads, d_head, _DTYPE_CODE[dtype],
-                                  ctypes.byref(self._h))
+                                  ctypes.byref(self._h.ptr))
         _check(code, "pa_pool_create")
         self.num_blocks, self.n_kv_heads, self.dtype = num_blocks, n_kv_heads, dtype
         self.device = torch.device("cuda", torch.cuda.current_device())
         k, v, nbytes = ctypes.c_void_p(), ctypes.c_void_p(), ctypes.c_size_t()
-        _check(lib.pa_pool_info(self._h, ctypes.byref(k), ctypes.byref(v), ctypes.byref(nbytes)), "pa_pool_info")
+        _check(lib.pa_pool_info(self._h.ptr, ctypes.byref(k), ctypes.byref(v), ctypes.byref(nbytes)), "pa_pool_info")
         self.bytes_per_pool = nbytes.value
         shape = (num_blocks, n_kv_heads, BLOCK_SIZE, HEAD_DIM)
         # views of the library-owned memory (int16 carrier, reinterpreted)
-        self.k = torch.as_tensor(_CudaArray(k.value, shape, "<i2"), device=self.device).view(dtype)
-        self.v = torch.as_tensor(_CudaArray(v.value, shape, "<i2"), device=self.device).view(dtype)
+        self.k = torch.as_tensor(_CudaArray(k.value, shape, "<i2", self._h), device=self.device).view(dtype)
+        self.v = torch.as_tensor(_CudaArray(v.value, shape, "<i2", self._h), device=self.device).view(dtype)
 
     @property
     def handle(self):
-        return self._h
+        return self._h.ptr
 
     def close(self):
-        if self._h:
+        if self._h.ptr:
             self.k = self.v = None
-            lib.pa_pool_destroy(self._h)
-            self._h = ctypes.c_void_p()
-
-    def __del__(self):
-        try:
-            self.close()
-        except Exception:
-            pass
+            self._h.destroy()
 
 
 def pa_pool_bytes(num_blocks, n_kv_heads, dtype, block_size=BLOCK_SIZE, d_head=HEAD_DIM):
