@@ -119,6 +119,39 @@ int pa_pool_shape(pa_pool_t pool, int* num_blocks, int* n_kv_heads,
 int pa_cache_append(pa_pool_t pool, const void* k_new, const void* v_new,
                     const int64_t* slot_mapping, int n_tok, void* stream);
 
+/* Cache write with rotary positions of one or several axes (time, height,
+ * width, ...): what a model does to a new token's q and k before the cache
+ * sees them, and the write itself, in one pass.  For token n, head h and pair
+ * f < rot_dim/2, with angle a = positions[axis_of_pair[f]][n] * inv_freq[f]:
+ *   (x, y) -> (x cos a - y sin a, y cos a + x sin a),
+ * (x, y) the head's dims (f, f + rot_dim/2), or (2f, 2f+1) with interleaved;
+ * dims past rot_dim pass through.  Query rows go to q_out, key rows to slot
+ * slot_mapping[n] of the cache, v_new rows to the same slot unturned.
+ *   q, q_out     : device, token n's heads [n_q_heads][128] at n * q_stride
+ *                  (q_out_stride) elements; pool dtype.  q_out may be q with
+ *                  the same stride, and may not overlap the inputs otherwise.
+ *   k_new, v_new : device, [n_kv_heads][128] at n * k_stride (v_stride): rows
+ *                  may be slices of one fused projection.
+ *   positions    : device int32 [n_axes][n_tok]; any value (the angle is
+ *                  reduced without loss of precision at far positions).
+ *   axis_of_pair : HOST uint8 [rot_dim/2], each < n_axes, read before the
+ *                  call returns.
+ *   inv_freq     : device fp32 [rot_dim/2].
+ *   slot_mapping : as for pa_cache_append; a token whose slot is negative (or
+ *                  out of range, which is reported) writes no K/V, its q is
+ *                  still turned.
+ * Pointers are 16-byte aligned and strides multiples of 8 elements that hold
+ * a token's heads (else INVALID).  rot_dim is a multiple of 16 up to 128, 1 <=
+ * n_axes <= PA_MAX_ROPE_AXES, n_q_heads <= PA_MAX_ROPE_HEADS (else
+ * UNSUPPORTED).  Arithmetic is fp32, rounded once to the pool's type.
+ * n_tok == 0 is a no-op. */
+enum { PA_MAX_ROPE_AXES = 4, PA_MAX_ROPE_HEADS = 65536 };
+int pa_rope_append(pa_pool_t pool, const void* q, int64_t q_stride, int n_q_heads, const void* k_new,
+                   int64_t k_stride, const void* v_new, int64_t v_stride, const int32_t* positions,
+                   int n_axes, const uint8_t* axis_of_pair, const float* inv_freq, int rot_dim,
+                   int interleaved, const int64_t* slot_mapping, int n_tok, void* q_out,
+                   int64_t q_out_stride, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Decode attention over the paged cache ("Serving" 23.2 and 23.4).
  * For sequence i and query head h, with kv head g = h / (n_q_heads/n_kv_heads)
@@ -248,6 +281,91 @@ int pa_decode_cascade(pa_pool_t pool, const void* q, const int32_t* block_tables
                       void* out, int out_dtype, void* workspace, size_t workspace_bytes,
                       void* stream);
 
+/* Shared-prefix decode for groups of any size: pa_decode's result, with each
+ * group's shared prefix attended once for all of its members as a matrix
+ * product (pa_decode_cascade takes at most 8 / G members a group and walks
+ * the prefix with each sequence's few query heads).  Group k's members are
+ * members[group_start[k] .. group_start[k+1]-1] (device int32, n_members =
+ * group_start[n_groups] in all); they share their first prefix_blocks[k]
+ * table entries, each full (16 * prefix_blocks[k] <= every member's length);
+ * a prefix of 0 blocks is allowed.  pa_cascade_groups with max_members =
+ * num_seqs finds such groups.  A sequence in no group is decoded alone.
+ * A group that breaks these rules, or names a sequence that is named more than
+ * once, is reported (PA_ERR_DEVICE_CHECK) and its members are decoded without
+ * it; a group_start that does not run from 0 to n_members, or has an empty
+ * group, is reported and no group takes part.  A shared block id out of range
+ * is skipped for every member (reported).
+ * q, out, block_tables, seq_lens as for pa_decode.  With a 16-bit out the
+ * prefix's weights are rounded to the pool's 16 bits for the value product
+ * (2^-9 or 2^-12 of each, against an output rounded by as much); with fp32
+ * out they are carried as a high and a low half (2^-17).  The result does not
+ * depend on timing.
+ * num_seqs and n_groups <= 4096 (else UNSUPPORTED); n_members <= num_seqs,
+ * num_seqs * max_blocks_per_seq < 2^31 (else INVALID).  workspace: device, >=
+ * pa_decode_shared_workspace_bytes(...), 256-byte aligned, caller-owned. */
+size_t pa_decode_shared_workspace_bytes(pa_pool_t pool, int num_seqs, int n_q_heads,
+                                        int max_blocks_per_seq, int n_groups);
+int pa_decode_shared(pa_pool_t pool, const void* q, const int32_t* block_tables,
+                     int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs, int n_q_heads,
+                     float scale, const int32_t* group_start, const int32_t* members, int n_members,
+                     const int32_t* prefix_blocks, int n_groups, void* out, int out_dtype,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Decode that also sums the attention weights, the measure by which pa_evict
+ * ranks cached tokens.  out as pa_decode_split's (partition_blocks 0), and
+ * for every kv head g and position t < L:
+ *   weights[i][g][t] = decay * weights[i][g][t] + sum_h softmax(scale K q_h)[t]
+ * over the query heads h of kv head g.
+ *   weights : device fp32 [num_seqs][n_kv_heads][16 * max_blocks_per_seq],
+ *             row i of table row i, 16-byte aligned; positions t >= L are
+ *             left as they are.  A new token's sum starts as whatever it
+ *             holds: start with zeros (pa_evict clears what it frees).
+ *   decay   : 1 accumulates; below 1 earlier steps fade.
+ * A position whose block id is out of range counts as not attended (reported
+ * by pa_check).  workspace: device, >= pa_decode_weights_workspace_bytes(...),
+ * 256-byte aligned, caller-owned; it holds the scores (4 bytes a query head
+ * and table position) and the split's records.  num_seqs <= 4096 (else
+ * UNSUPPORTED). */
+size_t pa_decode_weights_workspace_bytes(pa_pool_t pool, int num_seqs, int n_q_heads,
+                                         int max_blocks_per_seq);
+int pa_decode_weights(pa_pool_t pool, const void* q, const int32_t* block_tables,
+                      int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs, int n_q_heads,
+                      float scale, void* out, int out_dtype, float* weights, float decay,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Eviction from the cache by accumulated weight.  Each kv head of sequence i
+ * keeps n = min(keep[i], L) of its L tokens: the first n_sink, the last
+ * n_recent (as many of each as n allows, the first ones first), and of the
+ * others those with the largest weights[i][g][t]; of equal sums the lowest
+ * position stays, NaN ranks below every number.  The kept tokens close up in
+ * their order: K and V rows move to positions 0 .. n-1 of the destination
+ * table, bit for bit (rotary positions are in the keys, so nothing is turned
+ * again), and the sums with them; heads of one sequence may keep different
+ * tokens.  Afterwards attention over n tokens is attention over the kept ones.
+ *   weights      : device fp32 [num_seqs][n_kv_heads][16*max_blocks_per_seq].
+ *   weights_out  : same shape; weights itself, or no part of it.  [0, n) get
+ *                  the kept sums, [n, L) zeros; from L on left as they are.
+ *   block_tables : the tables the tokens are read through.
+ *   dst_tables   : device int32 [num_seqs][dst_blocks_per_seq], the tables
+ *                  they are written through, or NULL: block_tables (in place).
+ *                  Entry j < ceil(n/16) is either entry j of the sequence's
+ *                  own block_tables row, held by this sequence alone, or a
+ *                  block that no sequence of the call reads; no block serves
+ *                  two destinations.  pa_alloc_evict gives such tables.
+ *   seq_lens, keep : device int32 [num_seqs].  A length out of range or a
+ *                  negative keep is clamped and reported by pa_check, and so
+ *                  is a keep past 16*dst_blocks_per_seq.
+ *   seq_lens_out : device int32 [num_seqs] <- n; not seq_lens or keep.
+ *   kept         : device int32 [num_seqs][n_kv_heads][16*max_blocks_per_seq]
+ *                  <- the kept positions, ascending, in [0, n); the rest is
+ *                  left as it is.
+ * A row whose source or destination block is out of range is not moved
+ * (reported).  num_seqs == 0 is a no-op; num_seqs <= 65535 (else UNSUPPORTED). */
+int pa_evict(pa_pool_t pool, const float* weights, float* weights_out, const int32_t* block_tables,
+             int max_blocks_per_seq, const int32_t* dst_tables, int dst_blocks_per_seq,
+             const int32_t* seq_lens, const int32_t* keep, int num_seqs, int n_sink, int n_recent,
+             int32_t* seq_lens_out, int32_t* kept, void* stream);
+
 /* Split-KV decode that allocates nothing (the pages have no counterpart; this
  * is a deployment convenience).  Some callers cannot call cudaMalloc at the
  * time they decode: a serving loop whose device memory budget is fixed up
@@ -356,6 +474,17 @@ int pa_alloc_extend(pa_alloc_t a, int seq, int n, int64_t* slots,
                     int32_t* cow_src, int32_t* cow_dst, int* n_done);
 /* Releases the sequence's blocks (see policy) and forgets the sequence. */
 int pa_alloc_seq_free(pa_alloc_t a, int seq);
+/* The tables for a pa_evict call over n sequences (host arrays seqs, keep;
+ * each sequence at most once).  Sequence seqs[k] shrinks to keep[k] tokens (one
+ * that holds no more is left alone): of its first ceil(keep[k]/16) blocks
+ * those that other sequences hold too are replaced by new ones, the others
+ * stay and leave the prefix-cache index (their contents change), and the
+ * blocks behind them are released.  Its later tokens are not hashed.  Read the
+ * old tables (pa_alloc_table) before this call and the new ones after it, and
+ * launch pa_evict before anything else writes to released blocks.  All new
+ * blocks are taken before any is released.  INVALID (unknown or repeated
+ * sequence, keep < 0) and OOM change nothing. */
+int pa_alloc_evict(pa_alloc_t a, const int* seqs, const int* keep, int n);
 /* Copies up to cap table entries into out; *n_blocks = the table's length. */
 int pa_alloc_table(pa_alloc_t a, int seq, int32_t* out, int cap,
                    int* n_blocks);

@@ -47,6 +47,13 @@ def _load():
         "pa_pool_info": (i32, [vp, ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(sz)]),
         "pa_pool_shape": (i32, [vp] + [ctypes.POINTER(i32)] * 4),
         "pa_cache_append": (i32, [vp, vp, vp, vp, i32, vp]),
+        "pa_rope_append": (i32, [vp, vp, i64, i32, vp, i64, vp, i64, vp, i32, vp, vp, i32, i32, vp, i32, vp, i64, vp]),
+        "pa_decode_weights_workspace_bytes": (sz, [vp, i32, i32, i32]),
+        "pa_decode_weights": (i32, [vp, vp, vp, i32, vp, i32, i32, f32, vp, i32, vp, f32, vp, sz, vp]),
+        "pa_decode_shared_workspace_bytes": (sz, [vp, i32, i32, i32, i32]),
+        "pa_decode_shared": (i32, [vp, vp, vp, i32, vp, i32, i32, f32, vp, vp, i32, vp, i32, vp, i32, vp, sz, vp]),
+        "pa_evict": (i32, [vp, vp, vp, vp, i32, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp]),
+        "pa_alloc_evict": (i32, [vp, vp, vp, i32]),
         "pa_decode": (i32, [vp, vp, vp, i32, vp, i32, i32, f32, vp, i32, vp]),
         "pa_decode_workspace_bytes": (sz, [vp, i32, i32, i32, i32]),
         "pa_decode_split": (i32, [vp, vp, vp, i32, vp, i32, i32, f32, vp, i32, i32, vp, sz, vp]),
@@ -288,9 +295,11 @@ def pa_decode_multi(pool, q, q_start, block_tables, seq_lens, scale, out, worksp
                                workspace.numel() * workspace.element_size(), _stream(stream)), "pa_decode_multi")
 
 
-def cascade_groups(block_tables, seq_lens, n_q_heads, n_kv_heads):
+def cascade_groups(block_tables, seq_lens, n_q_heads, n_kv_heads, max_members=None):
     """Host: (group_start, members, prefix_blocks) int32 numpy arrays for
-    pa_decode_cascade from host tables [B][W] and lengths [B]."""
+    pa_decode_cascade from host tables [B][W] and lengths [B].  max_members: the
+    largest group, by default what pa_decode_cascade takes (8 / G); the batch
+    size for pa_decode_shared."""
     import numpy as np
     t = np.ascontiguousarray(block_tables, dtype=np.int32)
     lens = np.ascontiguousarray(seq_lens, dtype=np.int32)
@@ -300,7 +309,7 @@ def cascade_groups(block_tables, seq_lens, n_q_heads, n_kv_heads):
     pre = np.zeros(max(B, 1), np.int32)
     ng = ctypes.c_int()
     _check(lib.pa_cascade_groups(t.ctypes.data_as(ctypes.c_void_p), B, W, lens.ctypes.data_as(ctypes.c_void_p),
-                                 MAX_GROUP // (n_q_heads // n_kv_heads), gs.ctypes.data_as(ctypes.c_void_p),
+                                 MAX_GROUP // (n_q_heads // n_kv_heads) if max_members is None else int(max_members), gs.ctypes.data_as(ctypes.c_void_p),
                                  mem.ctypes.data_as(ctypes.c_void_p), pre.ctypes.data_as(ctypes.c_void_p),
                                  ctypes.byref(ng)), "pa_cascade_groups")
     n = ng.value
@@ -325,6 +334,158 @@ def pa_decode_cascade(pool, q, block_tables, seq_lens, scale, out, group_start, 
                                  _ptr(prefix_blocks) if ng else None, ng, _ptr(out), _DTYPE_CODE[out.dtype],
                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
            "pa_decode_cascade")
+
+
+def _on_pool(pool, **tensors):
+    """Tensors of one call live on the pool's device."""
+    for name, t in tensors.items():
+        if t is not None and t.device != pool.device:
+            raise ValueError(f"{name} must be on the pool's device {pool.device}, got {t.device}")
+
+
+def _workspace(nbytes, what, device, stream):
+    """A workspace for one call; the allocator may hand it out again only after
+    `stream` is done with it."""
+    if nbytes == 0:
+        raise PagedAttentionError(PA_ERR_INVALID, what)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def _heads(t, name, n_tok, n_heads, dtype):
+    """Checks [n_tok][n_heads][128] rows with contiguous heads; returns the token stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (n_tok, n_heads, HEAD_DIM):
+        raise ValueError(f"{name} must be [{n_tok}][{n_heads}][{HEAD_DIM}], got {tuple(t.shape)}")
+    if n_tok and (t.stride(2) != 1 or (n_heads > 1 and t.stride(1) != HEAD_DIM)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if n_tok > 1 else n_heads * HEAD_DIM
+
+
+def pa_rope_append(pool, q, k_new, v_new, positions, inv_freq, axis_of_pair, slot_mapping, q_out, interleaved=False,
+                   stream=None):
+    """Rotary positions of one or several axes on new tokens' q and k, with the
+    cache write of k and v (see include/pa.h).  q and q_out [n][Hq][128], k_new
+    and v_new [n][Hkv][128] with any token stride (slices of a fused projection
+    work), positions int32 [n_axes][n], inv_freq fp32 [rot_dim/2],
+    axis_of_pair: rot_dim/2 ints on the host, slot_mapping int64 [n].  q_out may
+    be q."""
+    _need(slot_mapping, "slot_mapping", torch.int64)
+    _need(positions, "positions", torch.int32)
+    _need(inv_freq, "inv_freq", torch.float32)
+    n = slot_mapping.numel()
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.dim() != 3:
+        raise ValueError("q must be [n_tok][Hq][128]")
+    Hq = q.shape[1]
+    qs = _heads(q, "q", n, Hq, pool.dtype)
+    ks = _heads(k_new, "k_new", n, pool.n_kv_heads, pool.dtype)
+    vs = _heads(v_new, "v_new", n, pool.n_kv_heads, pool.dtype)
+    os_ = _heads(q_out, "q_out", n, Hq, pool.dtype)
+    axes = [int(a) for a in axis_of_pair]
+    if positions.dim() != 2 or positions.shape[1] != n:
+        raise ValueError("positions must be [n_axes][n_tok]")
+    if inv_freq.shape != (len(axes),):
+        raise ValueError("inv_freq and axis_of_pair must have rot_dim / 2 entries each")
+    if any(a < 0 or a > 255 for a in axes):
+        raise ValueError("axis_of_pair holds axes of positions")
+    _on_pool(pool, q=q, k_new=k_new, v_new=v_new, positions=positions, inv_freq=inv_freq, slot_mapping=slot_mapping,
+             q_out=q_out)
+    _check(lib.pa_rope_append(pool.handle, _ptr(q), qs, Hq, _ptr(k_new), ks, _ptr(v_new), vs, _ptr(positions),
+                              positions.shape[0], bytes(axes), _ptr(inv_freq), 2 * len(axes), int(bool(interleaved)),
+                              _ptr(slot_mapping), n, _ptr(q_out), os_, _stream(stream)), "pa_rope_append")
+
+
+def shared_workspace_for(pool, q, block_tables, prefix_blocks, stream=None):
+    """Workspace of pa_decode_shared for these sizes."""
+    n = lib.pa_decode_shared_workspace_bytes(pool.handle, q.shape[0], q.shape[1], block_tables.shape[1],
+                                             prefix_blocks.shape[0])
+    return _workspace(n, "pa_decode_shared_workspace_bytes", pool.device, stream)
+
+
+def pa_decode_shared(pool, q, block_tables, seq_lens, scale, out, group_start, members, prefix_blocks, workspace=None,
+                     stream=None):
+    """pa_decode with each group's shared prefix attended once for all of its
+    members, groups of any size (see include/pa.h); the group arrays are int32
+    device tensors (cascade_groups with max_members=B finds them)."""
+    B, Hq, W = _decode_args(pool, q, block_tables, seq_lens, out)
+    for t, name in ((group_start, "group_start"), (members, "members"), (prefix_blocks, "prefix_blocks")):
+        _need(t, name, torch.int32)
+    ng, nm = prefix_blocks.numel(), members.numel()
+    if prefix_blocks.dim() != 1 or members.dim() != 1 or group_start.shape != (ng + 1,):
+        raise ValueError("shapes: group_start [n_groups+1], members [n_members], prefix_blocks [n_groups]")
+    if workspace is None:
+        workspace = shared_workspace_for(pool, q, block_tables, prefix_blocks, stream)
+    _on_pool(pool, q=q, block_tables=block_tables, seq_lens=seq_lens, out=out, group_start=group_start,
+             members=members, prefix_blocks=prefix_blocks, workspace=workspace)
+    _check(lib.pa_decode_shared(pool.handle, _ptr(q), _ptr(block_tables), W, _ptr(seq_lens), B, Hq, float(scale),
+                                _ptr(group_start), _ptr(members), nm, _ptr(prefix_blocks), ng, _ptr(out),
+                                _DTYPE_CODE[out.dtype], _ptr(workspace),
+                                workspace.numel() * workspace.element_size(), _stream(stream)), "pa_decode_shared")
+
+
+def weights_workspace_for(pool, q, block_tables, stream=None):
+    """Workspace of pa_decode_weights for these sizes."""
+    n = lib.pa_decode_weights_workspace_bytes(pool.handle, q.shape[0], q.shape[1], block_tables.shape[1])
+    return _workspace(n, "pa_decode_weights_workspace_bytes", pool.device, stream)
+
+
+def _weights_arg(pool, t, name, B, W, dtype=torch.float32):
+    _need(t, name, dtype)
+    if t.shape != (B, pool.n_kv_heads, W * BLOCK_SIZE):
+        raise ValueError(f"{name} must be [B][n_kv_heads][16 * W]")
+
+
+def pa_decode_weights(pool, q, block_tables, seq_lens, scale, out, weights, decay=1.0, workspace=None, stream=None):
+    """pa_decode_split that also adds each cached token's attention weight to
+    weights [B][Hkv][16*W] (fp32): weights = decay * weights + the weights of
+    this step, summed over the query heads of a kv head (see include/pa.h)."""
+    B, Hq, W = _decode_args(pool, q, block_tables, seq_lens, out)
+    _weights_arg(pool, weights, "weights", B, W)
+    if workspace is None:
+        workspace = weights_workspace_for(pool, q, block_tables, stream)
+    _on_pool(pool, q=q, block_tables=block_tables, seq_lens=seq_lens, out=out, weights=weights, workspace=workspace)
+    _check(lib.pa_decode_weights(pool.handle, _ptr(q), _ptr(block_tables), W, _ptr(seq_lens), B, Hq, float(scale),
+                                 _ptr(out), _DTYPE_CODE[out.dtype], _ptr(weights), float(decay), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)), "pa_decode_weights")
+
+
+def pa_evict(pool, weights, block_tables, seq_lens, keep, seq_lens_out, kept, n_sink=0, n_recent=0, dst_tables=None,
+             weights_out=None, stream=None):
+    """Keeps the heaviest keep[i] tokens of each kv head of sequence i, with the
+    first n_sink and the last n_recent always among them, and closes the cache
+    up in order (see include/pa.h).  In place unless dst_tables [B][Wd] is given;
+    weights_out defaults to weights.  seq_lens_out int32 [B] and kept int32
+    [B][Hkv][16*W] are written."""
+    _need(block_tables, "block_tables", torch.int32); _need(seq_lens, "seq_lens", torch.int32)
+    _need(keep, "keep", torch.int32); _need(seq_lens_out, "seq_lens_out", torch.int32)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [B][W]")
+    B, W = block_tables.shape
+    if seq_lens.shape != (B,) or keep.shape != (B,) or seq_lens_out.shape != (B,):
+        raise ValueError("seq_lens, keep and seq_lens_out must be [B]")
+    weights_out = weights if weights_out is None else weights_out
+    _weights_arg(pool, weights, "weights", B, W); _weights_arg(pool, weights_out, "weights_out", B, W)
+    _weights_arg(pool, kept, "kept", B, W, torch.int32)
+    if dst_tables is not None:
+        _need(dst_tables, "dst_tables", torch.int32)
+        if dst_tables.dim() != 2 or dst_tables.shape[0] != B:
+            raise ValueError("dst_tables must be [B][Wd]")
+        if dst_tables.shape[1] == 0:  # (an empty tensor has a null pointer, which would mean in place)
+            raise PagedAttentionError(PA_ERR_INVALID, "pa_evict")
+    _on_pool(pool, weights=weights, block_tables=block_tables, seq_lens=seq_lens, keep=keep, seq_lens_out=seq_lens_out,
+             kept=kept, dst_tables=dst_tables, weights_out=weights_out)
+    _check(lib.pa_evict(pool.handle, _ptr(weights), _ptr(weights_out), _ptr(block_tables), W, _ptr(dst_tables),
+                        dst_tables.shape[1] if dst_tables is not None else 0, _ptr(seq_lens), _ptr(keep), B,
+                        int(n_sink), int(n_recent), _ptr(seq_lens_out), _ptr(kept), _stream(stream)), "pa_evict")
 
 
 def pa_copy_blocks(pool, src, dst, stream=None):
@@ -441,6 +602,18 @@ class BlockAllocator:
         _check(lib.pa_alloc_prefix_stats(self._h, ctypes.byref(q), ctypes.byref(h), ctypes.byref(c)),
                "pa_alloc_prefix_stats")
         return q.value, h.value, c.value
+
+    def evict(self, seqs, keep):
+        """Shrinks sequences for a pa_evict call (see pa_alloc_evict): read the
+        old tables before and the new ones after."""
+        n = len(seqs)
+        if len(keep) != n:
+            raise ValueError("seqs and keep must have the same length")
+        code = lib.pa_alloc_evict(self._h, (ctypes.c_int * max(n, 1))(*[int(x) for x in seqs]),
+                                  (ctypes.c_int * max(n, 1))(*[int(x) for x in keep]), n)
+        if code == PA_ERR_OOM:
+            raise MemoryError("no free block")
+        _check(code, "pa_alloc_evict")
 
     def seq_free(self, seq):
         _check(lib.pa_alloc_seq_free(self._h, seq), "pa_alloc_seq_free")

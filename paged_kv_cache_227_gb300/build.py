@@ -15,7 +15,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libpagedattn.so")
 OBJDIR = os.path.join(HERE, "_build")
 
-CU_SOURCES = ["pool.cu", "append.cu", "decode.cu"]
+CU_SOURCES = ["pool.cu", "append.cu", "decode.cu", "rope.cu", "weights.cu", "evict.cu", "shared.cu"]
 CPP_SOURCES = ["alloc.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -30,7 +30,7 @@ def _nvcc():
 
 def _sources():
     srcs = [os.path.join(CSRC, f) for f in CU_SOURCES + CPP_SOURCES]
-    deps = srcs + [os.path.join(CSRC, "pa_internal.h"), os.path.join(INCLUDE, "pa.h")]
+    deps = srcs + [os.path.join(CSRC, "pa_internal.h"), os.path.join(CSRC, "device_utils.cuh"), os.path.join(INCLUDE, "pa.h")]
     return srcs, deps
 
 

@@ -12,6 +12,7 @@
 #include <array>
 #include <cstring>
 #include <list>
+#include <new>
 #include <unordered_map>
 #include <vector>
 
@@ -285,6 +286,66 @@ int pa_alloc_seq_free(pa_alloc_t a, int seq) {
   }
   a->seqs.erase(it);
   return PA_OK;
+}
+
+// Every destination is taken before any block is released, so no sequence of
+// the call gets a block that another of them still reads; nothing changes
+// before the last thing that can fail.
+int pa_alloc_evict(pa_alloc_t a, const int* seqs, const int* keep, int n) try {
+  if (!a || n < 0 || (n > 0 && (!seqs || !keep))) return PA_ERR_INVALID;
+  struct Change {
+    pa_alloc::Seq* s;
+    long long len;
+    std::vector<int32_t> table;
+  };
+  std::vector<Change> changes;
+  std::vector<int> ids;
+  long long need = 0;
+  for (int k = 0; k < n; ++k) {
+    auto it = a->seqs.find(seqs[k]);
+    if (it == a->seqs.end() || keep[k] < 0) return PA_ERR_INVALID;
+    ids.push_back(seqs[k]);
+    pa_alloc::Seq& s = it->second;
+    if (keep[k] >= s.len) continue;  // nothing to evict
+    const size_t nb = (static_cast<size_t>(keep[k]) + a->block_size - 1) / a->block_size;
+    changes.push_back(Change{&s, keep[k], std::vector<int32_t>(s.table.begin(), s.table.begin() + nb)});
+    for (int32_t b : changes.back().table) need += a->refcount[b] > 1;
+  }
+  std::sort(ids.begin(), ids.end());
+  if (std::adjacent_find(ids.begin(), ids.end()) != ids.end()) return PA_ERR_INVALID;
+  if (need > static_cast<long long>(a->free_list.size())) return PA_ERR_OOM;
+  // (the free list's nodes for the blocks released below)
+  std::list<int32_t> spare;
+  for (const Change& c : changes) spare.insert(spare.end(), c.s->table.size(), -1);
+  for (Change& c : changes)
+    for (int32_t& b : c.table) {
+      if (a->refcount[b] > 1) {
+        b = a->take();
+      } else if (a->indexed[b]) {  // rewritten in place: not what its hash names any more
+        a->index.erase(a->key_of[b]);
+        a->indexed[b] = 0;
+      }
+    }
+  for (Change& c : changes) {
+    for (size_t k = 0; k < c.s->table.size(); ++k) {
+      const int32_t b = c.s->table[k];
+      if (k < c.table.size() && c.table[k] == b) continue;
+      if (--a->refcount[b] == 0) {
+        a->free_list.splice(a->free_list.end(), spare, spare.begin());
+        a->free_list.back() = b;
+        a->free_pos[b] = std::prev(a->free_list.end());
+        a->on_free[b] = 1;
+      }
+    }
+    c.s->table.swap(c.table);
+    c.s->len = c.len;
+    c.s->tracked = false;
+    c.s->tokens.clear();
+    c.s->chain.clear();
+  }
+  return PA_OK;
+} catch (const std::bad_alloc&) {
+  return PA_ERR_OOM;
 }
 
 int pa_alloc_table(pa_alloc_t a, int seq, int32_t* out, int cap, int* n_blocks) {

@@ -51,6 +51,7 @@
 #include <mutex>
 #include <vector>
 
+#include "device_utils.cuh"
 #include "pa_internal.h"
 
 namespace pa {
@@ -100,6 +101,7 @@ struct Params {
                              // tokens are the rows that follow), or -1 (none); null: q and out are
                              // [B][Hq][128]
   int ext_hq;                // with ext_qbase: heads of a q / out row ([rows][ext_hq][128])
+  float* scores;            // [B][Hkv][max_blocks * 16][G] scaled scores in log2 units (score variant), or null
   const int32_t* seq_lens;  // [B]
   void* out;                // [B][Hq][128]
   float* ws;                // partial records
@@ -157,40 +159,6 @@ __device__ __forceinline__ long long packed_io_offset(const Params& P, int r0, i
 // ---------------------------------------------------------------------------
 // PTX helpers.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ long long global_ns() {
-  long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // L2 policy for the K/V stream: evict first, so that the tiles, read once,
 // do not push out what is read again (q rows, tables, the partial records
 // the merge kernel reads back).
@@ -229,30 +197,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// Two fp32 values as a 16-bit pair (a in the low half), rounded to nearest;
-// pack_lo packs what rounding left over, so hi + lo carries a to ~2^-17.
-template <bool kBf16>
-__device__ __forceinline__ uint32_t pack_hi(float a, float b) {
-  if (kBf16) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<uint32_t*>(&h);
-  }
-  __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-template <bool kBf16>
-__device__ __forceinline__ uint32_t pack_lo(float a, float b) {
-  if (kBf16) {
-    const float ra = a - __bfloat162float(__float2bfloat16_rn(a));
-    const float rb = b - __bfloat162float(__float2bfloat16_rn(b));
-    __nv_bfloat162 h = __floats2bfloat162_rn(ra, rb);
-    return *reinterpret_cast<uint32_t*>(&h);
-  }
-  const float ra = a - __half2float(__float2half_rn(a));
-  const float rb = b - __half2float(__float2half_rn(b));
-  __half2 h = __floats2half2_rn(ra, rb);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
 // D = A B + D for m16n8k16 (fp32 accumulate).
 template <bool kBf16>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -276,23 +220,6 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return static_cast<uint32_t>((c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// Bounded wait on an mbarrier phase.  Returns false if the CTA is aborting or
-// the wait ran out (then it records PA_ERR_TIMEOUT and raises the abort flag).
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                           long long limit_ns, long long* err, int site) {
-  if (mbar_try_wait(bar, parity)) return true;
-  long long t0 = global_ns();
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (global_ns() - t0 > limit_ns) {
-      *abort_flag = 1;
-      record_error(err, PA_ERR_TIMEOUT, site);
-      return false;
-    }
-  }
-}
-
 // 16-bit -> fp32 pairs for 8 packed elements (element 2k in .x, 2k+1 in .y).
 template <bool kBf16>
 __device__ __forceinline__ void unpack8(const uint4& v, float2 f[4]) {
@@ -305,31 +232,6 @@ __device__ __forceinline__ void unpack8(const uint4& v, float2 f[4]) {
       __half2 h = *reinterpret_cast<const __half2*>(&w[k]);
       f[k] = __half22float2(h);
     }
-  }
-}
-
-__device__ __forceinline__ void store_out(void* out, long long idx, float x, int out_dtype) {
-  if (out_dtype == PA_FP32)
-    static_cast<float*>(out)[idx] = x;
-  else if (out_dtype == PA_BF16)
-    static_cast<__nv_bfloat16*>(out)[idx] = __float2bfloat16_rn(x);
-  else
-    static_cast<__half*>(out)[idx] = __float2half_rn(x);
-}
-
-// Four consecutive outputs starting at an index that is a multiple of 4.
-__device__ __forceinline__ void store_out4(void* out, long long idx, float a, float b, float c, float d,
-                                           int out_dtype) {
-  if (out_dtype == PA_FP32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(out) + idx) = make_float4(a, b, c, d);
-  } else if (out_dtype == PA_BF16) {
-    __nv_bfloat162 h0 = __floats2bfloat162_rn(a, b), h1 = __floats2bfloat162_rn(c, d);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + idx) =
-        make_uint2(*reinterpret_cast<uint32_t*>(&h0), *reinterpret_cast<uint32_t*>(&h1));
-  } else {
-    __half2 h0 = __floats2half2_rn(a, b), h1 = __floats2half2_rn(c, d);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + idx) =
-        make_uint2(*reinterpret_cast<uint32_t*>(&h0), *reinterpret_cast<uint32_t*>(&h1));
   }
 }
 
@@ -593,7 +495,7 @@ constexpr size_t smem_bytes(int B, bool rows = false) {
 // ---------------------------------------------------------------------------
 // The decode kernel.
 // ---------------------------------------------------------------------------
-template <int G, bool kBf16, bool kFused, bool kExt>
+template <int G, bool kBf16, bool kFused, bool kExt, bool kScores = false>
 __global__ void __launch_bounds__(Shape<G>::kThreads, Shape<G>::kMinCtas) decode_kernel(const __grid_constant__ Params P) {
   constexpr int NW = Shape<G>::NW;
   constexpr int SW = Shape<G>::SW;
@@ -643,7 +545,7 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, Shape<G>::kMinCtas) decode
         for (int x = threadIdx.x; x < P.Hq * kHeadDim; x += blockDim.x)
           store_out(P.out, static_cast<long long>(i) * P.Hq * kHeadDim + x, 0.f, P.out_dtype);
       }
-      if (kExt && P.lse)
+      if ((kExt || kScores) && P.lse)
         for (int x = threadIdx.x; x < P.Hq; x += blockDim.x) P.lse[static_cast<long long>(i) * P.Hq + x] = -INFINITY;
     }
   }
@@ -894,6 +796,26 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, Shape<G>::kMinCtas) decode
       }
     };
 
+    // score variant: tile j's scores s (columns g0, +1 of tokens r4, r4 + 8),
+    // [token][head of the group]: 64 G contiguous bytes of a whole tile
+    auto store_scores = [&](int j, const float (&s)[4]) {
+      if constexpr (kScores) {
+        float* at = P.scores + ((static_cast<long long>(pc.i) * P.Hkv + pc.h) * P.max_blocks + j) * (kBlock * G);
+        const int valid = pc.L - j * kBlock;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int tok = r4 + 8 * r;
+          if (tok >= valid) continue;
+          if constexpr (G % 2 == 0) {
+            if (g0 < G) *reinterpret_cast<float2*>(at + tok * G + g0) = make_float2(s[2 * r], s[2 * r + 1]);
+          } else {
+            if (g0 < G) at[tok * G + g0] = s[2 * r];
+            if (g0 + 1 < G) at[tok * G + g0 + 1] = s[2 * r + 1];
+          }
+        }
+      }
+    };
+
     float acc[NCH][kSc][4];
     int cur_blk = -1;
     bool cur_touched = false;
@@ -938,6 +860,7 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, Shape<G>::kMinCtas) decode
             mx[hf][c] = fmaxf(st[hf][c], st[hf][2 + c]);
             grow = grow || mx[hf][c] > m_run[hf][c] + kRescaleThreshold;
           }
+        if constexpr (kScores) store_scores(j, st[0]);
         if (__any_sync(0xffffffffu, grow)) {  // warp-uniform
 #pragma unroll
           for (int hf = 0; hf < NCH; ++hf) {
@@ -1013,6 +936,12 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, Shape<G>::kMinCtas) decode
             pb[r4 + 8][g0 + 1] = p[0][3];
           }
           __syncwarp();
+        }
+      }
+      if constexpr (kScores) {
+        if (cur_blk < 0) {  // a block outside the pool: its tokens are skipped
+          const float none[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          store_scores(j, none);
         }
       }
       // ---- next tile: wait for it and issue its score product now
@@ -1154,7 +1083,7 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, Shape<G>::kMinCtas) decode
     }
     const long long row0 = (static_cast<long long>(pc.i) * P.Hq + pc.h * G) * kHeadDim;
     float* rec = P.ws + pc.rec * record_floats(G);
-    if (kExt && P.lse && pc.final_out && lane == 0) {
+    if ((kExt || kScores) && P.lse && pc.final_out && lane == 0) {
 #pragma unroll
       for (int g = 0; g < G; ++g)
         P.lse[static_cast<long long>(pc.i) * P.Hq + pc.h * G + g] = lg[g] > 0.f ? mg[g] + __log2f(lg[g]) : -INFINITY;
@@ -1680,7 +1609,7 @@ static void profile_release() {
   g_prof_next = 0;
 }
 
-template <int G, bool kBf16, bool kFused, bool kExt>
+template <int G, bool kBf16, bool kFused, bool kExt, bool kScores>
 static int occupancy_for(size_t bytes) {
   static std::mutex mu;
   static int cached_dev = -1;
@@ -1690,12 +1619,12 @@ static int occupancy_for(size_t bytes) {
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lock(mu);
   if (dev == cached_dev && bytes == cached_bytes) return cached_occ;
-  if (cudaFuncSetAttribute(decode_kernel<G, kBf16, kFused, kExt>,
+  if (cudaFuncSetAttribute(decode_kernel<G, kBf16, kFused, kExt, kScores>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem_bytes<G>(kMaxSplitSeqs, true))) != cudaSuccess)
     return 0;
   int occ = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, decode_kernel<G, kBf16, kFused, kExt>,
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, decode_kernel<G, kBf16, kFused, kExt, kScores>,
                                                     Shape<G>::kThreads, bytes) != cudaSuccess)
     return 0;
   if (occ > kMaxCtasPerSm) occ = kMaxCtasPerSm;
@@ -1705,12 +1634,12 @@ static int occupancy_for(size_t bytes) {
   return occ;
 }
 
-template <int G, bool kBf16, bool kFused, bool kExt>
+template <int G, bool kBf16, bool kFused, bool kExt, bool kScores>
 static int launch_typed(Params& P, int device, cudaStream_t stream) {
   constexpr int NW = Shape<G>::NW;
   int B_smem = P.sched == SCHED_SEGMENT ? 0 : P.B;
   size_t bytes = smem_bytes<G>(B_smem, P.table_offs != nullptr);
-  int occ = occupancy_for<G, kBf16, kFused, kExt>(bytes);
+  int occ = occupancy_for<G, kBf16, kFused, kExt, kScores>(bytes);
   if (occ <= 0) return PA_ERR_CUDA;
   long long slots = static_cast<long long>(sm_count(device)) * occ;
   long long grid;
@@ -1753,9 +1682,9 @@ static int launch_typed(Params& P, int device, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, decode_kernel<G, kBf16, kFused, kExt>, P) != cudaSuccess) return PA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, decode_kernel<G, kBf16, kFused, kExt, kScores>, P) != cudaSuccess) return PA_ERR_CUDA;
   } else if (with_decode) {
-    decode_kernel<G, kBf16, kFused, kExt><<<static_cast<int>(grid), Shape<G>::kThreads, bytes, stream>>>(P);
+    decode_kernel<G, kBf16, kFused, kExt, kScores><<<static_cast<int>(grid), Shape<G>::kThreads, bytes, stream>>>(P);
   }
   if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
   if (with_merge) {
@@ -1784,19 +1713,19 @@ static int launch_typed(Params& P, int device, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-template <bool kBf16, bool kFused, bool kExt>
+template <bool kBf16, bool kFused, bool kExt, bool kScores = false>
 static int launch_g(int G, Params& P, int device, cudaStream_t stream) {
   switch (G) {
-    case 1: return launch_typed<1, kBf16, kFused, kExt>(P, device, stream);
-    case 2: return launch_typed<2, kBf16, kFused, kExt>(P, device, stream);
-    case 3: return launch_typed<3, kBf16, kFused, kExt>(P, device, stream);
-    case 4: return launch_typed<4, kBf16, kFused, kExt>(P, device, stream);
-    case 5: return launch_typed<5, kBf16, kFused, kExt>(P, device, stream);
-    case 6: return launch_typed<6, kBf16, kFused, kExt>(P, device, stream);
-    case 7: return launch_typed<7, kBf16, kFused, kExt>(P, device, stream);
-    case 8: return launch_typed<8, kBf16, kFused, kExt>(P, device, stream);
+    case 1: return launch_typed<1, kBf16, kFused, kExt, kScores>(P, device, stream);
+    case 2: return launch_typed<2, kBf16, kFused, kExt, kScores>(P, device, stream);
+    case 3: return launch_typed<3, kBf16, kFused, kExt, kScores>(P, device, stream);
+    case 4: return launch_typed<4, kBf16, kFused, kExt, kScores>(P, device, stream);
+    case 5: return launch_typed<5, kBf16, kFused, kExt, kScores>(P, device, stream);
+    case 6: return launch_typed<6, kBf16, kFused, kExt, kScores>(P, device, stream);
+    case 7: return launch_typed<7, kBf16, kFused, kExt, kScores>(P, device, stream);
+    case 8: return launch_typed<8, kBf16, kFused, kExt, kScores>(P, device, stream);
     case kMaxPackedCols:  // packed tokens only (two column halves)
-      if constexpr (kExt && !kFused) return launch_typed<kMaxPackedCols, kBf16, kFused, kExt>(P, device, stream);
+      if constexpr (kExt && !kFused) return launch_typed<kMaxPackedCols, kBf16, kFused, kExt, kScores>(P, device, stream);
       return PA_ERR_UNSUPPORTED;
     default: return PA_ERR_UNSUPPORTED;
   }
@@ -1831,7 +1760,7 @@ static int decode_common(pa_pool_t p, const void* q, const void* k_new, const vo
                          int partition_blocks, void* ws, size_t ws_bytes, void* stream,
                          const int32_t* table_offs = nullptr, float* lse = nullptr,
                          const int32_t* ext_ntok = nullptr, int ext_g = 0, int launch_flags = 0,
-                         const int32_t* ext_qbase = nullptr, int ext_hq = 0) {
+                         const int32_t* ext_qbase = nullptr, int ext_hq = 0, float* scores = nullptr) {
   if (!p || !q || !tables || !seq_lens || !out || B <= 0 || Hq <= 0 || max_blocks <= 0)
     return PA_ERR_INVALID;
   if (out_dtype != PA_FP16 && out_dtype != PA_BF16 && out_dtype != PA_FP32) return PA_ERR_INVALID;
@@ -1845,6 +1774,8 @@ static int decode_common(pa_pool_t p, const void* q, const void* k_new, const vo
   if (fused && ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15))
     return PA_ERR_INVALID;
   if ((table_offs || lse) && (sched == SCHED_SEGMENT || fused)) return PA_ERR_INVALID;
+  // (the score variant returns the log2-sum-exps that its scores go with)
+  if (scores && (table_offs || !lse)) return PA_ERR_INVALID;
   // packed tokens in q / out rows: ext_g columns each in the G, columns past the
   // last whole token empty (no log2-sum-exp out)
   if (ext_qbase && (!table_offs || !ext_ntok || lse || ext_g <= 0 || ext_g > G || ext_hq <= 0 ||
@@ -1873,6 +1804,7 @@ static int decode_common(pa_pool_t p, const void* q, const void* k_new, const vo
   P.ext_g = ext_g > 0 ? ext_g : 1;
   P.ext_qbase = ext_qbase;
   P.ext_hq = ext_hq;
+  P.scores = scores;
   P.seq_lens = seq_lens;
   P.out = out;
   P.ws = static_cast<float*>(ws);
@@ -1898,7 +1830,10 @@ static int decode_common(pa_pool_t p, const void* q, const void* k_new, const vo
     // table offsets (and, optionally, log2-sum-exp outputs) select the
     // extended kernel; the plain and fused kernels carry neither
     const bool ext = table_offs != nullptr;
-    if (lse && !ext) return PA_ERR_INVALID;
+    if (lse && !ext && !scores) return PA_ERR_INVALID;
+    if (scores)
+      return bf16 ? launch_g<true, false, false, true>(G, P, p->device, st)
+                  : launch_g<false, false, false, true>(G, P, p->device, st);
     if (bf16) {
       if (ext) return launch_g<true, false, true>(G, P, p->device, st);
       return fused ? launch_g<true, true, false>(G, P, p->device, st) : launch_g<true, false, false>(G, P, p->device, st);
@@ -1977,6 +1912,67 @@ int pa_append_decode(pa_pool_t p, const void* q, const void* k_new, const void* 
                        n_q_heads, scale, out, out_dtype, sched, partition_blocks, workspace,
                        workspace_bytes, stream);
 }
+
+// Decode with attention-weight sums: workspace pieces, each 256-byte aligned.
+struct WeightsLayout {
+  size_t scores, lse, rec, total;
+};
+static bool weights_layout(const pa_pool* p, int B, int Hq, int max_blocks, WeightsLayout* L) {
+  WorkspaceLayout rw{};
+  if (!workspace_layout(p, B, Hq, max_blocks, 0, &rw)) return false;
+  if (max_blocks > 0x7fffffff / kBlock) return false;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  L->scores = take(sizeof(float) * static_cast<size_t>(B) * Hq * max_blocks * kBlock);
+  L->lse = take(sizeof(float) * static_cast<size_t>(B) * Hq);
+  L->rec = take(rw.total);
+  L->total = off;
+  return true;
+}
+
+size_t pa_decode_weights_workspace_bytes(pa_pool_t p, int num_seqs, int n_q_heads, int max_blocks_per_seq) {
+  WeightsLayout L{};
+  return weights_layout(p, num_seqs, n_q_heads, max_blocks_per_seq, &L) ? L.total : 0;
+}
+
+int pa_decode_weights(pa_pool_t p, const void* q, const int32_t* block_tables, int max_blocks_per_seq,
+                      const int32_t* seq_lens, int num_seqs, int n_q_heads, float scale, void* out, int out_dtype,
+                      float* weights, float decay, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!p || !weights || (reinterpret_cast<uintptr_t>(weights) & 15)) return PA_ERR_INVALID;
+  if (num_seqs > kMaxSplitSeqs) return PA_ERR_UNSUPPORTED;
+  WeightsLayout L{};
+  if (!weights_layout(p, num_seqs, n_q_heads, max_blocks_per_seq, &L)) return PA_ERR_INVALID;
+  if (!workspace || workspace_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return PA_ERR_INVALID;
+  char* ws = static_cast<char*>(workspace);
+  float* scores = reinterpret_cast<float*>(ws + L.scores);
+  float* lse = reinterpret_cast<float*>(ws + L.lse);
+  const int rc = decode_common(p, q, nullptr, nullptr, block_tables, max_blocks_per_seq, seq_lens, num_seqs,
+                               n_q_heads, scale, out, out_dtype, SCHED_LEAN, 0, ws + L.rec, L.total - L.rec, stream,
+                               nullptr, lse, nullptr, 0, 0, nullptr, 0, scores);
+  if (rc != PA_OK) return rc;
+  return launch_weight_sums(p, scores, lse, weights, decay, seq_lens, num_seqs, n_q_heads, max_blocks_per_seq,
+                            as_stream(stream));
+}
+
+}  // extern "C"
+
+namespace pa {
+
+int decode_own_tokens(pa_pool* p, const void* q, const int32_t* tables, int max_blocks, const int32_t* lens,
+                      const int32_t* table_offs, int B, int Hq, float scale, float* out, float* lse, void* ws,
+                      size_t ws_bytes, void* stream) {
+  return decode_common(p, q, nullptr, nullptr, tables, max_blocks, lens, B, Hq, scale, out, PA_FP32, SCHED_LEAN, 0, ws,
+                       ws_bytes, stream, table_offs, lse, nullptr, 0, kLaunchAfterPlan);
+}
+
+}  // namespace pa
+
+extern "C" {
 
 // Multi-token queries: workspace pieces, each 256-byte aligned.
 struct MultiLayout {

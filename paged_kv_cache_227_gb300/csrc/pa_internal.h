@@ -23,6 +23,7 @@ struct pa_pool {
   void* v;            // device
   size_t bytes;       // bytes of one of k / v
   long long* err;     // device: [0] = status code, [1] = detail
+  CUtensorMap tmap_half;  // the same view, loaded half a row at a time: boxes of 16 rows x 64 elements
 };
 
 namespace pa {
@@ -70,5 +71,17 @@ long long wait_limit_ns();
 int launch_append_tail(void* k_pool, void* v_pool, int n_kv_heads, long long num_blocks, long long* err,
                        int device, const void* k_new, const void* v_new, const int32_t* tables,
                        int max_blocks, const int32_t* seq_lens, int B, cudaStream_t stream);
+
+// The second half of pa_decode_weights: adds the attention weights of the
+// decode's scores to the sums (weights.cu).
+int launch_weight_sums(const pa_pool* p, const float* scores, const float* lse, float* weights, float decay,
+                       const int32_t* seq_lens, int B, int Hq, int max_blocks, cudaStream_t stream);
+
+// The split decode of each sequence's lens[i] tokens whose table starts at
+// element table_offs[i] (kernel results of the kernel before it in the
+// stream, whose programmatic dependent it is): fp32 out and log2-sum-exps.
+int decode_own_tokens(pa_pool* p, const void* q, const int32_t* tables, int max_blocks, const int32_t* lens,
+                      const int32_t* table_offs, int B, int Hq, float scale, float* out, float* lse, void* ws,
+                      size_t ws_bytes, void* stream);
 
 }  // namespace pa

@@ -29,15 +29,17 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
 // with byte strides {256 (row), 128 (half), bytes of one array}; the box
 // {64, 16, 2, 2} is one (block, head) tile of K followed by the same tile of
 // V, written to shared memory as [K|V][half][row][128 bytes] with the 128-byte
-// swizzle.
+// swizzle.  With `half` the box is {64, 16, 1, 1}: one half of one tile of
+// one array, [row][128 bytes].
 static bool encode_pool_map(CUtensorMap* map, void* base, long long rows, size_t array_bytes,
-                            int dtype) {
+                            int dtype, bool half) {
   auto fn = encode_tiled();
   if (!fn) return false;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(kHeadDim / 2), static_cast<cuuint64_t>(rows), 2, 2};
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(kRowBytes), static_cast<cuuint64_t>(kRowBytes / 2),
                            static_cast<cuuint64_t>(array_bytes)};
   cuuint32_t box[4] = {static_cast<cuuint32_t>(kHeadDim / 2), static_cast<cuuint32_t>(kBlock), 2, 2};
+  if (half) box[2] = box[3] = 1;
   cuuint32_t elem[4] = {1, 1, 1, 1};
   CUresult r = fn(map, dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                   4, base, dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -119,7 +121,8 @@ int pa_pool_create(int num_blocks, int block_size, int n_kv_heads, int d_head, i
   p->k = kv;
   p->v = static_cast<char*>(kv) + p->bytes;
   const long long rows = static_cast<long long>(num_blocks) * n_kv_heads * kBlock;
-  if (!encode_pool_map(&p->tmap_kv, kv, rows, p->bytes, dtype)) {
+  if (!encode_pool_map(&p->tmap_kv, kv, rows, p->bytes, dtype, false) ||
+      !encode_pool_map(&p->tmap_half, kv, rows, p->bytes, dtype, true)) {
     cudaFree(kv); cudaFree(p->err);
     delete p;
     return PA_ERR_CUDA;
