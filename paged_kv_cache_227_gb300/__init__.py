@@ -336,11 +336,50 @@ def pa_decode_cascade(pool, q, block_tables, seq_lens, scale, out, group_start, 
            "pa_decode_cascade")
 
 
-def _on_pool(pool, **tensors):
-    """Tensors of one call live on the pool's device."""
-    for name, t in tensors.items():
-        if t is not None and t.device != pool.device:
-            raise ValueError(f"{name} must be on the pool's device {pool.device}, got {t.device}")
+# The cache operators' checks: one pass over each tensor that also yields its
+# address, since at the smallest sizes a call is bound by the host (a decode
+# step of 64 tokens spends 4 us in the library's entry and on the GPU).
+def _at(pool, t, name, dtype):
+    """Address of a contiguous `dtype` tensor on the pool's device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != pool.device:
+        raise ValueError(f"{name} must be on the pool's device {pool.device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _int32(x):
+    """A count for a C int: past its range it means the same as its ends."""
+    return max(-1, min(int(x), 0x7fffffff))
+
+
+def _raw_stream(pool, stream):
+    """The given stream, or the pool's device's current one, as an address."""
+    return torch._C._cuda_getCurrentRawStream(pool.device.index) if stream is None else stream.cuda_stream
+
+
+def _decode_at(pool, q, block_tables, seq_lens, out):
+    """Checks of a decode's tensors (as _decode_args); their addresses and sizes."""
+    qa = _at(pool, q, "q", pool.dtype)
+    ta = _at(pool, block_tables, "block_tables", torch.int32)
+    la = _at(pool, seq_lens, "seq_lens", torch.int32)
+    code = _DTYPE_CODE.get(out.dtype) if isinstance(out, torch.Tensor) else 0
+    if code is None:
+        raise ValueError("out must be [B][Hq][128] of fp16, bf16 or fp32")
+    oa = _at(pool, out, "out", getattr(out, "dtype", None))
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != HEAD_DIM or block_tables.dim() != 2 or block_tables.shape[0] != shape[0] \
+            or seq_lens.shape != shape[:1]:
+        raise ValueError("shapes: q [B][Hq][128], block_tables [B][W], seq_lens [B]")
+    if out.shape != shape:
+        raise ValueError("out must be [B][Hq][128] of fp16, bf16 or fp32")
+    return qa, ta, la, oa, code, shape[0], shape[1], block_tables.shape[1]
 
 
 def _workspace(nbytes, what, device, stream):
@@ -354,19 +393,23 @@ def _workspace(nbytes, what, device, stream):
     return ws
 
 
-def _heads(t, name, n_tok, n_heads, dtype):
-    """Checks [n_tok][n_heads][128] rows with contiguous heads; returns the token stride in elements."""
+def _heads(pool, t, name, n_tok, n_heads):
+    """Checks [n_tok][n_heads][128] rows of the pool's type with contiguous
+    heads; their address and token stride in elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dtype != pool.dtype:
+        raise TypeError(f"{name} must be {pool.dtype}, got {t.dtype}")
+    if t.device != pool.device:
+        raise ValueError(f"{name} must be on the pool's device {pool.device}, got {t.device}")
     if t.shape != (n_tok, n_heads, HEAD_DIM):
         raise ValueError(f"{name} must be [{n_tok}][{n_heads}][{HEAD_DIM}], got {tuple(t.shape)}")
-    if n_tok and (t.stride(2) != 1 or (n_heads > 1 and t.stride(1) != HEAD_DIM)):
+    s = t.stride()
+    if n_tok and (s[2] != 1 or (n_heads > 1 and s[1] != HEAD_DIM)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if n_tok > 1 else n_heads * HEAD_DIM
+    return t.data_ptr(), (s[0] if n_tok > 1 else n_heads * HEAD_DIM)
 
 
 def pa_rope_append(pool, q, k_new, v_new, positions, inv_freq, axis_of_pair, slot_mapping, q_out, interleaved=False,
@@ -375,33 +418,28 @@ def pa_rope_append(pool, q, k_new, v_new, positions, inv_freq, axis_of_pair, slo
     cache write of k and v (see include/pa.h).  q and q_out [n][Hq][128], k_new
     and v_new [n][Hkv][128] with any token stride (slices of a fused projection
     work), positions int32 [n_axes][n], inv_freq fp32 [rot_dim/2],
-    axis_of_pair: rot_dim/2 ints on the host, slot_mapping int64 [n].  q_out may
-    be q."""
-    _need(slot_mapping, "slot_mapping", torch.int64)
-    _need(positions, "positions", torch.int32)
-    _need(inv_freq, "inv_freq", torch.float32)
+    axis_of_pair: rot_dim/2 ints on the host (bytes are taken as they are),
+    slot_mapping int64 [n].  q_out may be q."""
+    sa = _at(pool, slot_mapping, "slot_mapping", torch.int64)
+    pos = _at(pool, positions, "positions", torch.int32)
+    fa = _at(pool, inv_freq, "inv_freq", torch.float32)
     n = slot_mapping.numel()
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     if q.dim() != 3:
         raise ValueError("q must be [n_tok][Hq][128]")
-    Hq = q.shape[1]
-    qs = _heads(q, "q", n, Hq, pool.dtype)
-    ks = _heads(k_new, "k_new", n, pool.n_kv_heads, pool.dtype)
-    vs = _heads(v_new, "v_new", n, pool.n_kv_heads, pool.dtype)
-    os_ = _heads(q_out, "q_out", n, Hq, pool.dtype)
-    axes = [int(a) for a in axis_of_pair]
+    Hq, Hkv = q.shape[1], pool.n_kv_heads
+    qa, qs = _heads(pool, q, "q", n, Hq)
+    ka, ks = _heads(pool, k_new, "k_new", n, Hkv)
+    va, vs = _heads(pool, v_new, "v_new", n, Hkv)
+    oa, os_ = _heads(pool, q_out, "q_out", n, Hq)
+    axes = bytes(axis_of_pair)  # (ValueError outside 0 .. 255)
     if positions.dim() != 2 or positions.shape[1] != n:
         raise ValueError("positions must be [n_axes][n_tok]")
     if inv_freq.shape != (len(axes),):
         raise ValueError("inv_freq and axis_of_pair must have rot_dim / 2 entries each")
-    if any(a < 0 or a > 255 for a in axes):
-        raise ValueError("axis_of_pair holds axes of positions")
-    _on_pool(pool, q=q, k_new=k_new, v_new=v_new, positions=positions, inv_freq=inv_freq, slot_mapping=slot_mapping,
-             q_out=q_out)
-    _check(lib.pa_rope_append(pool.handle, _ptr(q), qs, Hq, _ptr(k_new), ks, _ptr(v_new), vs, _ptr(positions),
-                              positions.shape[0], bytes(axes), _ptr(inv_freq), 2 * len(axes), int(bool(interleaved)),
-                              _ptr(slot_mapping), n, _ptr(q_out), os_, _stream(stream)), "pa_rope_append")
+    _check(lib.pa_rope_append(pool.handle, qa, qs, Hq, ka, ks, va, vs, pos, positions.shape[0], axes, fa, 2 * len(axes),
+                              1 if interleaved else 0, sa, n, oa, os_, _raw_stream(pool, stream)), "pa_rope_append")
 
 
 def shared_workspace_for(pool, q, block_tables, prefix_blocks, stream=None):
@@ -416,20 +454,18 @@ def pa_decode_shared(pool, q, block_tables, seq_lens, scale, out, group_start, m
     """pa_decode with each group's shared prefix attended once for all of its
     members, groups of any size (see include/pa.h); the group arrays are int32
     device tensors (cascade_groups with max_members=B finds them)."""
-    B, Hq, W = _decode_args(pool, q, block_tables, seq_lens, out)
-    for t, name in ((group_start, "group_start"), (members, "members"), (prefix_blocks, "prefix_blocks")):
-        _need(t, name, torch.int32)
+    qa, ta, la, oa, code, B, Hq, W = _decode_at(pool, q, block_tables, seq_lens, out)
+    ga = _at(pool, group_start, "group_start", torch.int32)
+    ma = _at(pool, members, "members", torch.int32)
+    pa_ = _at(pool, prefix_blocks, "prefix_blocks", torch.int32)
     ng, nm = prefix_blocks.numel(), members.numel()
     if prefix_blocks.dim() != 1 or members.dim() != 1 or group_start.shape != (ng + 1,):
         raise ValueError("shapes: group_start [n_groups+1], members [n_members], prefix_blocks [n_groups]")
     if workspace is None:
         workspace = shared_workspace_for(pool, q, block_tables, prefix_blocks, stream)
-    _on_pool(pool, q=q, block_tables=block_tables, seq_lens=seq_lens, out=out, group_start=group_start,
-             members=members, prefix_blocks=prefix_blocks, workspace=workspace)
-    _check(lib.pa_decode_shared(pool.handle, _ptr(q), _ptr(block_tables), W, _ptr(seq_lens), B, Hq, float(scale),
-                                _ptr(group_start), _ptr(members), nm, _ptr(prefix_blocks), ng, _ptr(out),
-                                _DTYPE_CODE[out.dtype], _ptr(workspace),
-                                workspace.numel() * workspace.element_size(), _stream(stream)), "pa_decode_shared")
+    _check(lib.pa_decode_shared(pool.handle, qa, ta, W, la, B, Hq, float(scale), ga, ma, nm, pa_, ng, oa, code,
+                                _at(pool, workspace, "workspace", torch.uint8), workspace.numel(),
+                                _raw_stream(pool, stream)), "pa_decode_shared")
 
 
 def weights_workspace_for(pool, q, block_tables, stream=None):
@@ -438,24 +474,24 @@ def weights_workspace_for(pool, q, block_tables, stream=None):
     return _workspace(n, "pa_decode_weights_workspace_bytes", pool.device, stream)
 
 
-def _weights_arg(pool, t, name, B, W, dtype=torch.float32):
-    _need(t, name, dtype)
+def _per_token_at(pool, t, name, B, W, dtype):
+    a = _at(pool, t, name, dtype)
     if t.shape != (B, pool.n_kv_heads, W * BLOCK_SIZE):
         raise ValueError(f"{name} must be [B][n_kv_heads][16 * W]")
+    return a
 
 
 def pa_decode_weights(pool, q, block_tables, seq_lens, scale, out, weights, decay=1.0, workspace=None, stream=None):
     """pa_decode_split that also adds each cached token's attention weight to
     weights [B][Hkv][16*W] (fp32): weights = decay * weights + the weights of
     this step, summed over the query heads of a kv head (see include/pa.h)."""
-    B, Hq, W = _decode_args(pool, q, block_tables, seq_lens, out)
-    _weights_arg(pool, weights, "weights", B, W)
+    qa, ta, la, oa, code, B, Hq, W = _decode_at(pool, q, block_tables, seq_lens, out)
+    wa = _per_token_at(pool, weights, "weights", B, W, torch.float32)
     if workspace is None:
         workspace = weights_workspace_for(pool, q, block_tables, stream)
-    _on_pool(pool, q=q, block_tables=block_tables, seq_lens=seq_lens, out=out, weights=weights, workspace=workspace)
-    _check(lib.pa_decode_weights(pool.handle, _ptr(q), _ptr(block_tables), W, _ptr(seq_lens), B, Hq, float(scale),
-                                 _ptr(out), _DTYPE_CODE[out.dtype], _ptr(weights), float(decay), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), _stream(stream)), "pa_decode_weights")
+    _check(lib.pa_decode_weights(pool.handle, qa, ta, W, la, B, Hq, float(scale), oa, code, wa, float(decay),
+                                 _at(pool, workspace, "workspace", torch.uint8), workspace.numel(),
+                                 _raw_stream(pool, stream)), "pa_decode_weights")
 
 
 def pa_evict(pool, weights, block_tables, seq_lens, keep, seq_lens_out, kept, n_sink=0, n_recent=0, dst_tables=None,
@@ -465,27 +501,28 @@ def pa_evict(pool, weights, block_tables, seq_lens, keep, seq_lens_out, kept, n_
     up in order (see include/pa.h).  In place unless dst_tables [B][Wd] is given;
     weights_out defaults to weights.  seq_lens_out int32 [B] and kept int32
     [B][Hkv][16*W] are written."""
-    _need(block_tables, "block_tables", torch.int32); _need(seq_lens, "seq_lens", torch.int32)
-    _need(keep, "keep", torch.int32); _need(seq_lens_out, "seq_lens_out", torch.int32)
+    ta = _at(pool, block_tables, "block_tables", torch.int32)
+    la = _at(pool, seq_lens, "seq_lens", torch.int32)
+    ka = _at(pool, keep, "keep", torch.int32)
+    na = _at(pool, seq_lens_out, "seq_lens_out", torch.int32)
     if block_tables.dim() != 2:
         raise ValueError("block_tables must be [B][W]")
     B, W = block_tables.shape
     if seq_lens.shape != (B,) or keep.shape != (B,) or seq_lens_out.shape != (B,):
         raise ValueError("seq_lens, keep and seq_lens_out must be [B]")
-    weights_out = weights if weights_out is None else weights_out
-    _weights_arg(pool, weights, "weights", B, W); _weights_arg(pool, weights_out, "weights_out", B, W)
-    _weights_arg(pool, kept, "kept", B, W, torch.int32)
+    wa = _per_token_at(pool, weights, "weights", B, W, torch.float32)
+    oa = wa if weights_out is None else _per_token_at(pool, weights_out, "weights_out", B, W, torch.float32)
+    xa = _per_token_at(pool, kept, "kept", B, W, torch.int32)
+    da, Wd = None, 0
     if dst_tables is not None:
-        _need(dst_tables, "dst_tables", torch.int32)
+        da = _at(pool, dst_tables, "dst_tables", torch.int32)
         if dst_tables.dim() != 2 or dst_tables.shape[0] != B:
             raise ValueError("dst_tables must be [B][Wd]")
-        if dst_tables.shape[1] == 0:  # (an empty tensor has a null pointer, which would mean in place)
+        Wd = dst_tables.shape[1]
+        if Wd == 0:  # (an empty tensor has a null address, which would mean in place)
             raise PagedAttentionError(PA_ERR_INVALID, "pa_evict")
-    _on_pool(pool, weights=weights, block_tables=block_tables, seq_lens=seq_lens, keep=keep, seq_lens_out=seq_lens_out,
-             kept=kept, dst_tables=dst_tables, weights_out=weights_out)
-    _check(lib.pa_evict(pool.handle, _ptr(weights), _ptr(weights_out), _ptr(block_tables), W, _ptr(dst_tables),
-                        dst_tables.shape[1] if dst_tables is not None else 0, _ptr(seq_lens), _ptr(keep), B,
-                        int(n_sink), int(n_recent), _ptr(seq_lens_out), _ptr(kept), _stream(stream)), "pa_evict")
+    _check(lib.pa_evict(pool.handle, wa, oa, ta, W, da, Wd, la, ka, B, _int32(n_sink), _int32(n_recent), na, xa,
+                        _raw_stream(pool, stream)), "pa_evict")
 
 
 def pa_copy_blocks(pool, src, dst, stream=None):
@@ -610,7 +647,7 @@ class BlockAllocator:
         if len(keep) != n:
             raise ValueError("seqs and keep must have the same length")
         code = lib.pa_alloc_evict(self._h, (ctypes.c_int * max(n, 1))(*[int(x) for x in seqs]),
-                                  (ctypes.c_int * max(n, 1))(*[int(x) for x in keep]), n)
+                                  (ctypes.c_int * max(n, 1))(*[_int32(x) for x in keep]), n)
         if code == PA_ERR_OOM:
             raise MemoryError("no free block")
         _check(code, "pa_alloc_evict")

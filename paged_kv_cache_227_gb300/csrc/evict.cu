@@ -10,17 +10,18 @@
 // tile belongs to one head.
 //
 // Two kernels.  The selection finds the r-th largest sum exactly, by radix
-// (the sums as order-preserving 32-bit keys, 11 + 11 + 10 bits), and compacts
-// in position order; counts in shared memory only, so the result does not
-// depend on timing.  The move copies rows; in place it is safe because batch
-// c (rows j of [a, b)) is written after batches up to c are read, and later
-// batches read positions t_j >= j >= b only.
+// (the sums as order-preserving 32-bit keys, four passes of 8 bits), and
+// compacts in position order; counts in shared memory only, so the result
+// does not depend on timing.  The move copies rows.  Into fresh blocks every
+// row is independent.  In place it is safe because batch c (rows j of [a, b))
+// is written after batches up to c are read, and later batches read positions
+// t_j >= j >= b only.
 #include "pa_internal.h"
 
 namespace pa {
 
-constexpr int kSelThreads = 1024;
-constexpr int kBins = 2048;
+constexpr int kBins = 256;
+constexpr int kCopies = 8;  // of each histogram bin, by lane: equal keys of a warp meet 4 at a time
 constexpr int kMoveThreads = 256;
 
 struct EvictArgs {
@@ -44,170 +45,401 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// Inclusive scan over the block of a 64-bit pair of counters.
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* s_warp,
-                                                         unsigned long long* total) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += y;
-  }
-  if (lane == 31) s_warp[wid] = v;
-  __syncthreads();
-  if (wid == 0) {
-    unsigned long long x = s_warp[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+// What a row keeps: n of its L tokens, those before lo and from hi on always,
+// and `r` of the others.
+struct EvictRow {
+  int L, n, lo, hi, r;
+  const float* w;
+  float* w_out;
+  int32_t* kept;
+  __device__ EvictRow(const EvictArgs& A, int i, int h, bool first) {
+    const int span = A.max_blocks * kBlock;
+    L = A.seq_lens[i];
+    n = A.keep[i];
+    if (L < 0 || L > span || n < 0) {
+      if (first && h == 0) record_error(A.err, PA_ERR_DEVICE_CHECK, L < 0 || L > span ? L : n);
+      L = L < 0 ? 0 : (L > span ? span : L);
+      n = n < 0 ? 0 : n;
     }
-    s_warp[lane] = x;
+    if (n > L) n = L;
+    if (n > A.dst_blocks * kBlock) {  // more rows than the destination holds
+      if (first && h == 0) record_error(A.err, PA_ERR_DEVICE_CHECK, n);
+      n = A.dst_blocks * kBlock;
+    }
+    if (first && h == 0) A.lens_out[i] = n;
+    const int a = n < A.n_sink ? n : A.n_sink;
+    const int b = n - a < A.n_recent ? n - a : A.n_recent;
+    lo = a;
+    hi = L - b;
+    r = n - a - b;
+    const long long row = (static_cast<long long>(i) * A.Hkv + h) * span;
+    w = A.w + row;
+    w_out = A.w_out + row;
+    kept = A.kept + row;
   }
-  __syncthreads();
-  if (wid) v += s_warp[wid - 1];
-  *total = s_warp[31];
-  __syncthreads();
+  __device__ bool contest() const { return r > 0 && r < hi - lo; }
+};
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// `x` of CTA `rank` of this cluster.
+__device__ __forceinline__ int remote_int(const int* x, int rank) {
+  uint32_t at;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(at)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(x))), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
   return v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs A) {
-  __shared__ int s_hist[kBins];
-  __shared__ unsigned long long s_warp[32];
-  __shared__ int s_bin, s_above;
-  const int i = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
-  const int span = A.max_blocks * kBlock;
-  int L = A.seq_lens[i], n = A.keep[i];
-  if (L < 0 || L > span || n < 0) {
-    if (tid == 0 && h == 0) record_error(A.err, PA_ERR_DEVICE_CHECK, L < 0 || L > span ? L : n);
-    L = L < 0 ? 0 : (L > span ? span : L);
-    n = n < 0 ? 0 : n;
+// The bin of the r-th key from the top, given thread e's count `c` of bin 255 -
+// e (e < 256; every thread of the block calls).  found[0] = bin, [1] = keys in
+// higher bins, [2] = keys in the bin.  Ends with a block barrier.
+__device__ __forceinline__ void find_bin(int r, int c, int* s_sums, int* found) {
+  const int e = threadIdx.x, lane = e & 31, wid = e >> 5;
+  int incl = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
   }
-  if (n > L) n = L;
-  if (n > A.dst_blocks * kBlock) {  // more rows than the destination holds
-    if (tid == 0 && h == 0) record_error(A.err, PA_ERR_DEVICE_CHECK, n);
-    n = A.dst_blocks * kBlock;
-  }
-  if (tid == 0 && h == 0) A.lens_out[i] = n;
-  const int a = n < A.n_sink ? n : A.n_sink;
-  const int b = n - a < A.n_recent ? n - a : A.n_recent;
-  const int lo = a, hi = L - b;  // the tokens that compete
-  int r = n - a - b;             // how many of them stay
-  const long long row = (static_cast<long long>(i) * A.Hkv + h) * span;
-  const float* w = A.w + row;
-  float* w_out = A.w_out + row;
-  int32_t* kept = A.kept + row;
-
-  // the r-th largest key `cut`, and how many keys equal to it stay
-  uint32_t cut = 0;
-  int ties = 0;
-  const bool all = r == hi - lo;
-  if (!all && r > 0) {
-    uint32_t prefix = 0;
-    int shift = 32;
-    for (int pass = 0; pass < 3; ++pass) {
-      const int bits = pass < 2 ? 11 : 10;
-      const int above_shift = shift;
-      shift -= bits;
-      for (int x = tid; x < kBins; x += kSelThreads) s_hist[x] = 0;
-      __syncthreads();
-      for (int t = lo + tid; t < hi; t += kSelThreads) {
-        const uint32_t key = weight_key(w[t]);
-        if (pass == 0 || (key >> above_shift) == prefix) atomicAdd(&s_hist[(key >> shift) & ((1u << bits) - 1)], 1);
-      }
-      __syncthreads();
-      // bins from the top: thread tid takes bins kBins - 1 - 2 tid and the one below
-      const int c0 = s_hist[kBins - 1 - 2 * tid], c1 = s_hist[kBins - 2 - 2 * tid];
-      unsigned long long total;
-      const int incl = static_cast<int>(block_scan(c0 + c1, s_warp, &total));
-      const int before = incl - c0 - c1;
-      if (before < r && r <= before + c0) {
-        s_bin = kBins - 1 - 2 * tid;
-        s_above = before;
-      } else if (before + c0 < r && r <= incl) {
-        s_bin = kBins - 2 - 2 * tid;
-        s_above = before + c0;
-      }
-      __syncthreads();
-      prefix = (pass == 0 ? 0u : prefix << bits) | static_cast<uint32_t>(s_bin);
-      r -= s_above;
-      __syncthreads();
+  if (lane == 31 && e < kBins) s_sums[wid] = incl;
+  __syncthreads();
+  if (e < kBins) {
+#pragma unroll
+    for (int w = 0; w < kBins / 32 - 1; ++w) incl += w < wid ? s_sums[w] : 0;
+    if (incl - c < r && r <= incl) {
+      found[0] = kBins - 1 - e;
+      found[1] = incl - c;
+      found[2] = c;
     }
-    cut = prefix;
-    ties = r;
-  }
-
-  // compaction: rank = stayers before + equal keys before (the first `ties` stay)
-  unsigned long long carry = 0;  // high half: equal keys, low half: other stayers
-  for (int base = 0; base < L; base += kSelThreads) {
-    const int t = base + tid;
-    float x = 0.f;
-    bool stays = false, equal = false;
-    if (t < L) {
-      x = w[t];
-      const uint32_t key = weight_key(x);
-      const bool open = t >= lo && t < hi && !all;
-      stays = !open || (n - a - b > 0 && key > cut);
-      equal = open && ties > 0 && key == cut;
-    }
-    unsigned long long total;
-    const unsigned long long mine = (static_cast<unsigned long long>(equal) << 32) | (stays ? 1u : 0u);
-    const unsigned long long before = carry + block_scan(mine, s_warp, &total) - mine;
-    const int eq = static_cast<int>(before >> 32);
-    if (stays || (equal && eq < ties)) {
-      const int rank = static_cast<int>(before & 0xffffffffu) + (eq < ties ? eq : ties);
-      kept[rank] = t;
-      w_out[rank] = x;
-    }
-    carry += total;
   }
   __syncthreads();
-  for (int t = n + tid; t < L; t += kSelThreads) w_out[t] = 0.f;
 }
 
-// One CTA per (sequence, kv head, K or V, slice of the row): 16 / slices
-// lanes of 16 bytes a row.
-template <int kSlices>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs A, uint4* k_pool, uint4* v_pool) {
-  constexpr int LPR = 16 / kSlices;          // lanes a row
-  constexpr int RPP = kMoveThreads / LPR;    // rows a pass
-  constexpr int U = 4;                       // passes a batch
+// A bin's count over its copies, which are cleared for the next pass.
+__device__ __forceinline__ int take_bin(int* s_hist, int e) {
+  int4* p = reinterpret_cast<int4*>(s_hist + e * kCopies);
+  const int4 u = p[0], v = p[1];
+  p[0] = p[1] = make_int4(0, 0, 0, 0);
+  return (u.x + u.y) + (u.z + u.w) + ((v.x + v.y) + (v.z + v.w));
+}
+
+// Rows of up to CL * THREADS * K tokens: a cluster of CL CTAs a row, the keys
+// in registers (K a thread at most; the warps share the row's tokens evenly
+// and a warp's are contiguous, so ranks grow with lane, warp and CTA).  A thread's tokens are bits of two masks: those that
+// stay for sure, and those whose key agrees with the cut so far; a pass costs
+// a token only while its bit is in the second.
+template <int THREADS, int K, int CL>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(const EvictArgs A) {
+  constexpr int NW = THREADS / 32;
+  __shared__ __align__(16) int s_hist[kBins * kCopies];
+  __shared__ int s_total[2][kBins];
+  __shared__ int s_found[3], s_sums[kBins / 32];
+  __shared__ int s_warp[32];
+  __shared__ int s_equal, s_stay;  // this CTA's
+  const int rank = CL > 1 ? static_cast<int>(blockIdx.x % CL) : 0;
+  const int h = blockIdx.x / CL, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the move waits for this grid)
+  const EvictRow R(A, blockIdx.y, h, rank == 0 && tid == 0);
+  const int used = (R.L + 32 * NW * CL - 1) / (32 * NW * CL);  // tokens a thread, at most K
+  const int t0 = (rank * NW + wid) * 32 * used + lane;         // token of bit k: t0 + 32 k
+  auto sync = [] {
+    if (CL > 1) cluster_barrier(); else __syncthreads();
+  };
+  // this thread's share of the CTAs' `x` before this one, by warp 0's lanes
+  auto before = [&](const int* x) {
+    int sum = 0;
+#pragma unroll
+    for (int c = 0; c < CL - 1; ++c) sum += c < rank ? remote_int(x, c) : 0;
+    return sum;
+  };
+  auto warp_scan = [&](int* own) {  // exclusive over the CTA's warps; *own: the CTA's total
+    int v = lane < NW ? s_warp[lane] : 0;
+    const int mine = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (tid == 31) *own = v;
+    return __shfl_sync(0xffffffffu, v - mine, wid);
+  };
+
+  uint32_t key[K];
+  uint32_t stay = 0, open = 0;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    key[k] = 0;
+    if (k >= used) continue;
+    const int t = t0 + 32 * k;
+    const float x = t < R.L ? R.w[t] : 0.f;
+    key[k] = weight_key(x);
+    const bool inside = t >= R.lo && t < R.hi;
+    stay |= static_cast<uint32_t>(t < R.L && !inside) << k;
+    open |= static_cast<uint32_t>(inside) << k;
+  }
+  if (R.r == R.hi - R.lo) stay |= open;
+  if (R.contest()) {
+    int r = R.r;
+    for (int e = tid; e < kBins * kCopies; e += THREADS) s_hist[e] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      if (__any_sync(0xffffffffu, open)) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (k < used && ((open >> k) & 1))
+            atomicAdd(&s_hist[((key[k] >> shift) & 255) * kCopies + (lane & (kCopies - 1))], 1);
+      }
+      __syncthreads();
+      int c = 0;
+      if (CL == 1) {
+        if (tid < kBins) c = take_bin(s_hist, kBins - 1 - tid);
+      } else {  // (two buffers: the next pass writes the other one)
+        int* total = s_total[(shift >> 3) & 1];
+        if (tid < kBins) total[tid] = take_bin(s_hist, kBins - 1 - tid);
+        cluster_barrier();
+#pragma unroll
+        for (int x = 0; x < CL; ++x) c += tid < kBins ? remote_int(&total[tid], x) : 0;
+      }
+      find_bin(r, c, s_sums, s_found);
+      const uint32_t bin = s_found[0];
+      r -= s_found[1];
+      if (__any_sync(0xffffffffu, open)) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (k >= used) continue;
+          const uint32_t digit = (key[k] >> shift) & 255;
+          const uint32_t bit = open & (1u << k);
+          if (digit > bin) stay |= bit;
+          if (digit != bin) open &= ~bit;
+        }
+      }
+    }
+    if (r == s_found[2]) {
+      stay |= open;  // every key equal to the cut stays
+    } else {         // the first r of them do
+      const int mine = __reduce_add_sync(0xffffffffu, __popc(open));
+      if (lane == 0) s_warp[wid] = mine;
+      __syncthreads();
+      int first = warp_scan(&s_equal);
+      sync();
+      first += before(&s_equal);
+      uint32_t some = 0;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (k >= used) continue;
+        const uint32_t m = __ballot_sync(0xffffffffu, (open >> k) & 1);
+        if (((open >> k) & 1) && first + __popc(m & ((1u << lane) - 1)) < r) some |= 1u << k;
+        first += __popc(m);
+      }
+      stay |= some;
+      __syncthreads();  // s_warp is read
+    }
+  }
+
+  // the stayers' sums again (a key does not tell -0 from 0 or one NaN from
+  // another), read before any is written: w_out may be w
+  float x[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) x[k] = (stay >> k) & 1 ? R.w[t0 + 32 * k] : 0.f;
+  const int mine = __reduce_add_sync(0xffffffffu, __popc(stay));
+  if (lane == 0) s_warp[wid] = mine;
+  __syncthreads();
+  int at = warp_scan(&s_stay);
+  sync();
+  at += before(&s_stay);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (k >= used) continue;
+    const bool mine = (stay >> k) & 1;
+    const uint32_t m = __ballot_sync(0xffffffffu, mine);
+    if (mine) {
+      const int j = at + __popc(m & ((1u << lane) - 1));
+      R.kept[j] = t0 + 32 * k;
+      R.w_out[j] = x[k];
+    }
+    at += __popc(m);
+  }
+  for (int t = R.n + rank * THREADS + tid; t < R.L; t += THREADS * CL) R.w_out[t] = 0.f;
+  if (CL > 1) cluster_barrier();  // s_stay may still be read by the other CTAs
+}
+
+// Longer rows: one CTA a row, which reads the row again for every pass (from
+// L2: 128K tokens are 512 KB).
+__global__ void __launch_bounds__(1024) evict_select_long_kernel(const EvictArgs A) {
+  constexpr int K = 8, TILE = 1024 * K;
+  __shared__ __align__(16) int s_hist[kBins * kCopies];
+  __shared__ int s_found[3], s_sums[kBins / 32];
+  __shared__ int2 s_warp[32];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const EvictRow R(A, blockIdx.y, blockIdx.x, tid == 0);
+  float x[K];
+  auto load = [&](int tile) {  // token k of this lane: tile + 32 (K wid + k) + lane
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int t = tile + 32 * (K * wid + k) + lane;
+      x[k] = t < R.L ? R.w[t] : 0.f;
+    }
+  };
+  uint32_t cut = 0;
+  int ties = 0;
+  const bool contest = R.contest(), all = R.r == R.hi - R.lo;
+  if (contest) {
+    int r = R.r;
+    for (int e = tid; e < kBins * kCopies; e += 1024) s_hist[e] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      for (int tile = 0; tile < R.L; tile += TILE) {
+        load(tile);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const int t = tile + 32 * (K * wid + k) + lane;
+          const uint32_t key = weight_key(x[k]);
+          if (t >= R.lo && t < R.hi && (shift == 24 || (key >> (shift + 8)) == cut))
+            atomicAdd(&s_hist[((key >> shift) & 255) * kCopies + (lane & (kCopies - 1))], 1);
+        }
+      }
+      __syncthreads();
+      find_bin(r, tid < kBins ? take_bin(s_hist, kBins - 1 - tid) : 0, s_sums, s_found);
+      cut = cut << 8 | static_cast<uint32_t>(s_found[0]);
+      r -= s_found[1];
+    }
+    ties = r;
+  }
+  // rank = stayers before + equal keys before (the first `ties` of them stay);
+  // a tile's ranks are at or before its tokens, which are read by then
+  const uint32_t below = (1u << lane) - 1;
+  int2 carry = make_int2(0, 0);
+  for (int tile = 0; tile < R.L; tile += TILE) {
+    load(tile);
+    uint32_t stay = 0, equal = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int t = tile + 32 * (K * wid + k) + lane;
+      const uint32_t key = weight_key(x[k]);
+      const bool inside = t >= R.lo && t < R.hi;
+      stay |= static_cast<uint32_t>(t < R.L && (!inside || all || (contest && key > cut))) << k;
+      equal |= static_cast<uint32_t>(inside && contest && key == cut) << k;
+    }
+    const int2 mine = make_int2(__reduce_add_sync(0xffffffffu, __popc(stay)),
+                                __reduce_add_sync(0xffffffffu, __popc(equal)));
+    if (lane == 0) s_warp[wid] = mine;
+    __syncthreads();  // (and every token of the tile is read)
+    int2 v = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v.x, o), z = __shfl_up_sync(0xffffffffu, v.y, o);
+      if (lane >= o) {
+        v.x += y;
+        v.y += z;
+      }
+    }
+    int sb = carry.x + __shfl_sync(0xffffffffu, v.x, wid) - mine.x;
+    int eb = carry.y + __shfl_sync(0xffffffffu, v.y, wid) - mine.y;
+    carry.x += __shfl_sync(0xffffffffu, v.x, 31);
+    carry.y += __shfl_sync(0xffffffffu, v.y, 31);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const bool s = (stay >> k) & 1, q = (equal >> k) & 1;
+      const uint32_t ms = __ballot_sync(0xffffffffu, s), mq = __ballot_sync(0xffffffffu, q);
+      const int e = eb + __popc(mq & below);
+      if (s || (q && e < ties)) {
+        const int j = sb + __popc(ms & below) + (e < ties ? e : ties);
+        R.kept[j] = tile + 32 * (K * wid + k) + lane;
+        R.w_out[j] = x[k];
+      }
+      sb += __popc(ms);
+      eb += __popc(mq);
+    }
+    __syncthreads();  // s_warp is read
+  }
+  for (int t = R.n + tid; t < R.L; t += 1024) R.w_out[t] = 0.f;
+}
+
+// CTAs of one (sequence, kv head, K or V) share its rows, 256-byte rows of 16
+// lanes: 64 rows a batch and CTA, every CTA its own batches.  A sequence with
+// a destination block of its own table has to move batch by batch: its rows
+// are cut into 1 << lg slices instead, one CTA a slice, and the other CTAs
+// leave.
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs A, uint4* k_pool, uint4* v_pool,
+                                                                  int lg) {
+  constexpr int U = 4;  // rows a thread in flight
   const int i = blockIdx.y;
-  int x = blockIdx.x;
-  const int slice = x % kSlices;
-  x /= kSlices;
-  uint4* pool = (x & 1) ? v_pool : k_pool;
-  const int h = x >> 1;
-  const int n = A.lens_out[i];
-  const int c = slice * LPR + threadIdx.x % LPR, rr = threadIdx.x / LPR;
+  uint4* pool = (blockIdx.x & 1) ? v_pool : k_pool;
+  const int h = blockIdx.x >> 1;
   const int32_t* kept = A.kept + (static_cast<long long>(i) * A.Hkv + h) * A.max_blocks * kBlock;
   const int32_t* src = A.src + static_cast<long long>(i) * A.max_blocks;
   const int32_t* dst = A.dst + static_cast<long long>(i) * A.dst_blocks;
-  for (int j0 = 0; j0 < n; j0 += RPP * U) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the selection
+  const int n = A.lens_out[i];
+  bool ordered = A.src == A.dst;
+  if (!ordered) {
+    int own = 0;
+    const int nb = (n + kBlock - 1) / kBlock;
+    for (int j = threadIdx.x; j < nb; j += kMoveThreads) own |= j < A.max_blocks && dst[j] == src[j];
+    ordered = __syncthreads_or(own);
+  }
+  if (!ordered) lg = 0;
+  const int lanes = 4 - lg;                          // log2 of a row's lanes
+  const int part = ordered ? 0 : blockIdx.z, parts = ordered ? 1 : gridDim.z;
+  if (ordered && static_cast<int>(blockIdx.z) >= (1 << lg)) return;
+  const int c = (ordered ? blockIdx.z << lanes : 0) + (threadIdx.x & ((1 << lanes) - 1)), rr = threadIdx.x >> lanes;
+  const int rpp = kMoveThreads >> lanes, batch = rpp * U;
+  int t[U];
+  auto indexes = [&](int j0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * rpp + rr;
+      t[u] = j < n ? kept[j] : -1;
+    }
+  };
+  indexes(part * batch);
+  for (int j0 = part * batch; j0 < n; j0 += batch * parts) {
     uint4 d[U];
     uint4* to[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * RPP + rr;
+      const int j = j0 + u * rpp + rr;
       to[u] = nullptr;
-      if (j >= n) continue;
-      const int t = kept[j];
-      const long long sb = src[t >> 4], db = dst[j >> 4];
+      if (t[u] < 0) continue;
+      const long long sb = __ldg(src + (t[u] >> 4)), db = __ldg(dst + (j >> 4));
       if (sb < 0 || sb >= A.num_blocks || db < 0 || db >= A.num_blocks) {
         record_error(A.err, PA_ERR_DEVICE_CHECK, sb < 0 || sb >= A.num_blocks ? sb : db);
         continue;
       }
-      const uint4* from = pool + ((sb * A.Hkv + h) * kBlock + (t & 15)) * 16 + c;
+      const uint4* from = pool + ((sb * A.Hkv + h) * kBlock + (t[u] & 15)) * 16 + c;
       uint4* at = pool + ((db * A.Hkv + h) * kBlock + (j & 15)) * 16 + c;
       if (from == at) continue;
       d[u] = *from;
       to[u] = at;
     }
-    __syncthreads();  // the batch is read: its rows may be written
+    indexes(j0 + batch * parts);
+    if (ordered) __syncthreads();  // the batch is read: its rows may be written
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (to[u]) *to[u] = d[u];
   }
+}
+
+template <int THREADS, int K, int CL>
+static cudaError_t launch_select(const EvictArgs& A, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(A.Hkv) * CL, static_cast<unsigned>(A.B));
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CL;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CL > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<THREADS, K, CL>, A);
 }
 
 }  // namespace pa
@@ -244,9 +476,38 @@ extern "C" int pa_evict(pa_pool_t p, const float* weights, float* weights_out, c
   A.num_blocks = p->num_blocks;
   A.err = p->err;
   cudaStream_t st = as_stream(stream);
-  evict_select_kernel<<<dim3(A.Hkv, num_seqs), kSelThreads, 0, st>>>(A);
-  if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
-  uint4 *k = static_cast<uint4*>(p->k), *v = static_cast<uint4*>(p->v);
-  evict_move_kernel<4><<<dim3(A.Hkv * 2 * 4, num_seqs), kMoveThreads, 0, st>>>(A, k, v);
+  const int span = max_blocks_per_seq * kBlock;
+  cudaError_t e = cudaSuccess;
+  if (span <= 256 * 8) e = launch_select<256, 8, 1>(A, st);
+  else if (span <= 256 * 16) e = launch_select<256, 16, 1>(A, st);
+  else if (span <= 512 * 16) e = launch_select<512, 16, 1>(A, st);
+  else if (span <= 512 * 16 * 2) e = launch_select<512, 16, 2>(A, st);
+  else if (span <= 512 * 16 * 4) e = launch_select<512, 16, 4>(A, st);
+  else if (span <= 512 * 16 * 8) e = launch_select<512, 16, 8>(A, st);
+  else evict_select_long_kernel<<<dim3(A.Hkv, A.B), 1024, 0, st>>>(A);
+  if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+  // CTAs of a row group: about 4,096 in all (64 sequences of 8 heads: 4 each,
+  // 85 us for 537 MB against 90 us with 1), at most one a batch of the longest
+  // row; slices: about 512 CTAs that move in order (4 long sequences of 8
+  // heads in place: 60 us with 8 slices, 140 us with 1; 64 sequences: 165 and 157 us)
+  const long long groups = 2ll * A.Hkv * num_seqs;
+  int lg = 0;
+  while (lg < 3 && (groups << lg) < 512) ++lg;
+  long long parts = 4096 / groups;
+  const long long batches = (static_cast<long long>(A.dst_blocks) * kBlock + 63) / 64;
+  if (parts > batches) parts = batches;
+  if (A.src == A.dst || parts < (1 << lg)) parts = 1 << lg;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * A.Hkv, num_seqs, static_cast<unsigned>(parts));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, evict_move_kernel, A, static_cast<uint4*>(p->k), static_cast<uint4*>(p->v), lg) !=
+      cudaSuccess)
+    return PA_ERR_CUDA;
   return cuda_status(cudaGetLastError());
 }
