@@ -10,9 +10,9 @@
 // tile belongs to one head.
 //
 // Two kernels.  The selection finds the r-th largest sum exactly, by radix
-// (the sums as order-preserving 32-bit keys, four passes of 8 bits), and
-// compacts in position order; counts in shared memory only, so the result
-// does not depend on timing.  The move copies rows.  Into fresh blocks every
+// (the sums as order-preserving 32-bit keys, 11 + 11 + 10 bits, and direct
+// ranking as soon as few keys are left), and compacts in position order;
+// counts in shared memory only, so the result does not depend on timing.  The move copies rows.  Into fresh blocks every
 // row is independent.  In place it is safe because batch c (rows j of [a, b))
 // is written after batches up to c are read, and later batches read positions
 // t_j >= j >= b only.
@@ -20,8 +20,13 @@
 
 namespace pa {
 
-constexpr int kBins = 256;
-constexpr int kCopies = 8;  // of each histogram bin, by lane: equal keys of a warp meet 4 at a time
+// Radix digits of the selection: 11 bits first (sign, exponent and two bits of
+// the mantissa: sums of attention weights spread over about 50 bins, so one
+// pass mostly leaves few enough keys to rank directly).
+constexpr int kBins = 2048;
+constexpr int kCopies = 2;    // of each bin, by lane: equal keys of a warp meet 16 at a time
+constexpr int kList = 64;     // keys ranked directly: two warps' work, less than a pass
+constexpr int kLongBins = 256, kLongCopies = 8;  // the long rows' four passes of 8 bits
 constexpr int kMoveThreads = 256;
 
 struct EvictArgs {
@@ -94,37 +99,38 @@ __device__ __forceinline__ int remote_int(const int* x, int rank) {
   return v;
 }
 
-// The bin of the r-th key from the top, given thread e's count `c` of bin 255 -
-// e (e < 256; every thread of the block calls).  found[0] = bin, [1] = keys in
-// higher bins, [2] = keys in the bin.  Ends with a block barrier.
-__device__ __forceinline__ void find_bin(int r, int c, int* s_sums, int* found) {
+// The bin of the r-th key from the top, given thread e's counts c of bins
+// N - 1 - e BPT and the BPT - 1 below it (N = THREADS * BPT bins; threads past
+// them pass zeros).  found[0] = bin, [1] = keys in higher bins, [2] = keys in
+// the bin.  Ends with a block barrier.
+template <int BPT>
+__device__ __forceinline__ void find_bin(int r, const int (&c)[BPT], int bins, int* s_sums, int* found) {
   const int e = threadIdx.x, lane = e & 31, wid = e >> 5;
-  int incl = c;
+  int sum = 0;
+#pragma unroll
+  for (int q = 0; q < BPT; ++q) sum += c[q];
+  int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31 && e < kBins) s_sums[wid] = incl;
+  if (lane == 31) s_sums[wid] = incl;
   __syncthreads();
-  if (e < kBins) {
+  int w = lane < wid ? s_sums[lane] : 0;
+  int above = incl - sum + __reduce_add_sync(0xffffffffu, w);
+  if (above < r && r <= above + sum) {
 #pragma unroll
-    for (int w = 0; w < kBins / 32 - 1; ++w) incl += w < wid ? s_sums[w] : 0;
-    if (incl - c < r && r <= incl) {
-      found[0] = kBins - 1 - e;
-      found[1] = incl - c;
-      found[2] = c;
+    for (int q = 0; q < BPT; ++q) {
+      if (above < r && r <= above + c[q]) {
+        found[0] = bins - 1 - e * BPT - q;
+        found[1] = above;
+        found[2] = c[q];
+      }
+      above += c[q];
     }
   }
   __syncthreads();
-}
-
-// A bin's count over its copies, which are cleared for the next pass.
-__device__ __forceinline__ int take_bin(int* s_hist, int e) {
-  int4* p = reinterpret_cast<int4*>(s_hist + e * kCopies);
-  const int4 u = p[0], v = p[1];
-  p[0] = p[1] = make_int4(0, 0, 0, 0);
-  return (u.x + u.y) + (u.z + u.w) + ((v.x + v.y) + (v.z + v.w));
 }
 
 // Rows of up to CL * THREADS * K tokens: a cluster of CL CTAs a row, the keys
@@ -135,9 +141,14 @@ __device__ __forceinline__ int take_bin(int* s_hist, int e) {
 template <int THREADS, int K, int CL>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(const EvictArgs A) {
   constexpr int NW = THREADS / 32;
+  constexpr int BPT = kBins / THREADS;
   __shared__ __align__(16) int s_hist[kBins * kCopies];
-  __shared__ int s_total[2][kBins];
-  __shared__ int s_found[3], s_sums[kBins / 32];
+  __shared__ __align__(16) int s_total[2][CL > 1 ? kBins : 4];
+  __shared__ int s_found[3], s_sums[32];
+  __shared__ uint2 s_list[kList];  // key, token
+  __shared__ uint2 s_all[CL > 1 ? kList : 1];
+  __shared__ int s_n;              // entries of s_list
+  __shared__ uint32_t s_ranked[NW * K];  // by warp and k: the lanes whose token is ranked in
   __shared__ int s_warp[32];
   __shared__ int s_equal, s_stay;  // this CTA's
   const int rank = CL > 1 ? static_cast<int>(blockIdx.x % CL) : 0;
@@ -168,60 +179,113 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
     return __shfl_sync(0xffffffffu, v - mine, wid);
   };
 
+  float x[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int t = t0 + 32 * k;
+    x[k] = k < used && t < R.L ? R.w[t] : 0.f;
+  }
   uint32_t key[K];
   uint32_t stay = 0, open = 0;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    key[k] = 0;
-    if (k >= used) continue;
     const int t = t0 + 32 * k;
-    const float x = t < R.L ? R.w[t] : 0.f;
-    key[k] = weight_key(x);
-    const bool inside = t >= R.lo && t < R.hi;
-    stay |= static_cast<uint32_t>(t < R.L && !inside) << k;
+    key[k] = weight_key(x[k]);
+    const bool inside = k < used && t >= R.lo && t < R.hi;
+    stay |= static_cast<uint32_t>(k < used && t < R.L && !inside) << k;
     open |= static_cast<uint32_t>(inside) << k;
   }
   if (R.r == R.hi - R.lo) stay |= open;
   if (R.contest()) {
     int r = R.r;
-    for (int e = tid; e < kBins * kCopies; e += THREADS) s_hist[e] = 0;
+    for (int e = tid; e < kBins * kCopies / 4; e += THREADS) reinterpret_cast<int4*>(s_hist)[e] = make_int4(0, 0, 0, 0);
+    if (tid == 0) s_n = 0;
     __syncthreads();
 #pragma unroll 1
-    for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t ones = pass < 2 ? 2047 : 1023;
       if (__any_sync(0xffffffffu, open)) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-          if (k < used && ((open >> k) & 1))
-            atomicAdd(&s_hist[((key[k] >> shift) & 255) * kCopies + (lane & (kCopies - 1))], 1);
+          if ((open >> k) & 1)
+            atomicAdd(&s_hist[((key[k] >> shift) & ones) * kCopies + (lane & (kCopies - 1))], 1);
       }
       __syncthreads();
-      int c = 0;
-      if (CL == 1) {
-        if (tid < kBins) c = take_bin(s_hist, kBins - 1 - tid);
-      } else {  // (two buffers: the next pass writes the other one)
-        int* total = s_total[(shift >> 3) & 1];
-        if (tid < kBins) total[tid] = take_bin(s_hist, kBins - 1 - tid);
+      int c[BPT];  // of bins kBins - 1 - BPT tid - q
+#pragma unroll
+      for (int q = 0; q < BPT; q += 2) {  // two bins, two copies each
+        int4* p = reinterpret_cast<int4*>(s_hist + (kBins - 2 - BPT * tid - q) * kCopies);
+        const int4 v = *p;
+        *p = make_int4(0, 0, 0, 0);
+        c[q] = v.z + v.w;
+        c[q + 1] = v.x + v.y;
+      }
+      if (CL > 1) {  // (two buffers: the next pass writes the other one)
+        int* total = s_total[pass & 1];
+#pragma unroll
+        for (int q = 0; q < BPT; ++q) total[q * THREADS + tid] = c[q];
         cluster_barrier();
 #pragma unroll
-        for (int x = 0; x < CL; ++x) c += tid < kBins ? remote_int(&total[tid], x) : 0;
+        for (int q = 0; q < BPT; ++q) {
+          c[q] = 0;
+#pragma unroll
+          for (int o = 0; o < CL; ++o) c[q] += remote_int(&total[q * THREADS + tid], o);
+        }
       }
-      find_bin(r, c, s_sums, s_found);
+      find_bin<BPT>(r, c, kBins, s_sums, s_found);
       const uint32_t bin = s_found[0];
       r -= s_found[1];
       if (__any_sync(0xffffffffu, open)) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          if (k >= used) continue;
-          const uint32_t digit = (key[k] >> shift) & 255;
+          const uint32_t digit = (key[k] >> shift) & ones;
           const uint32_t bit = open & (1u << k);
           if (digit > bin) stay |= bit;
           if (digit != bin) open &= ~bit;
         }
       }
+      if (s_found[2] == r || s_found[2] <= kList) break;
     }
-    if (r == s_found[2]) {
-      stay |= open;  // every key equal to the cut stays
-    } else {         // the first r of them do
+    const int left = s_found[2];
+    if (left == r) {
+      stay |= open;  // every key that agrees with the cut stays
+    } else if (left <= kList) {
+      // few keys left: a thread each counts those that come before it
+      for (int e = tid; e < NW * K; e += THREADS) s_ranked[e] = 0;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if ((open >> k) & 1) s_list[atomicAdd(&s_n, 1)] = make_uint2(key[k], t0 + 32 * k);
+      sync();
+      const uint2* list = s_list;
+      if (CL > 1) {
+        int first = 0;
+        for (int o = 0; o < CL; ++o) {
+          const int n = remote_int(&s_n, o);
+          if (tid < n) {
+            s_all[first + tid].x = remote_int(reinterpret_cast<const int*>(&s_list[tid].x), o);
+            s_all[first + tid].y = remote_int(reinterpret_cast<const int*>(&s_list[tid].y), o);
+          }
+          first += n;
+        }
+        list = s_all;
+        __syncthreads();
+      }
+      if (tid < left) {
+        const uint2 me = list[tid];
+        int ahead = 0;
+        for (int e = 0; e < left; ++e) {
+          const uint2 y = list[e];
+          ahead += y.x > me.x || (y.x == me.x && y.y < me.y);
+        }
+        const int at = static_cast<int>(me.y) - rank * NW * 32 * used;  // among this CTA's tokens
+        if (ahead < r && at >= 0 && at < NW * 32 * used)
+          atomicOr(&s_ranked[at / (32 * used) * K + at / 32 % used], 1u << (at & 31));
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < K; ++k) stay |= ((s_ranked[wid * K + k] >> lane) & 1) << k;
+    } else {  // many equal keys: the first r of them stay
       const int mine = __reduce_add_sync(0xffffffffu, __popc(open));
       if (lane == 0) s_warp[wid] = mine;
       __syncthreads();
@@ -231,7 +295,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
       uint32_t some = 0;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (k >= used) continue;
         const uint32_t m = __ballot_sync(0xffffffffu, (open >> k) & 1);
         if (((open >> k) & 1) && first + __popc(m & ((1u << lane) - 1)) < r) some |= 1u << k;
         first += __popc(m);
@@ -243,7 +306,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
 
   // the stayers' sums again (a key does not tell -0 from 0 or one NaN from
   // another), read before any is written: w_out may be w
-  float x[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) x[k] = (stay >> k) & 1 ? R.w[t0 + 32 * k] : 0.f;
   const int mine = __reduce_add_sync(0xffffffffu, __popc(stay));
@@ -272,8 +334,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
 // L2: 128K tokens are 512 KB).
 __global__ void __launch_bounds__(1024) evict_select_long_kernel(const EvictArgs A) {
   constexpr int K = 8, TILE = 1024 * K;
-  __shared__ __align__(16) int s_hist[kBins * kCopies];
-  __shared__ int s_found[3], s_sums[kBins / 32];
+  __shared__ __align__(16) int s_hist[kLongBins * kLongCopies];
+  __shared__ int s_found[3], s_sums[32];
   __shared__ int2 s_warp[32];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -291,7 +353,7 @@ __global__ void __launch_bounds__(1024) evict_select_long_kernel(const EvictArgs
   const bool contest = R.contest(), all = R.r == R.hi - R.lo;
   if (contest) {
     int r = R.r;
-    for (int e = tid; e < kBins * kCopies; e += 1024) s_hist[e] = 0;
+    for (int e = tid; e < kLongBins * kLongCopies; e += 1024) s_hist[e] = 0;
     __syncthreads();
 #pragma unroll 1
     for (int shift = 24; shift >= 0; shift -= 8) {
@@ -302,11 +364,18 @@ __global__ void __launch_bounds__(1024) evict_select_long_kernel(const EvictArgs
           const int t = tile + 32 * (K * wid + k) + lane;
           const uint32_t key = weight_key(x[k]);
           if (t >= R.lo && t < R.hi && (shift == 24 || (key >> (shift + 8)) == cut))
-            atomicAdd(&s_hist[((key >> shift) & 255) * kCopies + (lane & (kCopies - 1))], 1);
+            atomicAdd(&s_hist[((key >> shift) & 255) * kLongCopies + (lane & (kLongCopies - 1))], 1);
         }
       }
       __syncthreads();
-      find_bin(r, tid < kBins ? take_bin(s_hist, kBins - 1 - tid) : 0, s_sums, s_found);
+      int c[1] = {0};
+      if (tid < kLongBins) {
+        int4* p = reinterpret_cast<int4*>(s_hist + (kLongBins - 1 - tid) * kLongCopies);
+        const int4 u = p[0], v = p[1];
+        p[0] = p[1] = make_int4(0, 0, 0, 0);
+        c[0] = (u.x + u.y) + (u.z + u.w) + ((v.x + v.y) + (v.z + v.w));
+      }
+      find_bin<1>(r, c, kLongBins, s_sums, s_found);
       cut = cut << 8 | static_cast<uint32_t>(s_found[0]);
       r -= s_found[1];
     }
