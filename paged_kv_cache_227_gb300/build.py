@@ -30,7 +30,8 @@ def _nvcc():
 
 def _sources():
     srcs = [os.path.join(CSRC, f) for f in CU_SOURCES + CPP_SOURCES]
-    deps = srcs + [os.path.join(CSRC, "pa_internal.h"), os.path.join(CSRC, "device_utils.cuh"), os.path.join(INCLUDE, "pa.h")]
+    deps = srcs + [os.path.join(CSRC, "pa_internal.h"), os.path.join(CSRC, "device_utils.cuh"),
+                   os.path.join(CSRC, "shared_plan.cuh"), os.path.join(INCLUDE, "pa.h")]
     return srcs, deps
 
 

@@ -53,6 +53,7 @@
 
 #include "device_utils.cuh"
 #include "pa_internal.h"
+#include "shared_plan.cuh"
 
 namespace pa {
 
@@ -83,6 +84,14 @@ struct Shape {
   static constexpr int kMinCtas = 4;  // CTAs per SM the register budget is sized for
   static constexpr int kThreads = NW * 32;
   static constexpr int PB = G <= 4 ? 4 : 8;  // row stride of the per-warp p buffer
+};
+
+// Shared-prefix decode: where the combination finds the prefix's records and
+// writes the result.
+struct CombineArgs {
+  PrefixRecords X;
+  void* out;
+  int out_dtype;
 };
 
 struct Params {
@@ -117,6 +126,7 @@ struct Params {
   int lean_cost;            // LEAN: units counted ahead of each segment's tiles
   long long wait_limit_ns;
   int launch_flags;         // kLaunch* (host side; kLaunchSecondary also read by the kernel)
+  const CombineArgs* combine;  // host side: combine with prefix records instead of the plain merge
 };
 
 // Launch variants of one decode call (host side).  Secondary: the decode is
@@ -1350,6 +1360,138 @@ __global__ void __launch_bounds__(kMergeThreads, (kExt && G > 8) ? 8 : 4) merge_
 }
 
 // ---------------------------------------------------------------------------
+// The combination of the shared-prefix decode: a query row's records of its
+// own tokens (as in the merge) and of its group's prefix, in that order, by
+// log-sum-exp.  One warp per (sequence, query head); a lane holds 4 dims.  The
+// o loads of up to RB records are in flight together.
+// ---------------------------------------------------------------------------
+struct Combined {
+  float M = -INFINITY, L = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  // lane k: m and l of record k < n (n <= 32); o(k): this lane's dims of record k
+  template <int RB, typename Load>
+  __device__ __forceinline__ void add(int n, float mk, float lk, const Load& o) {
+    float mx = mk;
+#pragma unroll
+    for (int msk = 1; msk < 32; msk <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, msk));
+    const float mn = fmaxf(M, mx);
+    if (mn == -INFINITY) return;  // no token in any record so far
+    const float a = M == mn ? 1.f : fast_exp2(M - mn);
+    const float wk = mk == -INFINITY ? 0.f : fast_exp2(mk - mn);
+    float lw = wk * lk;
+#pragma unroll
+    for (int msk = 1; msk < 32; msk <<= 1) lw += __shfl_xor_sync(0xffffffffu, lw, msk);
+    L = L * a + lw;
+    O.x *= a;
+    O.y *= a;
+    O.z *= a;
+    O.w *= a;
+    M = mn;
+    for (int b0 = 0; b0 < n; b0 += RB) {
+      float4 ob[RB];
+      float w[RB];
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        w[r] = __shfl_sync(0xffffffffu, wk, (b0 + r) & 31);
+        if (b0 + r >= n) w[r] = 0.f;
+        // (a record without tokens holds no output)
+        ob[r] = w[r] != 0.f ? o(b0 + r) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        O.x = fmaf(w[r], ob[r].x, O.x);
+        O.y = fmaf(w[r], ob[r].y, O.y);
+        O.z = fmaf(w[r], ob[r].z, O.z);
+        O.w = fmaf(w[r], ob[r].w, O.w);
+      }
+    }
+  }
+};
+
+template <int G>
+__global__ void __launch_bounds__(kMergeThreads, 8) combine_kernel(const __grid_constant__ Params P,
+                                                                   const __grid_constant__ CombineArgs C) {
+  extern __shared__ int mpfx[];  // [B + 1]
+  // the own tokens' lengths and the plan are complete: the decode that this
+  // grid depends on read them
+  block_prefix(P, mpfx, nullptr, false);
+  const int lane = threadIdx.x & 31;
+  const long long wpb = kMergeThreads / 32;
+  const long long n_items = static_cast<long long>(P.B) * P.Hkv * G;
+  constexpr bool kFrag = G > 4;  // the decode's records are in fragment order
+  bool waited = false;
+  for (long long it = blockIdx.x * wpb + (threadIdx.x >> 5); it < n_items; it += gridDim.x * wpb) {
+    const int g = static_cast<int>(it % G);
+    const long long sh = it / G;
+    const int h = static_cast<int>(sh % P.Hkv);
+    const int i = static_cast<int>(sh / P.Hkv);
+    const long long row = static_cast<long long>(i) * P.Hq + h * G + g;
+    const int entry = C.X.n_groups ? __ldcg(&C.X.place[i]) : -1;
+    const bool own = mpfx[i + 1] != mpfx[i];
+    Combined R;
+    // lane's dims: 4 lane .. + 3, or in fragment order 32 (lane / 8) + lane % 8 + {0, 8, 16, 24}
+    const int d0 = kFrag ? 32 * (lane >> 3) + (lane & 7) : 4 * lane;
+    if (!waited) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      waited = true;
+    }
+    if (own) {
+      const SegmentRecords recs(P, mpfx, i, h);
+      if (recs.count <= 1) {  // a whole segment: the decode's normalised row
+        const float e = __ldcg(&P.lse[row]);
+        const float* o = static_cast<const float*>(P.out) + row * kHeadDim + d0;
+        R.add<1>(1, lane == 0 ? e : -INFINITY, 1.f, [&](int) {
+          if (kFrag) return make_float4(__ldcg(o), __ldcg(o + 8), __ldcg(o + 16), __ldcg(o + 24));
+          return __ldcg(reinterpret_cast<const float4*>(o));
+        });
+      } else {
+        for (int c0 = 0; c0 < recs.count; c0 += 32) {
+          const int cnt = recs.count - c0 < 32 ? recs.count - c0 : 32;
+          float mk = -INFINITY, lk = 0.f;
+          if (lane < cnt) {
+            const float* rl = P.ws + recs.at(P, c0 + lane) * record_floats(G) + record_cols(G) * kHeadDim + g;
+            mk = __ldcg(rl);
+            lk = __ldcg(rl + 64);
+          }
+          R.add<4>(cnt, mk, lk, [&](int k) {
+            const float4* r4p = reinterpret_cast<const float4*>(P.ws + recs.at(P, c0 + k) * record_floats(G));
+            return __ldcg(r4p + (kFrag ? frag_record_index(g, lane) : g * (kHeadDim / 4) + lane));
+          });
+        }
+      }
+    }
+    if (entry >= 0) {
+      const RowRecords recs(C.X, entry, __ldcg(&C.X.group_of[i]), h, g, G, P.Hkv);
+      for (int c0 = 0; c0 < recs.count; c0 += 32) {
+        const int cnt = recs.count - c0 < 32 ? recs.count - c0 : 32;
+        float mk = -INFINITY, lk = 0.f;
+        if (lane < cnt) {
+          const float* m = recs.m(c0 + lane);
+          mk = __ldcg(m);
+          lk = __ldcg(m + kItemRows);
+        }
+        R.add<4>(cnt, mk, lk, [&](int k) {
+          const float* o = reinterpret_cast<const float*>(recs.o(c0 + k)) + d0;
+          if (kFrag) return make_float4(__ldcg(o), __ldcg(o + 8), __ldcg(o + 16), __ldcg(o + 24));
+          return __ldcg(reinterpret_cast<const float4*>(o));
+        });
+      }
+    }
+    const float inv = R.L == 0.f ? 0.f : 1.f / R.L;
+    const long long at = row * kHeadDim + d0;
+    if constexpr (kFrag) {
+      store_out(C.out, at, R.O.x * inv, C.out_dtype);
+      store_out(C.out, at + 8, R.O.y * inv, C.out_dtype);
+      store_out(C.out, at + 16, R.O.z * inv, C.out_dtype);
+      store_out(C.out, at + 24, R.O.w * inv, C.out_dtype);
+    } else {
+      store_out4(C.out, at, R.O.x * inv, R.O.y * inv, R.O.z * inv, R.O.w * inv, C.out_dtype);
+    }
+  }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // Several new query tokens per sequence.  Sequence i's T_i new tokens are its
 // last T_i positions; token t sees positions 0 .. L_i - T_i + t.  They are
 // packed TC at a time (TC = 8 / G, or 16 / G in two column halves when the
@@ -1704,7 +1846,15 @@ static int launch_typed(Params& P, int device, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, merge_kernel<G, kExt>, P) != cudaSuccess) return PA_ERR_CUDA;
+    if constexpr (kExt && G <= PA_MAX_GROUP) {
+      if (P.combine) {
+        if (cudaLaunchKernelEx(&cfg, combine_kernel<G>, P, *P.combine) != cudaSuccess) return PA_ERR_CUDA;
+      } else if (cudaLaunchKernelEx(&cfg, merge_kernel<G, kExt>, P) != cudaSuccess) {
+        return PA_ERR_CUDA;
+      }
+    } else if (cudaLaunchKernelEx(&cfg, merge_kernel<G, kExt>, P) != cudaSuccess) {
+      return PA_ERR_CUDA;
+    }
   }
   if (timed) {
     if (cudaEventRecord(g_prof_events[2 * g_prof_next + 1], stream) != cudaSuccess) return PA_ERR_CUDA;
@@ -1760,7 +1910,8 @@ static int decode_common(pa_pool_t p, const void* q, const void* k_new, const vo
                          int partition_blocks, void* ws, size_t ws_bytes, void* stream,
                          const int32_t* table_offs = nullptr, float* lse = nullptr,
                          const int32_t* ext_ntok = nullptr, int ext_g = 0, int launch_flags = 0,
-                         const int32_t* ext_qbase = nullptr, int ext_hq = 0, float* scores = nullptr) {
+                         const int32_t* ext_qbase = nullptr, int ext_hq = 0, float* scores = nullptr,
+                         const CombineArgs* combine = nullptr) {
   if (!p || !q || !tables || !seq_lens || !out || B <= 0 || Hq <= 0 || max_blocks <= 0)
     return PA_ERR_INVALID;
   if (out_dtype != PA_FP16 && out_dtype != PA_BF16 && out_dtype != PA_FP32) return PA_ERR_INVALID;
@@ -1805,6 +1956,7 @@ static int decode_common(pa_pool_t p, const void* q, const void* k_new, const vo
   P.ext_qbase = ext_qbase;
   P.ext_hq = ext_hq;
   P.scores = scores;
+  P.combine = combine;
   P.seq_lens = seq_lens;
   P.out = out;
   P.ws = static_cast<float*>(ws);
@@ -1963,11 +2115,18 @@ int pa_decode_weights(pa_pool_t p, const void* q, const int32_t* block_tables, i
 
 namespace pa {
 
-int decode_own_tokens(pa_pool* p, const void* q, const int32_t* tables, int max_blocks, const int32_t* lens,
-                      const int32_t* table_offs, int B, int Hq, float scale, float* out, float* lse, void* ws,
-                      size_t ws_bytes, void* stream) {
-  return decode_common(p, q, nullptr, nullptr, tables, max_blocks, lens, B, Hq, scale, out, PA_FP32, SCHED_LEAN, 0, ws,
-                       ws_bytes, stream, table_offs, lse, nullptr, 0, kLaunchAfterPlan);
+int decode_own_and_combine(pa_pool* p, const void* q, const int32_t* tables, int max_blocks, const int32_t* lens,
+                           const int32_t* table_offs, int B, int Hq, float scale, float* o_s, float* lse_s, void* out,
+                           int out_dtype, const PrefixRecords& X, void* ws, size_t ws_bytes, void* stream) {
+  CombineArgs C{};
+  C.X = X;
+  C.out = out;
+  C.out_dtype = out_dtype;
+  // with groups the kernel before is the prefix product, which ran past the
+  // plan; without, it is the plan itself
+  return decode_common(p, q, nullptr, nullptr, tables, max_blocks, lens, B, Hq, scale, o_s, PA_FP32, SCHED_LEAN, 0, ws,
+                       ws_bytes, stream, table_offs, lse_s, nullptr, 0, X.n_groups ? kLaunchSecondary : kLaunchAfterPlan,
+                       nullptr, 0, nullptr, &C);
 }
 
 }  // namespace pa

@@ -77,11 +77,14 @@ int launch_append_tail(void* k_pool, void* v_pool, int n_kv_heads, long long num
 int launch_weight_sums(const pa_pool* p, const float* scores, const float* lse, float* weights, float decay,
                        const int32_t* seq_lens, int B, int Hq, int max_blocks, cudaStream_t stream);
 
-// The split decode of each sequence's lens[i] tokens whose table starts at
-// element table_offs[i] (kernel results of the kernel before it in the
-// stream, whose programmatic dependent it is): fp32 out and log2-sum-exps.
-int decode_own_tokens(pa_pool* p, const void* q, const int32_t* tables, int max_blocks, const int32_t* lens,
-                      const int32_t* table_offs, int B, int Hq, float scale, float* out, float* lse, void* ws,
-                      size_t ws_bytes, void* stream);
+// The second half of pa_decode_shared (decode.cu): the split decode of each
+// sequence's lens[i] own tokens, whose table starts at element table_offs[i]
+// (both written by a kernel that is complete when the kernel before this call
+// in the stream has started all of its CTAs), and the combination with the
+// prefix's records, which that kernel may still be writing.
+struct PrefixRecords;
+int decode_own_and_combine(pa_pool* p, const void* q, const int32_t* tables, int max_blocks, const int32_t* lens,
+                           const int32_t* table_offs, int B, int Hq, float scale, float* o_s, float* lse_s, void* out,
+                           int out_dtype, const PrefixRecords& X, void* ws, size_t ws_bytes, void* stream);
 
 }  // namespace pa

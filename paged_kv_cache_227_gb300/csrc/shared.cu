@@ -10,8 +10,13 @@
 // ordinary decode (decode.cu), and the two are joined by log-sum-exp:
 //   out = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k.
 //
-// Four kernels in stream order: the plan (checks the groups, lays out the
-// work), the decode of the own tokens, the prefix product, the combination.
+// Four kernels, each a programmatic dependent of the one before: the plan
+// (checks the groups, lays out the work), the prefix product, the decode of the
+// own tokens, and the combination (in decode.cu, with the decode's own merge).
+// The product is bound by the tensor cores and the decode by memory, so they
+// share the GPU: the plan gives the product as many SMs as its part of the
+// work, estimated, and the decode's CTAs take the others, and what the product
+// frees.
 //
 // The prefix product runs on the tcgen05 tensor cores, one CTA an SM:
 //  - an item is up to 256 rows of one group; a segment is (item, kv head); a
@@ -41,12 +46,11 @@
 
 #include "device_utils.cuh"
 #include "pa_internal.h"
+#include "shared_plan.cuh"
 
 namespace pa {
 
 constexpr int kMaxSharedSeqs = 4096;   // the own-token decode's limit
-constexpr int kRows = 128;             // rows of a warpgroup
-constexpr int kItemRows = 2 * kRows;
 constexpr int kChunkBlocks = 8;        // cache blocks of a chunk: 128 tokens
 constexpr int kChunk = kChunkBlocks * kBlock;
 constexpr int kTile = kChunk * kRowBytes;  // 32 KiB: K or V of a chunk, Q of a warpgroup
@@ -58,17 +62,10 @@ constexpr float kMoveBy = 8.f;         // log2 units the maximum may lag behind
 constexpr int kPlanCluster = 8, kPlanThreads = 512;
 constexpr int kSoftWarps = 8;
 constexpr int kPrefixThreads = (kSoftWarps + 2) * 32;  // + producer warp, + MMA warp
-constexpr int kRecFloats = kItemRows * kHeadDim + 2 * kItemRows;  // o, m, l
-
-// Plan of one group (device, written by the plan kernel).
-struct GroupPlan {
-  long long unit0;  // units before this group
-  int item0;        // items before this group
-  int rows;         // S * G, 0 for a group that takes no part
-  int chunks;       // ceil(P / 8)
-  int blocks;       // P
-  int member0;      // its first entry in members
-};
+constexpr int kMasks = 4;              // chunk masks in flight
+// The work of the two halves, in ns of one SM, to divide the SMs by: a chunk
+// of the product (two 128-row tiles), and a tile of 16 tokens of the decode.
+constexpr int kChunkNs = 1300, kTileNs = 130;
 
 struct SharedArgs {
   CUtensorMap tmap;               // [K|V][half][rows][64] boxes of 16 rows x 64 elements
@@ -81,20 +78,18 @@ struct SharedArgs {
   int B, Hq, Hkv, G, n_groups, n_members, max_blocks;
   float qscale;                   // |scale| * log2(e)
   uint32_t qflip;                 // sign bits to flip in q (negative scale)
-  void* out;
-  int out_dtype;
   // workspace
   GroupPlan* plan;                // [n_groups + 1]; the last: totals
-  int32_t* claims;                // [B]: groups that name the sequence
+  int32_t* owner;                 // [B]: entry in members + 1 that claimed the sequence, or 0
   int32_t* bad;                   // [n_groups]
   int32_t* place;                 // [B]: entry in members, or -1
   int32_t* group_of;              // [B]
+  long long* tiles;               // [kPlanCluster]: each plan CTA's part of sum ceil(L / 16)
   int32_t* lens_s;                // [B]: own tokens
   int32_t* offs_s;                // [B]: table element where they start
-  float* o_s;                     // [B][Hq][128]
-  float* lse_s;                   // [B][Hq]
   float* rec;                     // records
-  long long num_blocks, n_rec;
+  long long num_blocks;
+  int ctas;                       // of the prefix product: at most this many work
   long long* err;
   long long wait_limit_ns;
 };
@@ -108,15 +103,18 @@ __device__ __forceinline__ void cluster_sync() {
 // takes no part; its members are decoded without it.
 __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThreads) shared_plan_kernel(
     const __grid_constant__ SharedArgs A) {
-  const int n_threads = kPlanCluster * kPlanThreads;
+  __shared__ long long s_tiles[kPlanThreads / 32];
+  constexpr int n_threads = kPlanCluster * kPlanThreads;
   const int tid = blockIdx.x * kPlanThreads + threadIdx.x;
   const int lane = threadIdx.x & 31;
   const int cap = A.max_blocks * kBlock;
-  // the decode launched as this grid's dependent waits for it to complete
+  // the product launched as this grid's dependent waits for it to complete
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  long long tiles = 0;
   for (int i = tid; i < A.B; i += n_threads) {
-    A.claims[i] = 0;
-    A.place[i] = -1;
+    A.owner[i] = 0;
+    const int L = A.seq_lens[i];
+    tiles += L > 0 ? ((L < cap ? L : cap) + kBlock - 1) / kBlock : 0;
   }
   // group_start runs from 0 to n_members and every group has a member, else
   // no group takes part (every CTA looks at all of it)
@@ -126,54 +124,71 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
     broken |= m0 < 0 || m0 >= m1 || m1 > A.n_members || (k == 0 && m0 != 0) ||
               (k == A.n_groups - 1 && m1 != A.n_members);
   }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+  if (lane == 0) s_tiles[threadIdx.x >> 5] = tiles;
   broken = __syncthreads_or(broken);
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kPlanThreads / 32; ++w) tiles += s_tiles[w];
+    A.tiles[blockIdx.x] = tiles;
+  }
   for (int k = tid; k < A.n_groups; k += n_threads) {
     const int P = A.prefix_blocks[k];
     A.bad[k] = broken || P < 0 || P > A.max_blocks;
   }
-  cluster_sync();
-  // members: in range, long enough, on the first member's blocks.  One warp
-  // an entry; its group is the last that starts at or before it.
-  for (int e = tid >> 5; e < A.n_members; e += n_threads >> 5) {
+  // a member entry's group: the last that starts at or before it
+  auto group_at = [&](int e) {
     int lo = 0, hi = A.n_groups - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (A.group_start[mid] <= e) lo = mid; else hi = mid - 1;
     }
-    const int k = lo;
+    return lo;
+  };
+  cluster_sync();
+  // members: in range, named once, long enough, on the first member's blocks.
+  // One warp an entry.
+  for (int e = tid >> 5; e < A.n_members; e += n_threads >> 5) {
+    const int k = group_at(e);
     const int i = A.members[e];
     const bool in = i >= 0 && i < A.B;
-    if (lane == 0 && in) atomicAdd(&A.claims[i], 1);
-    if (__ldcg(&A.bad[k])) continue;
-    const int first = A.members[A.group_start[k]];
-    const int P = A.prefix_blocks[k];
+    if (lane == 0 && in) {
+      const int before = atomicExch(&A.owner[i], e + 1);
+      if (before) A.bad[k] = A.bad[group_at(before - 1)] = 1;
+      A.group_of[i] = k;  // (either, when named twice: both groups are bad)
+    }
+    const int m0 = A.group_start[k], P = A.prefix_blocks[k];
+    if (broken || P < 0 || P > A.max_blocks) continue;
+    const int first = A.members[m0];
     bool fine = in && first >= 0 && first < A.B;
     if (fine) {
       const int L = A.seq_lens[i];
       fine = L <= cap && L >= P * kBlock;
       const int32_t* a = A.tables + static_cast<long long>(i) * A.max_blocks;
       const int32_t* b = A.tables + static_cast<long long>(first) * A.max_blocks;
-      if (i != first)
-#pragma unroll 8
-        for (int x = lane; x < P; x += 32) fine = fine && a[x] == b[x];
+      int other = 0;
+      if (i != first) {
+        int x = lane;
+        for (; x + 7 * 32 < P; x += 8 * 32) {  // 16 loads in flight
+          int va[8], vb[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            va[y] = a[x + 32 * y];
+            vb[y] = b[x + 32 * y];
+          }
+#pragma unroll
+          for (int y = 0; y < 8; ++y) other |= va[y] ^ vb[y];
+        }
+        for (; x < P; x += 32) other |= a[x] ^ b[x];
+      }
+      fine = fine && other == 0;
     }
     if (!__all_sync(0xffffffffu, fine) && lane == 0) A.bad[k] = 1;
   }
   cluster_sync();
-  for (int e = tid; e < A.n_members; e += n_threads) {
-    const int i = A.members[e];
-    if (i < 0 || i >= A.B || __ldcg(&A.claims[i]) < 2) continue;
-    int lo = 0, hi = A.n_groups - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (A.group_start[mid] <= e) lo = mid; else hi = mid - 1;
-    }
-    A.bad[lo] = 1;
-  }
-  cluster_sync();
-  if (tid < 32) {  // the groups' items and units, in group order
+  if (blockIdx.x == 0 && threadIdx.x < 32) {  // the groups' items and units, in group order
     int item = 0;
-    long long unit = 0;
+    long long unit = 0, shared_tiles = 0;
     for (int k0 = 0; k0 < A.n_groups; k0 += 32) {
       const int k = k0 + lane;
       GroupPlan g{};
@@ -184,10 +199,12 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
         if (bad) record_error(A.err, PA_ERR_DEVICE_CHECK, k);
         g.member0 = A.group_start[k];
         g.blocks = A.prefix_blocks[k];
-        g.rows = bad || g.blocks == 0 ? 0 : (A.group_start[k + 1] - g.member0) * A.G;
-        g.chunks = (g.blocks + kChunkBlocks - 1) / kChunkBlocks;
+        const int members = bad || g.blocks == 0 ? 0 : A.group_start[k + 1] - g.member0;
+        g.rows = members * A.G;
+        g.chunks = bad ? 0 : (g.blocks + kChunkBlocks - 1) / kChunkBlocks;
         items = (g.rows + kItemRows - 1) / kItemRows;
         units = static_cast<long long>(items) * A.Hkv * g.chunks;
+        shared_tiles += static_cast<long long>(members) * g.blocks;
       }
       int ii = items;
       long long uu = units;
@@ -206,31 +223,28 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
       item += __shfl_sync(0xffffffffu, ii, 31);
       unit += __shfl_sync(0xffffffffu, uu, 31);
     }
+    long long own = lane < kPlanCluster ? __ldcg(&A.tiles[lane]) : 0;
+    own -= shared_tiles;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
     if (lane == 0) {
       GroupPlan g{};
       g.unit0 = unit;
       g.item0 = item;
+      // SMs of the product: its share of the work
+      const float a = static_cast<float>(unit) * kChunkNs, b = static_cast<float>(own) * A.Hkv * kTileNs;
+      int n = unit ? static_cast<int>(A.ctas * (a / (a + b)) + 0.5f) : 0;
+      n = n < 1 ? 1 : (n > A.ctas ? A.ctas : n);
+      g.rows = unit < n ? static_cast<int>(unit) : n;
       A.plan[A.n_groups] = g;
     }
   }
-  for (int e = tid; e < A.n_members; e += n_threads) {
-    const int i = A.members[e];
-    if (i < 0 || i >= A.B) continue;
-    int lo = 0, hi = A.n_groups - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (A.group_start[mid] <= e) lo = mid; else hi = mid - 1;
-    }
-    if (!__ldcg(&A.bad[lo]) && A.prefix_blocks[lo] > 0) {
-      A.place[i] = e;
-      A.group_of[i] = lo;
-    }
-  }
-  cluster_sync();
   for (int i = tid; i < A.B; i += n_threads) {
-    const int L = A.seq_lens[i];
-    const int P = __ldcg(&A.place[i]) >= 0 ? A.prefix_blocks[__ldcg(&A.group_of[i])] : 0;
-    A.lens_s[i] = L - P * kBlock;  // (a length out of range is the decode's to report)
+    const int e = __ldcg(&A.owner[i]) - 1;
+    const int k = e >= 0 ? __ldcg(&A.group_of[i]) : 0;
+    const int P = e >= 0 && !__ldcg(&A.bad[k]) ? A.prefix_blocks[k] : 0;
+    A.place[i] = P > 0 ? e : -1;
+    A.lens_s[i] = A.seq_lens[i] - P * kBlock;  // (a length out of range is the decode's to report)
     A.offs_s[i] = i * A.max_blocks + P;
   }
 }
@@ -294,6 +308,23 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -321,37 +352,15 @@ struct SharedPiece {
   bool both;           // more than 128 rows: every chunk for both warpgroups
 };
 
-__device__ __forceinline__ GroupPlan load_plan(const GroupPlan* p) {
-  const int4* s = reinterpret_cast<const int4*>(p);
-  const int4 a = __ldcg(s), b = __ldcg(s + 1);
-  GroupPlan g;
-  g.unit0 = static_cast<long long>(static_cast<unsigned>(a.x)) | static_cast<long long>(a.y) << 32;
-  g.item0 = a.z;
-  g.rows = a.w;
-  g.chunks = b.x;
-  g.blocks = b.y;
-  g.member0 = b.z;
-  return g;
-}
-static_assert(sizeof(GroupPlan) == 32 && offsetof(GroupPlan, item0) == 8 && offsetof(GroupPlan, chunks) == 16,
-              "load_plan reads a plan as two 16-byte vectors");
-
-// Smallest range of a CTA, in chunks.
-constexpr int kMinUnits = 1;
-__device__ __forceinline__ long long units_per_cta(long long units, int ctas) {
-  const long long per = (units + ctas - 1) / ctas;
-  return per < kMinUnits ? kMinUnits : per;
-}
-
 struct SharedPieces {
   const SharedArgs& A;
   long long cur, end;
   int cta, k;
   GroupPlan g;
 
-  __device__ SharedPieces(const SharedArgs& a, int c, int ctas) : A(a), cta(c) {
-    const long long total = __ldcg(&A.plan[A.n_groups].unit0);
-    const long long per = units_per_cta(total, ctas);
+  __device__ SharedPieces(const SharedArgs& a, int c) : A(a), cta(c) {
+    const GroupPlan all = load_plan(&A.plan[A.n_groups]);
+    const long long total = all.unit0, per = units_per_cta(total, all.rows);
     cur = per * cta;
     end = cur + per < total ? cur + per : total;
     k = -1;
@@ -387,7 +396,6 @@ struct SharedPieces {
     p.c1 = seg_units - p.c0 < left ? static_cast<int>(seg_units) : p.c0 + static_cast<int>(left);
     p.blocks = g.blocks;
     p.member0 = g.member0;
-    // segment number + CTA number grows with every piece: one record each
     p.rec = static_cast<long long>(g.item0) * A.Hkv + seg + cta;
     cur += p.c1 - p.c0;
     return true;
@@ -399,8 +407,8 @@ struct __align__(1024) PrefixSmem {
   uint8_t k[kStages][kTile];
   uint8_t v[kStages][kTile];
   unsigned long long kfull[kStages], kfree[kStages], vfull[kStages], vfree[kStages];
-  unsigned long long qfull, qfree, sfull[2], pfull[2], ofull[2], drain;
-  uint32_t mask[kStages];  // blocks of the chunk that are there
+  unsigned long long qfull, qfree, sfull[2], pfull[2][2], ofull[2], drain;
+  uint32_t mask[kMasks];  // blocks of the chunk that are there
   uint32_t tmem;
   int abort_flag;
 };
@@ -423,7 +431,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
     mbar_init(smem_addr(&S.qfree), 2 * kRows);
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_addr(&S.sfull[w]), 1);
-      mbar_init(smem_addr(&S.pfull[w]), kRows);
+      mbar_init(smem_addr(&S.pfull[w][0]), kRows);
+      mbar_init(smem_addr(&S.pfull[w][1]), kRows);
       mbar_init(smem_addr(&S.ofull[w]), 1);
     }
     mbar_init(smem_addr(&S.drain), 1);
@@ -438,18 +447,20 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
   }
   __syncthreads();
   tc_fence_after();
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = S.tmem;
   volatile int* abort_flag = &S.abort_flag;
   const long long limit = A.wait_limit_ns;
   auto wait = [&](unsigned long long& bar, uint32_t parity, int site) {
     return wait_phase(smem_addr(&bar), parity, abort_flag, limit, A.err, site);
   };
-  SharedPieces pieces(A, blockIdx.x, gridDim.x);
+  SharedPieces pieces(A, blockIdx.x);
   SharedPiece p;
 
   if (warp == kProducer) {
     // ---- loads: K and V of each chunk, lane 2b + half for block b
-    int n = 0;
+    int n = 0, nk = 0, nv = 0;  // chunks, K and V loads issued
     bool ok = true;
     while (ok && pieces.next(p)) {
       const int32_t* row = A.tables + static_cast<long long>(A.members[p.member0]) * A.max_blocks;
@@ -472,37 +483,45 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
         const int y = static_cast<int>((static_cast<long long>(blk) * A.Hkv + p.h) * kBlock);
         const uint32_t at = (lane & 1) * kHalf + (lane >> 1) * (kBlock * 128);
         const uint32_t bytes = __popc(mask) * kTileBytes;
-        // mask[s] is last read by the weights' product of the stage's previous chunk
-        ok = (use == 0) || (wait(S.kfree[s], (use - 1) & 1, 20) && wait(S.vfree[s], (use - 1) & 1, 21));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (lane == 0) {
-          S.mask[s] = mask;
-          if (bytes) {
-            mbar_arrive_expect_tx(smem_addr(&S.kfull[s]), bytes);
-            mbar_arrive_expect_tx(smem_addr(&S.vfull[s]), bytes);
-          } else {
-            mbar_arrive(smem_addr(&S.kfull[s]));
-            mbar_arrive(smem_addr(&S.vfull[s]));
+        // (mask[n % 4] was last read for chunk n - 4, whose scores and values
+        // came before the scores of chunk n - 2, which free this K stage)
+        if (use > 0 && !__all_sync(0xffffffffu, wait(S.kfree[s], (use - 1) & 1, 20))) {
+          ok = false;
+          break;
+        }
+        auto load = [&](unsigned long long& full, uint8_t* tile, int kv) {
+          if (lane == 0) {
+            if (bytes)
+              mbar_arrive_expect_tx(smem_addr(&full), bytes);
+            else
+              mbar_arrive(smem_addr(&full));
           }
+          __syncwarp();
+          if (valid) tma_load_half(smem_addr(tile) + at, &A.tmap, y, lane & 1, kv, smem_addr(&full));
+        };
+        if (lane == 0) S.mask[n % kMasks] = mask;
+        load(S.kfull[s], S.k[s], 0);
+        ++nk;
+        if (use > 0 && !__all_sync(0xffffffffu, wait(S.vfree[s], (use - 1) & 1, 21))) {
+          ok = false;
+          break;
         }
-        __syncwarp();
-        if (valid) {
-          tma_load_half(smem_addr(S.k[s]) + at, &A.tmap, y, lane & 1, 0, smem_addr(&S.kfull[s]));
-          tma_load_half(smem_addr(S.v[s]) + at, &A.tmap, y, lane & 1, 1, smem_addr(&S.vfull[s]));
-        }
+        load(S.vfull[s], S.v[s], 1);
+        ++nv;
         blk = ahead;
       }
     }
     // never leave a load in flight into this CTA's shared memory
     if (lane == 0 && *abort_flag) {
-      for (int k = n > kStages ? n - kStages : 0; k < n; ++k) {
-        const long long t0 = global_ns();
-        while (!(mbar_try_wait(smem_addr(&S.kfull[k % kStages]), (k / kStages) & 1) &&
-                 mbar_try_wait(smem_addr(&S.vfull[k % kStages]), (k / kStages) & 1)) &&
-               global_ns() - t0 < limit) {
+      auto drain = [&](unsigned long long* full, int issued) {
+        for (int k = issued > kStages ? issued - kStages : 0; k < issued; ++k) {
+          const long long t0 = global_ns();
+          while (!mbar_try_wait(smem_addr(&full[k % kStages]), (k / kStages) & 1) && global_ns() - t0 < limit) {
+          }
         }
-      }
+      };
+      drain(S.kfull, nk);
+      drain(S.vfull, nv);
     }
   } else if (warp == kMma) {
     // ---- products.  Step t of a piece serves warpgroup t & 1; S of step
@@ -540,16 +559,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
         if (ok && steps > 1) scores(1);
         for (int t = 0; ok && t < steps; ++t) {
           const int w = t & 1, n = n0 + (p.both ? t >> 1 : t), s = n % kStages;
-          ok = wait(S.pfull[w], p_phase[w], 24);
-          p_phase[w] ^= 1;
+          ok = wait(S.pfull[w][0], p_phase[w], 24);
           if (ok && (!p.both || w == 0)) ok = wait(S.vfull[s], (n / kStages) & 1, 25);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&S.mask[s]);
-          {
-            const uint32_t b = smem_addr(S.v[s]);
-            bool add = !first[w];
-            for (int kb = 0; kb < kChunkBlocks; ++kb) {
+          const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&S.mask[n % kMasks]);
+          const uint32_t b = smem_addr(S.v[s]);
+          bool add = !first[w];
+          auto values = [&](int kb0) {
+            for (int kb = kb0; kb < kb0 + kChunkBlocks / 2; ++kb) {
               if (!((mask >> kb) & 1)) continue;
               // 16 tokens: P's 8 columns, V's 16 rows; halves of the dims kHalf apart
               const uint64_t bd = operand_desc(b + kb * (kBlock * 128), kHalf, 1024);
@@ -557,9 +575,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
               add = true;
               if (kLo) mma_ts(tmem + 256 + w * 128, tmem + w * 128 + 64 + kb * 8, bd, kIdO, true);
             }
-            if (!p.both || w == 1) mma_commit(smem_addr(&S.vfree[s]));
-            if (t + 2 >= steps) mma_commit(smem_addr(&S.ofull[w]));
-          }
+          };
+          values(0);
+          ok = wait(S.pfull[w][1], p_phase[w], 29);
+          p_phase[w] ^= 1;
+          if (!ok) break;
+          tc_fence_after();
+          values(kChunkBlocks / 2);
+          if (!p.both || w == 1) mma_commit(smem_addr(&S.vfree[s]));
+          if (t + 2 >= steps) mma_commit(smem_addr(&S.ofull[w]));
           if (mask) first[w] = false;
           if (t + 2 < steps) scores(t + 2);
         }
@@ -630,28 +654,26 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
         if (!ok) break;
         any = true;
         tc_fence_after();
-        const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&S.mask[(n0 + j) % kStages]);
+        const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&S.mask[(n0 + j) % kMasks]);
         uint32_t raw[128];
 #pragma unroll
         for (int x = 0; x < 4; ++x) tmem_ld32(t_s + 32 * x, raw + 32 * x);
         tmem_wait_ld();
-        float mx = -INFINITY;
-        if (mask == 0xffu) {
+        if (mask != 0xffu) {  // blocks past the prefix or outside the pool weigh nothing
 #pragma unroll
-          for (int x = 0; x < 128; ++x) {
-            const float v = __uint_as_float(raw[x]) * A.qscale;
-            raw[x] = __float_as_uint(v);
-            mx = fmaxf(mx, v);
-          }
-        } else {  // blocks past the prefix or outside the pool weigh nothing
-#pragma unroll
-          for (int x = 0; x < 128; ++x) {
-            const float v = (mask >> (x >> 4)) & 1 ? __uint_as_float(raw[x]) * A.qscale : -INFINITY;
-            raw[x] = __float_as_uint(v);
-            mx = fmaxf(mx, v);
-          }
+          for (int x = 0; x < 128; ++x)
+            if (!((mask >> (x >> 4)) & 1)) raw[x] = 0xff800000u;
         }
-        const bool move = mx > m + kMoveBy;
+        float mx4[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mx4[x] = __uint_as_float(raw[x]);
+#pragma unroll
+        for (int x = 4; x < 128; x += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)  // (one three-way maximum each)
+            mx4[y] = fmaxf(fmaxf(mx4[y], __uint_as_float(raw[x + y])), __uint_as_float(raw[(x + 4 + y) & 127]));
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * A.qscale;
+        const bool move = mx > m + kMoveBy;  // (a row of masked scores: -inf, or NaN at scale 0)
         if (__any_sync(0xffffffffu, move)) {
           const float mn = move ? mx : m;
           const float alpha = mn == m ? 1.f : fast_exp2(m - mn);
@@ -659,36 +681,42 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
           m = mn;
           if (j != j0) {  // O holds earlier chunks: their product is done (S came after it)
 #pragma unroll 1
-            for (int x = 0; x < 4; ++x) {
-              uint32_t o[32];
-              tmem_ld32(t_o + 32 * x, o);
+            for (int x = 0; x < 8; ++x) {
+              uint32_t o[16];
+              tmem_ld16(t_o + 16 * x, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
-              tmem_st32(t_o + 32 * x, o);
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
+              tmem_st16(t_o + 16 * x, o);
             }
           }
         }
         const float base = m == -INFINITY ? 0.f : m;
-        float sum = 0.f;
+        const float2 qs2 = make_float2(A.qscale, A.qscale), mb2 = make_float2(-base, -base);
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t hi[32], lo[32];
+        for (int x = 0; x < 4; ++x) {  // 32 tokens each
+          uint32_t hi[16], lo[kLo ? 16 : 1];
 #pragma unroll
-          for (int y = 0; y < 32; ++y) {
-            const float a = fast_exp2(__uint_as_float(raw[64 * x + 2 * y]) - base);
-            const float b = fast_exp2(__uint_as_float(raw[64 * x + 2 * y + 1]) - base);
-            sum += a + b;
-            hi[y] = pack_hi<kBf16>(a, b);
-            if (kLo) lo[y] = pack_lo<kBf16>(a, b);
+          for (int y = 0; y < 16; ++y) {
+            const int c = 32 * x + 2 * y;
+            float2 e = __ffma2_rn(make_float2(__uint_as_float(raw[c]), __uint_as_float(raw[c + 1])), qs2, mb2);
+            e.x = fast_exp2(e.x);
+            e.y = fast_exp2(e.y);
+            if (mask != 0xffu && !((mask >> (c >> 4)) & 1)) e = make_float2(0.f, 0.f);
+            sum = __fadd2_rn(sum, e);
+            hi[y] = pack_hi<kBf16>(e.x, e.y);
+            if constexpr (kLo) lo[y] = pack_lo<kBf16>(e.x, e.y);
           }
-          tmem_st32(t_s + 32 * x, hi);
-          if (kLo) tmem_st32(t_s + 64 + 32 * x, lo);
+          tmem_st16(t_s + 16 * x, hi);
+          if constexpr (kLo) tmem_st16(t_s + 64 + 16 * x, lo);
+          if (x & 1) {  // half the chunk's weights are there
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(smem_addr(&S.pfull[w][x >> 1]));
+          }
         }
-        l += sum;
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(smem_addr(&S.pfull[w]));
+        l += sum.x + sum.y;
       }
       n0 += nc;
       if (!ok) break;
@@ -726,87 +754,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
   if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// One warp per (sequence, query head): its own tokens' normalised output with
-// log2-sum-exp e, and its records of the prefix.
-__global__ void __launch_bounds__(256) shared_combine_kernel(const __grid_constant__ SharedArgs A, int ctas) {
-  const long long wid = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (wid >= static_cast<long long>(A.B) * A.Hq) return;
-  const int i = static_cast<int>(wid / A.Hq), hq = static_cast<int>(wid - static_cast<long long>(i) * A.Hq);
-  const int place = A.place[i];
-  float4 O = reinterpret_cast<const float4*>(A.o_s + wid * kHeadDim)[lane];
-  if (place >= 0) {
-    const GroupPlan g = load_plan(&A.plan[A.group_of[i]]);
-    const long long per = units_per_cta(A.plan[A.n_groups].unit0, ctas);
-    const int h = hq / A.G;
-    const int row = (place - g.member0) * A.G + (hq - h * A.G);
-    const int item = row / kItemRows, ir = row - item * kItemRows;
-    const int rows = g.rows - item * kItemRows;
-    const int sub = rows > kRows ? 1 : 2;  // half-records of a row
-    const long long seg = static_cast<long long>(item) * A.Hkv + h;
-    const long long u0 = g.unit0 + seg * g.chunks;
-    const long long c0 = u0 / per, c1 = (u0 + g.chunks - 1) / per;
-    const int count = static_cast<int>(c1 - c0 + 1) * sub;
-    const float* rec0 = A.rec + (static_cast<long long>(g.item0) * A.Hkv + seg + c0) * kRecFloats;
-    auto row_of = [&](int x) { return (x % sub) * kRows + ir; };
-    auto rec_of = [&](int x) { return rec0 + static_cast<long long>(x / sub) * kRecFloats; };
-    const float e = A.lse_s[wid];
-    float M = e, Ls = e > -INFINITY ? 1.f : 0.f;
-    if (!(e > -INFINITY)) O = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x0 = 0; x0 < count; x0 += 32) {
-      const int x = x0 + lane;
-      float mk = -INFINITY, lk = 0.f;
-      if (x < count) {
-        const float* t = rec_of(x) + kItemRows * kHeadDim + row_of(x);
-        mk = __ldcg(t);
-        lk = __ldcg(t + kItemRows);
-      }
-      float mx = mk;
-#pragma unroll
-      for (int msk = 1; msk < 32; msk <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, msk));
-      const float mn = fmaxf(M, mx);
-      if (mn == -INFINITY) continue;
-      const float a = M == mn ? 1.f : fast_exp2(M - mn);
-      const float wk = mk == -INFINITY ? 0.f : fast_exp2(mk - mn);
-      float lw = wk * lk;
-#pragma unroll
-      for (int msk = 1; msk < 32; msk <<= 1) lw += __shfl_xor_sync(0xffffffffu, lw, msk);
-      Ls = Ls * a + lw;
-      O.x *= a; O.y *= a; O.z *= a; O.w *= a;
-      M = mn;
-      const int n = count - x0 < 32 ? count - x0 : 32;
-      constexpr int RB = 8;
-      for (int b0 = 0; b0 < n; b0 += RB) {
-        float4 ob[RB];
-        float wb[RB];
-#pragma unroll
-        for (int b = 0; b < RB; ++b) {
-          wb[b] = __shfl_sync(0xffffffffu, wk, (b0 + b) & 31);
-          if (b0 + b >= n) wb[b] = 0.f;
-          ob[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (wb[b] != 0.f)  // (a record without tokens holds no output)
-            ob[b] = __ldcg(reinterpret_cast<const float4*>(rec_of(x0 + b0 + b) + row_of(x0 + b0 + b) * kHeadDim) + lane);
-        }
-#pragma unroll
-        for (int b = 0; b < RB; ++b) {
-          O.x = fmaf(wb[b], ob[b].x, O.x);
-          O.y = fmaf(wb[b], ob[b].y, O.y);
-          O.z = fmaf(wb[b], ob[b].z, O.z);
-          O.w = fmaf(wb[b], ob[b].w, O.w);
-        }
-      }
-    }
-    const float inv = Ls > 0.f ? 1.f / Ls : (Ls == 0.f ? 0.f : Ls);
-    O.x *= inv; O.y *= inv; O.z *= inv; O.w *= inv;
-  }
-  store_out4(A.out, wid * kHeadDim + 4 * lane, O.x, O.y, O.z, O.w, A.out_dtype);
-}
-
 // Workspace pieces, each 256-byte aligned.
 struct SharedLayout {
-  size_t plan, claims, bad, place, group_of, lens_s, offs_s, o_s, lse_s, dec, rec, total;
+  size_t plan, owner, bad, place, group_of, tiles, lens_s, offs_s, o_s, lse_s, dec, rec, total;
   size_t dec_bytes;
-  long long n_rec;
 };
 static bool shared_layout(const pa_pool* p, int B, int Hq, int max_blocks, int n_groups, SharedLayout* L) {
   if (!p || B <= 0 || Hq <= 0 || n_groups < 0 || max_blocks <= 0 || Hq % p->n_kv_heads) return false;
@@ -820,7 +771,7 @@ static bool shared_layout(const pa_pool* p, int B, int Hq, int max_blocks, int n
   // a sequence is in one group at most, so the groups have at most
   // n_groups + B G / 256 items; a piece more per CTA
   const long long items = n_groups ? n_groups + static_cast<long long>(B) * G / kItemRows : 0;
-  L->n_rec = items * p->n_kv_heads + sm_count(p->device);
+  const long long n_rec = items * p->n_kv_heads + sm_count(p->device);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -828,16 +779,17 @@ static bool shared_layout(const pa_pool* p, int B, int Hq, int max_blocks, int n
     return at;
   };
   L->plan = take(sizeof(GroupPlan) * (static_cast<size_t>(n_groups) + 1));
-  L->claims = take(4 * static_cast<size_t>(B));
+  L->owner = take(4 * static_cast<size_t>(B));
   L->bad = take(4 * static_cast<size_t>(n_groups));
   L->place = take(4 * static_cast<size_t>(B));
   L->group_of = take(4 * static_cast<size_t>(B));
+  L->tiles = take(8 * kPlanCluster);
   L->lens_s = take(4 * static_cast<size_t>(B));
   L->offs_s = take(4 * static_cast<size_t>(B));
   L->o_s = take(static_cast<size_t>(B) * Hq * kHeadDim * 4);
   L->lse_s = take(static_cast<size_t>(B) * Hq * 4);
   L->dec = take(L->dec_bytes);
-  L->rec = take(static_cast<size_t>(L->n_rec) * kRecFloats * 4);
+  L->rec = take(static_cast<size_t>(n_rec) * kRecFloats * 4);
   L->total = off;
   return true;
 }
@@ -845,13 +797,22 @@ static bool shared_layout(const pa_pool* p, int B, int Hq, int max_blocks, int n
 static size_t prefix_smem_bytes() { return sizeof(PrefixSmem) + 1024; }
 
 template <bool kBf16, bool kLo>
-static int launch_prefix(const SharedArgs& A, int grid, cudaStream_t st) {
+static int launch_prefix(const SharedArgs& A, cudaStream_t st) {
   const size_t bytes = prefix_smem_bytes();
   if (cudaFuncSetAttribute(shared_prefix_kernel<kBf16, kLo>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(bytes)) != cudaSuccess)
     return PA_ERR_CUDA;
-  shared_prefix_kernel<kBf16, kLo><<<grid, kPrefixThreads, bytes, st>>>(A);
-  return cuda_status(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(A.ctas));
+  cfg.blockDim = dim3(kPrefixThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_prefix_kernel<kBf16, kLo>, A) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace pa
@@ -900,38 +861,32 @@ int pa_decode_shared(pa_pool_t p, const void* q, const int32_t* block_tables, in
   A.max_blocks = max_blocks_per_seq;
   A.qscale = fabsf(scale) * kLog2eF;
   A.qflip = scale < 0.f ? 0x80008000u : 0u;
-  A.out = out;
-  A.out_dtype = out_dtype;
   A.plan = reinterpret_cast<GroupPlan*>(ws + L.plan);
-  A.claims = reinterpret_cast<int32_t*>(ws + L.claims);
+  A.owner = reinterpret_cast<int32_t*>(ws + L.owner);
+  A.tiles = reinterpret_cast<long long*>(ws + L.tiles);
   A.bad = reinterpret_cast<int32_t*>(ws + L.bad);
   A.place = reinterpret_cast<int32_t*>(ws + L.place);
   A.group_of = reinterpret_cast<int32_t*>(ws + L.group_of);
   A.lens_s = reinterpret_cast<int32_t*>(ws + L.lens_s);
   A.offs_s = reinterpret_cast<int32_t*>(ws + L.offs_s);
-  A.o_s = reinterpret_cast<float*>(ws + L.o_s);
-  A.lse_s = reinterpret_cast<float*>(ws + L.lse_s);
   A.rec = reinterpret_cast<float*>(ws + L.rec);
   A.num_blocks = p->num_blocks;
-  A.n_rec = L.n_rec;
+  A.ctas = sm_count(p->device);
   A.err = p->err;
   A.wait_limit_ns = wait_limit_ns();
   cudaStream_t st = as_stream(stream);
   shared_plan_kernel<<<kPlanCluster, kPlanThreads, 0, st>>>(A);
   if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
-  int rc = decode_own_tokens(p, q, block_tables, max_blocks_per_seq, A.lens_s, A.offs_s, num_seqs, n_q_heads, scale,
-                             A.o_s, A.lse_s, ws + L.dec, L.dec_bytes, stream);
-  if (rc != PA_OK) return rc;
-  const int ctas = sm_count(p->device);
   if (n_groups > 0) {
     const bool bf16 = p->dtype == PA_BF16, lo = out_dtype == PA_FP32;
-    rc = bf16 ? (lo ? launch_prefix<true, true>(A, ctas, st) : launch_prefix<true, false>(A, ctas, st))
-              : (lo ? launch_prefix<false, true>(A, ctas, st) : launch_prefix<false, false>(A, ctas, st));
+    const int rc = bf16 ? (lo ? launch_prefix<true, true>(A, st) : launch_prefix<true, false>(A, st))
+                        : (lo ? launch_prefix<false, true>(A, st) : launch_prefix<false, false>(A, st));
     if (rc != PA_OK) return rc;
   }
-  const long long warps = static_cast<long long>(num_seqs) * n_q_heads;
-  shared_combine_kernel<<<static_cast<unsigned>((warps * 32 + 255) / 256), 256, 0, st>>>(A, ctas);
-  return cuda_status(cudaGetLastError());
+  PrefixRecords X{A.place, A.group_of, A.plan, A.rec, n_groups};
+  return decode_own_and_combine(p, q, block_tables, max_blocks_per_seq, A.lens_s, A.offs_s, num_seqs, n_q_heads, scale,
+                                reinterpret_cast<float*>(ws + L.o_s), reinterpret_cast<float*>(ws + L.lse_s), out,
+                                out_dtype, X, ws + L.dec, L.dec_bytes, stream);
 }
 
 }  // extern "C"
