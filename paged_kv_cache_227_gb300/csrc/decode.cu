@@ -1471,9 +1471,9 @@ __global__ void __launch_bounds__(kMergeThreads, 8) combine_kernel(const __grid_
           lk = __ldcg(m + kItemRows);
         }
         R.add<4>(cnt, mk, lk, [&](int k) {
-          const float* o = reinterpret_cast<const float*>(recs.o(c0 + k)) + d0;
-          if (kFrag) return make_float4(__ldcg(o), __ldcg(o + 8), __ldcg(o + 16), __ldcg(o + 24));
-          return __ldcg(reinterpret_cast<const float4*>(o));
+          if (!kFrag) return __ldcg(recs.o(c0 + k, lane));
+          auto dim = [&](int d) { return __ldcg(reinterpret_cast<const float*>(recs.o(c0 + k, d >> 2)) + (d & 3)); };
+          return make_float4(dim(d0), dim(d0 + 8), dim(d0 + 16), dim(d0 + 24));
         });
       }
     }

@@ -43,6 +43,7 @@
 
 #include <cmath>
 #include <cstddef>
+#include <type_traits>
 
 #include "device_utils.cuh"
 #include "pa_internal.h"
@@ -252,11 +253,17 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
 // ---------------------------------------------------------------------------
 // tcgen05 helpers.
 // ---------------------------------------------------------------------------
-// Shared-memory operand descriptor, 128-byte swizzle: start address, leading
-// and stride byte offsets in 16-byte units, version 1, swizzle mode 2.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | static_cast<uint64_t>((lead >> 4) & 0x3fff) << 16 |
-         static_cast<uint64_t>((stride >> 4) & 0x3fff) << 32 | 1ull << 46 | 2ull << 61;
+// Shared-memory operand descriptor, 128-byte swizzle, as two words.  Low: start
+// address and leading byte offset; high: stride byte offset (8 rows, 1,024
+// bytes), version 1, swizzle mode 2; offsets in 16-byte units.  The issuing
+// thread adds constants to the low word only: an MMA takes 64 cycles, and
+// descriptors built anew for each one cost more than that to issue.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead) { return addr >> 4 | (lead >> 4) << 16; }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 // Instruction descriptor: fp32 accumulate, A and B of the pool's type, 128 x
 // 128; bit 16: B is MN-major.
@@ -264,18 +271,19 @@ __host__ __device__ constexpr uint32_t mma_desc(bool bf16, bool b_mn) {
   return 1u << 4 | (bf16 ? 1u : 0u) << 7 | (bf16 ? 1u : 0u) << 10 | (b_mn ? 1u : 0u) << 16 | (128u / 8) << 17 |
          (128u / 16) << 24;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(add), "r"(kDescHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(add), "r"(kDescHigh)
       : "memory");
 }
 // Arrives on the mbarrier when every MMA this thread issued so far is done.
@@ -402,6 +410,21 @@ struct SharedPieces {
   }
 };
 
+// Barrier of the 128 threads of warpgroup w.
+__device__ __forceinline__ void wg_sync(int w) { asm volatile("bar.sync %0, 128;" ::"r"(w + 1) : "memory"); }
+
+// The same, and whether `x` holds for all of them.
+__device__ __forceinline__ bool wg_all(int w, bool x) {
+  uint32_t y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(y)
+      : "r"(x ? 1u : 0u), "r"(w + 1)
+      : "memory");
+  return y != 0;
+}
+
 struct __align__(1024) PrefixSmem {
   uint8_t q[2][kTile];
   uint8_t k[kStages][kTile];
@@ -527,73 +550,93 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
     // ---- products.  Step t of a piece serves warpgroup t & 1; S of step
     // t + 2 is issued behind P V of step t, whose P it overwrites (the MMAs of
     // one thread run in order).
-    if (lane == 0) {
-      constexpr uint32_t kIdS = mma_desc(kBf16, false), kIdO = mma_desc(kBf16, true);
-      int n0 = 0;         // chunks of earlier pieces
-      int piece_no = 0;
-      uint32_t p_phase[2] = {0, 0};
-      bool ok = true;
-      while (ok && pieces.next(p)) {
-        const int nc = p.c1 - p.c0;
-        const int steps = p.both ? 2 * nc : nc;
-        ok = wait(S.qfull, piece_no & 1, 22);
-        ++piece_no;
-        bool first[2] = {true, true};
-        auto scores = [&](int t) {
-          const int w = t & 1, n = n0 + (p.both ? t >> 1 : t), s = n % kStages;
-          if (!p.both || w == 0) ok = ok && wait(S.kfull[s], (n / kStages) & 1, 23);
-          if (!ok) return;
-          tc_fence_after();
-          {
-            const uint32_t a = smem_addr(S.q[p.both ? w : 0]), b = smem_addr(S.k[s]);
+    // The whole warp runs the loop, so that its values stay uniform; one
+    // elected lane issues.
+    constexpr uint32_t kIdS = mma_desc(kBf16, false), kIdO = mma_desc(kBf16, true);
+    const bool leader = elect_one();
+    const uint32_t q_lo = desc_low(smem_addr(S.q[0]), 16), k_lo = desc_low(smem_addr(S.k[0]), 16),
+                   v_lo = desc_low(smem_addr(S.v[0]), kHalf);
+    int n0 = 0;         // chunks of earlier pieces
+    int piece_no = 0;
+    uint32_t p_phase = 0;  // bit w
+    bool ok = true;
+    auto all = [&](bool x) { return __all_sync(0xffffffffu, x); };
+    while (ok && pieces.next(p)) {
+      const int nc = p.c1 - p.c0;
+      const int steps = p.both ? 2 * nc : nc;
+      ok = all(wait(S.qfull, piece_no & 1, 22));
+      ++piece_no;
+      uint32_t begun = 0;  // bit w: O of w holds something
+      auto scores = [&](int t) {
+        const int w = t & 1, n = n0 + (p.both ? t >> 1 : t), s = n % kStages;
+        if (!p.both || w == 0) ok = ok && all(wait(S.kfull[s], (n / kStages) & 1, 23));
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t a = q_lo + (p.both ? w * (kTile >> 4) : 0), b = k_lo + s * (kTile >> 4), d = tmem + w * 128;
+        if (leader) {
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-              const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
-              mma_ss(tmem + w * 128, operand_desc(a + off, 16, 1024), operand_desc(b + off, 16, 1024), kIdS, ks > 0);
-            }
-            mma_commit(smem_addr(&S.sfull[w]));
-            if (!p.both || w == 1) mma_commit(smem_addr(&S.kfree[s]));
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+            mma_ss(d, a + off, b + off, kIdS, ks > 0);
           }
-        };
-        if (ok) scores(0);
-        if (ok && steps > 1) scores(1);
-        for (int t = 0; ok && t < steps; ++t) {
-          const int w = t & 1, n = n0 + (p.both ? t >> 1 : t), s = n % kStages;
-          ok = wait(S.pfull[w][0], p_phase[w], 24);
-          if (ok && (!p.both || w == 0)) ok = wait(S.vfull[s], (n / kStages) & 1, 25);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&S.mask[n % kMasks]);
-          const uint32_t b = smem_addr(S.v[s]);
-          bool add = !first[w];
-          auto values = [&](int kb0) {
-            for (int kb = kb0; kb < kb0 + kChunkBlocks / 2; ++kb) {
-              if (!((mask >> kb) & 1)) continue;
-              // 16 tokens: P's 8 columns, V's 16 rows; halves of the dims kHalf apart
-              const uint64_t bd = operand_desc(b + kb * (kBlock * 128), kHalf, 1024);
-              mma_ts(tmem + 256 + w * 128, tmem + w * 128 + kb * 8, bd, kIdO, add);
-              add = true;
-              if (kLo) mma_ts(tmem + 256 + w * 128, tmem + w * 128 + 64 + kb * 8, bd, kIdO, true);
+          mma_commit(smem_addr(&S.sfull[w]));
+          if (!p.both || w == 1) mma_commit(smem_addr(&S.kfree[s]));
+        }
+        __syncwarp();
+      };
+      if (ok) scores(0);
+      if (ok && steps > 1) scores(1);
+      for (int t = 0; ok && t < steps; ++t) {
+        const int w = t & 1, n = n0 + (p.both ? t >> 1 : t), s = n % kStages;
+        const uint32_t phase = (p_phase >> w) & 1;
+        p_phase ^= 1u << w;
+        ok = all(wait(S.pfull[w][0], phase, 24));
+        if (ok && (!p.both || w == 0)) ok = all(wait(S.vfull[s], (n / kStages) & 1, 25));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&S.mask[n % kMasks]);
+        const uint32_t b = v_lo + s * (kTile >> 4), d = tmem + 256 + w * 128, pw = tmem + w * 128;
+        // 16 tokens an MMA: P's 8 columns, V's 16 rows; halves of the dims kHalf apart
+        auto values = [&](auto half) {
+          constexpr int kb0 = decltype(half)::value * (kChunkBlocks / 2);
+          if (leader) {
+            if (mask == 0xffu) {
+#pragma unroll
+              for (int kb = kb0; kb < kb0 + kChunkBlocks / 2; ++kb) {
+                mma_ts(d, pw + kb * 8, b + kb * (kBlock * 128 >> 4), kIdO, kb > 0 ? 1u : (begun >> w) & 1);
+                if (kLo) mma_ts(d, pw + 64 + kb * 8, b + kb * (kBlock * 128 >> 4), kIdO, 1);
+              }
+            } else {
+              uint32_t add = (begun >> w) & 1 || (kb0 && (mask & 15));
+              for (int kb = kb0; kb < kb0 + kChunkBlocks / 2; ++kb) {
+                if (!((mask >> kb) & 1)) continue;
+                mma_ts(d, pw + kb * 8, b + kb * (kBlock * 128 >> 4), kIdO, add);
+                add = 1;
+                if (kLo) mma_ts(d, pw + 64 + kb * 8, b + kb * (kBlock * 128 >> 4), kIdO, 1);
+              }
             }
-          };
-          values(0);
-          ok = wait(S.pfull[w][1], p_phase[w], 29);
-          p_phase[w] ^= 1;
-          if (!ok) break;
-          tc_fence_after();
-          values(kChunkBlocks / 2);
+          }
+          __syncwarp();
+        };
+        values(std::integral_constant<int, 0>{});
+        ok = all(wait(S.pfull[w][1], phase, 29));
+        if (!ok) break;
+        tc_fence_after();
+        values(std::integral_constant<int, 1>{});
+        if (leader) {
           if (!p.both || w == 1) mma_commit(smem_addr(&S.vfree[s]));
           if (t + 2 >= steps) mma_commit(smem_addr(&S.ofull[w]));
-          if (mask) first[w] = false;
-          if (t + 2 < steps) scores(t + 2);
         }
-        n0 += nc;
+        __syncwarp();
+        if (mask) begun |= 1u << w;
+        if (t + 2 < steps) scores(t + 2);
       }
-      if (!ok) {  // wait for the products in flight before the TMEM goes
-        mma_commit(smem_addr(&S.drain));
-        const long long t0 = global_ns();
-        while (!mbar_try_wait(smem_addr(&S.drain), 0) && global_ns() - t0 < limit) {
-        }
+      n0 += nc;
+    }
+    if (!ok && leader) {  // wait for the products in flight before the TMEM goes
+      mma_commit(smem_addr(&S.drain));
+      const long long t0 = global_ns();
+      while (!mbar_try_wait(smem_addr(&S.drain), 0) && global_ns() - t0 < limit) {
       }
     }
     __syncwarp();
@@ -610,13 +653,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
       const int nc = p.c1 - p.c0;
       // Q: rows of this warpgroup, or half the rows of the common tile, once
       // both warpgroups are done with the piece before (its products with it)
-      if (piece_no > 0) {
-        ok = wait(S.qfree, (piece_no - 1) & 1, 28);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-      }
+      if (piece_no > 0) ok = __all_sync(0xffffffffu, wait(S.qfree, (piece_no - 1) & 1, 28));
       ++piece_no;
-      {
+      if (ok) {
         uint8_t* tile = S.q[p.both ? w : 0];
         const int per = p.both ? 1 : 2;  // threads a row
         const int row = p.both ? r : (w * 64 + (r >> 1));
@@ -647,7 +686,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
       const int step = p.both ? 1 : 2;
       const int j0 = p.both ? 0 : w;
       bool any = false;
-      for (int j = j0; j < nc; j += step) {
+      for (int j = j0; ok && j < nc; j += step) {
         ok = wait(S.sfull[w], s_phase, 26);
         s_phase ^= 1;
         ok = __all_sync(0xffffffffu, ok);
@@ -719,32 +758,51 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
         l += sum.x + sum.y;
       }
       n0 += nc;
+      if (ok && any) ok = __all_sync(0xffffffffu, wait(S.ofull[w], o_phase, 27));
+      if (any) o_phase ^= 1;
+      // a wait that ran out in one warp ends the warpgroup, which meets below
+      ok = wg_all(w, ok);
       if (!ok) break;
-      // ---- the piece's record
+      // ---- the piece's record: 64 dims of the warpgroup's rows at a time, by
+      // way of its Q tile (the common tile's halves when the rows are common),
+      // whose products are done, as one bulk copy of whole rows
       float* rec = A.rec + p.rec * kRecFloats;
-      const bool mine = p.both ? w * kRows + r < p.rows : r < p.rows;
-      if (any) {
-        ok = wait(S.ofull[w], o_phase, 27);
-        o_phase ^= 1;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-          uint32_t o[32];
-          tmem_ld32(t_o + 32 * x, o);
-          tmem_wait_ld();
-          if (mine) {
-            uint4* to = reinterpret_cast<uint4*>(rec + static_cast<long long>(w * kRows + r) * kHeadDim + 32 * x);
-#pragma unroll
-            for (int y = 0; y < 8; ++y) to[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-          }
-        }
-        tc_fence_before();
-      }
-      if (mine) {
+      const int rows = p.both && w ? p.rows - kRows : (p.rows < kRows ? p.rows : kRows);
+      if (r < rows) {
         rec[kItemRows * kHeadDim + w * kRows + r] = m;
         rec[kItemRows * kHeadDim + kItemRows + w * kRows + r] = l;
+      }
+      if (any) {
+        tc_fence_after();
+        uint8_t* tile = S.q[w];
+        float4* to = reinterpret_cast<float4*>(tile) + r * 16;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint32_t o[64];
+          tmem_ld32(t_o + 64 * half, o);
+          tmem_ld32(t_o + 64 * half + 32, o + 32);
+          tmem_wait_ld();
+          if (half) {  // the first half's copy has read the tile
+            if (r == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            wg_sync(w);
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            to[c ^ (r & 15)] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                                           __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          wg_sync(w);
+          if (r == 0) {
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                             rec + half * (kItemRows * 64) + w * (kRows * 64)),
+                         "r"(smem_addr(tile)), "r"(rows * 256)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        }
+        if (r == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        wg_sync(w);
+        tc_fence_before();
       }
       mbar_arrive(smem_addr(&S.qfree));
     }

@@ -10,7 +10,10 @@ namespace pa {
 
 constexpr int kRows = 128;                 // rows of a warpgroup
 constexpr int kItemRows = 2 * kRows;       // rows of an item
-// Record of a piece: o [256][128], m [256], l [256] (fp32; m in log2 units)
+// Record of a piece: o [2 halves of 64 dims][256 rows][64], m [256], l [256]
+// (fp32; m in log2 units).  A row's 16 vectors of 4 dims are stored in the order
+// c ^ (row & 15), which lets the writer's threads, a row each, go through
+// shared memory without bank conflicts.
 constexpr int kRecFloats = kItemRows * kHeadDim + 2 * kItemRows;
 
 // Plan of one group; entry [n_groups] holds the totals (unit0, item0, and in
@@ -75,8 +78,10 @@ struct RowRecords {
   __device__ const float* rec(int x) const { return rec0 + static_cast<long long>(sub == 2 ? x >> 1 : x) * kRecFloats; }
   __device__ int row_of(int x) const { return sub == 2 ? (x & 1) * kRows + row : row; }
   __device__ const float* m(int x) const { return rec(x) + kItemRows * kHeadDim + row_of(x); }  // l follows at + kItemRows
-  __device__ const float4* o(int x) const {
-    return reinterpret_cast<const float4*>(rec(x) + static_cast<long long>(row_of(x)) * kHeadDim);
+  // dims 4 c .. 4 c + 3
+  __device__ const float4* o(int x, int c) const {
+    const int r = row_of(x);
+    return reinterpret_cast<const float4*>(rec(x)) + ((c >> 4) * kItemRows + r) * 16 + ((c & 15) ^ (r & 15));
   }
 };
 
