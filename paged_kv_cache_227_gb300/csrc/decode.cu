@@ -1368,9 +1368,19 @@ __global__ void __launch_bounds__(kMergeThreads, (kExt && G > 8) ? 8 : 4) merge_
 struct Combined {
   float M = -INFINITY, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  // lane k: m and l of record k < n (n <= 32); o(k): this lane's dims of record k
-  template <int RB, typename Load>
-  __device__ __forceinline__ void add(int n, float mk, float lk, const Load& o) {
+  // n records (n <= 32): lane k passes m and l of record k; o(k) loads this
+  // lane's dims of record k < RB's round.  The first RB loads are issued before
+  // the weights are known (a record without tokens holds no output: it is
+  // read, and left out).
+  template <int RB, typename Load, typename Stat>
+  __device__ __forceinline__ void add(int n, const Stat& stat, const Load& o) {
+    const int lane = threadIdx.x & 31;
+    float mk = -INFINITY, lk = 0.f;
+    if (lane < n) stat(lane, mk, lk);
+    float4 ob[RB];
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+      if (r < n) ob[r] = o(r);
     float mx = mk;
 #pragma unroll
     for (int msk = 1; msk < 32; msk <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, msk));
@@ -1388,21 +1398,20 @@ struct Combined {
     O.w *= a;
     M = mn;
     for (int b0 = 0; b0 < n; b0 += RB) {
-      float4 ob[RB];
-      float w[RB];
+      if (b0) {
 #pragma unroll
-      for (int r = 0; r < RB; ++r) {
-        w[r] = __shfl_sync(0xffffffffu, wk, (b0 + r) & 31);
-        if (b0 + r >= n) w[r] = 0.f;
-        // (a record without tokens holds no output)
-        ob[r] = w[r] != 0.f ? o(b0 + r) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < RB; ++r)
+          if (b0 + r < n) ob[r] = o(b0 + r);
       }
 #pragma unroll
       for (int r = 0; r < RB; ++r) {
-        O.x = fmaf(w[r], ob[r].x, O.x);
-        O.y = fmaf(w[r], ob[r].y, O.y);
-        O.z = fmaf(w[r], ob[r].z, O.z);
-        O.w = fmaf(w[r], ob[r].w, O.w);
+        const float w = __shfl_sync(0xffffffffu, wk, (b0 + r) & 31);
+        if (b0 + r < n && w != 0.f) {
+          O.x = fmaf(w, ob[r].x, O.x);
+          O.y = fmaf(w, ob[r].y, O.y);
+          O.z = fmaf(w, ob[r].z, O.z);
+          O.w = fmaf(w, ob[r].w, O.w);
+        }
       }
     }
   }
@@ -1419,6 +1428,8 @@ __global__ void __launch_bounds__(kMergeThreads, 8) combine_kernel(const __grid_
   const long long wpb = kMergeThreads / 32;
   const long long n_items = static_cast<long long>(P.B) * P.Hkv * G;
   constexpr bool kFrag = G > 4;  // the decode's records are in fragment order
+  // lane's dims: 4 lane .. + 3, or in fragment order 32 (lane / 8) + lane % 8 + {0, 8, 16, 24}
+  const int d0 = kFrag ? 32 * (lane >> 3) + (lane & 7) : 4 * lane;
   bool waited = false;
   for (long long it = blockIdx.x * wpb + (threadIdx.x >> 5); it < n_items; it += gridDim.x * wpb) {
     const int g = static_cast<int>(it % G);
@@ -1427,56 +1438,47 @@ __global__ void __launch_bounds__(kMergeThreads, 8) combine_kernel(const __grid_
     const int i = static_cast<int>(sh / P.Hkv);
     const long long row = static_cast<long long>(i) * P.Hq + h * G + g;
     const int entry = C.X.n_groups ? __ldcg(&C.X.place[i]) : -1;
-    const bool own = mpfx[i + 1] != mpfx[i];
+    RowRecords shared;
+    if (entry >= 0) shared.find(C.X, entry, __ldcg(&C.X.group_of[i]), h, g, G, P.Hkv);
     Combined R;
-    // lane's dims: 4 lane .. + 3, or in fragment order 32 (lane / 8) + lane % 8 + {0, 8, 16, 24}
-    const int d0 = kFrag ? 32 * (lane >> 3) + (lane & 7) : 4 * lane;
     if (!waited) {
       asm volatile("griddepcontrol.wait;" ::: "memory");
       waited = true;
     }
-    if (own) {
+    if (mpfx[i + 1] != mpfx[i]) {
       const SegmentRecords recs(P, mpfx, i, h);
       if (recs.count <= 1) {  // a whole segment: the decode's normalised row
-        const float e = __ldcg(&P.lse[row]);
-        const float* o = static_cast<const float*>(P.out) + row * kHeadDim + d0;
-        R.add<1>(1, lane == 0 ? e : -INFINITY, 1.f, [&](int) {
+        R.template add<1>(1, [&](int, float& m, float& l) {
+          m = __ldcg(&P.lse[row]);
+          l = 1.f;
+        }, [&](int) {
+          const float* o = static_cast<const float*>(P.out) + row * kHeadDim + d0;
           if (kFrag) return make_float4(__ldcg(o), __ldcg(o + 8), __ldcg(o + 16), __ldcg(o + 24));
           return __ldcg(reinterpret_cast<const float4*>(o));
         });
       } else {
-        for (int c0 = 0; c0 < recs.count; c0 += 32) {
-          const int cnt = recs.count - c0 < 32 ? recs.count - c0 : 32;
-          float mk = -INFINITY, lk = 0.f;
-          if (lane < cnt) {
-            const float* rl = P.ws + recs.at(P, c0 + lane) * record_floats(G) + record_cols(G) * kHeadDim + g;
-            mk = __ldcg(rl);
-            lk = __ldcg(rl + 64);
-          }
-          R.add<4>(cnt, mk, lk, [&](int k) {
+        for (int c0 = 0; c0 < recs.count; c0 += 32)
+          R.template add<2>(recs.count - c0 < 32 ? recs.count - c0 : 32, [&](int k, float& m, float& l) {
+            const float* rl = P.ws + recs.at(P, c0 + k) * record_floats(G) + record_cols(G) * kHeadDim + g;
+            m = __ldcg(rl);
+            l = __ldcg(rl + 64);
+          }, [&](int k) {
             const float4* r4p = reinterpret_cast<const float4*>(P.ws + recs.at(P, c0 + k) * record_floats(G));
             return __ldcg(r4p + (kFrag ? frag_record_index(g, lane) : g * (kHeadDim / 4) + lane));
           });
-        }
       }
     }
-    if (entry >= 0) {
-      const RowRecords recs(C.X, entry, __ldcg(&C.X.group_of[i]), h, g, G, P.Hkv);
-      for (int c0 = 0; c0 < recs.count; c0 += 32) {
-        const int cnt = recs.count - c0 < 32 ? recs.count - c0 : 32;
-        float mk = -INFINITY, lk = 0.f;
-        if (lane < cnt) {
-          const float* m = recs.m(c0 + lane);
-          mk = __ldcg(m);
-          lk = __ldcg(m + kItemRows);
-        }
-        R.add<4>(cnt, mk, lk, [&](int k) {
-          if (!kFrag) return __ldcg(recs.o(c0 + k, lane));
-          auto dim = [&](int d) { return __ldcg(reinterpret_cast<const float*>(recs.o(c0 + k, d >> 2)) + (d & 3)); };
+    if (entry >= 0)
+      for (int c0 = 0; c0 < shared.count; c0 += 32)
+        R.template add<4>(shared.count - c0 < 32 ? shared.count - c0 : 32, [&](int k, float& m, float& l) {
+          const float* at = shared.m(c0 + k);
+          m = __ldcg(at);
+          l = __ldcg(at + kItemRows);
+        }, [&](int k) {
+          if (!kFrag) return __ldcg(shared.o(c0 + k, lane));
+          auto dim = [&](int d) { return __ldcg(reinterpret_cast<const float*>(shared.o(c0 + k, d >> 2)) + (d & 3)); };
           return make_float4(dim(d0), dim(d0 + 8), dim(d0 + 16), dim(d0 + 24));
         });
-      }
-    }
     const float inv = R.L == 0.f ? 0.f : 1.f / R.L;
     const long long at = row * kHeadDim + d0;
     if constexpr (kFrag) {

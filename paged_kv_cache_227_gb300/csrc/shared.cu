@@ -24,12 +24,13 @@
 //    units is cut into equal ranges, one a CTA, so any mix of groups fills
 //    the GPU; what a CTA holds of one segment is a piece, and leaves one
 //    record (m, l, unnormalised o of 256 rows).
-//  - two softmax warpgroups, one thread a row.  An item of more than 128 rows
-//    gives each its own 128 rows and both use every chunk; an item of at most
-//    128 rows gives both the same rows, and they take chunks in turn (two
-//    half-records of one row, joined like any others).  Either way the tensor
-//    cores work for one warpgroup while the other one exponentiates.
-//  - per chunk: S_w (128 x 128 fp32 in TMEM) = Q_w K^T; the warpgroup reads it
+//  - two teams of 256 softmax threads, two threads a row (64 tokens of a chunk
+//    each, the maxima exchanged through shared memory).  An item of more than
+//    128 rows gives each team its own 128 rows and both use every chunk; an
+//    item of at most 128 rows gives both the same rows, and they take chunks
+//    in turn (two half-records of one row, joined like any others).  Either
+//    way the tensor cores work for one team while the other one exponentiates.
+//  - per chunk: S_w (128 x 128 fp32 in TMEM) = Q_w K^T; the team reads it
 //    (tcgen05.ld), writes P over it as 16-bit values, and P_w V accumulates in
 //    TMEM.  K and V tiles arrive by TMA, block by block through the table, as
 //    [half][128 rows][128 bytes] with the 128-byte swizzle: K is the K-major
@@ -41,6 +42,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 #include <type_traits>
@@ -60,13 +62,18 @@ constexpr int kStages = 2;
 constexpr float kLog2eF = 1.4426950408889634f;
 constexpr float kMoveBy = 8.f;         // log2 units the maximum may lag behind
 
-constexpr int kPlanCluster = 8, kPlanThreads = 512;
-constexpr int kSoftWarps = 8;
+constexpr int kPlanCluster = 8, kPlanThreads = 512, kSmallThreads = 1024;
+constexpr int kSoftWarps = 16;
+constexpr int kTeam = 256;             // threads of a team: two a row
 constexpr int kPrefixThreads = (kSoftWarps + 2) * 32;  // + producer warp, + MMA warp
 constexpr int kMasks = 4;              // chunk masks in flight
 // The work of the two halves, in ns of one SM, to divide the SMs by: a chunk
-// of the product (two 128-row tiles), and a tile of 16 tokens of the decode.
-constexpr int kChunkNs = 1300, kTileNs = 130;
+// of the product with its share of a piece's start and record, and a tile of
+// 16 tokens of the decode of short sequences.  The division was swept from 4
+// to 152 SMs for the product: 64 chats of 2,048 + about 280 tokens are flat
+// within 16-32 (20 chosen), 16 multi-head sequences best at 64 (63 chosen),
+// 256 samples of a 16K document at 96 (92 chosen).
+constexpr int kChunkNs = 2600, kTileNs = 300;
 
 struct SharedArgs {
   CUtensorMap tmap;               // [K|V][half][rows][64] boxes of 16 rows x 64 elements
@@ -99,28 +106,40 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// One cluster: checks every group and lays out items and units.  A group that
-// breaks a rule, or names a sequence that is named twice, is reported and
-// takes no part; its members are decoded without it.
-__global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThreads) shared_plan_kernel(
-    const __grid_constant__ SharedArgs A) {
-  __shared__ long long s_tiles[kPlanThreads / 32];
-  constexpr int n_threads = kPlanCluster * kPlanThreads;
-  const int tid = blockIdx.x * kPlanThreads + threadIdx.x;
+// Checks every group and lays out items and units: CL CTAs of T threads (a
+// cluster, for the table comparisons of large batches; else one CTA, which
+// keeps its marks in shared memory).  A group that breaks a rule, or names a
+// sequence that is named twice, is reported and takes no part; its members
+// are decoded without it.
+constexpr int kSmallPlan = 512;  // sequences and groups of the one-CTA plan
+
+template <int CL, int T>
+__global__ void __launch_bounds__(T) shared_plan_kernel(const __grid_constant__ SharedArgs A) {
+  __shared__ long long s_tiles[T / 32];
+  __shared__ int s_owner[CL == 1 ? kSmallPlan : 1], s_group[CL == 1 ? kSmallPlan : 1], s_bad[CL == 1 ? kSmallPlan : 1];
+  int* const owner = CL == 1 ? s_owner : A.owner;
+  int* const group_of = CL == 1 ? s_group : A.group_of;
+  int* const bad = CL == 1 ? s_bad : A.bad;
+  auto sync = [] {
+    if (CL > 1) cluster_sync(); else __syncthreads();
+  };
+  auto get = [](const int* x) { return CL > 1 ? __ldcg(x) : *const_cast<const volatile int*>(x); };
+  constexpr int n_threads = CL * T;
+  const int tid = blockIdx.x * T + threadIdx.x;
   const int lane = threadIdx.x & 31;
   const int cap = A.max_blocks * kBlock;
   // the product launched as this grid's dependent waits for it to complete
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   long long tiles = 0;
   for (int i = tid; i < A.B; i += n_threads) {
-    A.owner[i] = 0;
+    owner[i] = 0;
     const int L = A.seq_lens[i];
     tiles += L > 0 ? ((L < cap ? L : cap) + kBlock - 1) / kBlock : 0;
   }
   // group_start runs from 0 to n_members and every group has a member, else
   // no group takes part (every CTA looks at all of it)
   int broken = 0;
-  for (int k = threadIdx.x; k < A.n_groups; k += kPlanThreads) {
+  for (int k = threadIdx.x; k < A.n_groups; k += T) {
     const int m0 = A.group_start[k], m1 = A.group_start[k + 1];
     broken |= m0 < 0 || m0 >= m1 || m1 > A.n_members || (k == 0 && m0 != 0) ||
               (k == A.n_groups - 1 && m1 != A.n_members);
@@ -128,14 +147,28 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
 #pragma unroll
   for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
   if (lane == 0) s_tiles[threadIdx.x >> 5] = tiles;
+  // (a member entry's loads start before the barrier)
+  const int e0 = tid >> 5;
+  int i0 = 0, first0 = 0;
+  if (e0 < A.n_members) {
+    i0 = A.members[e0];
+    first0 = A.members[0];
+  }
   broken = __syncthreads_or(broken);
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kPlanThreads / 32; ++w) tiles += s_tiles[w];
-    A.tiles[blockIdx.x] = tiles;
+  if (threadIdx.x < 32) {
+    long long sum = lane < T / 32 ? s_tiles[lane] : 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      if (CL > 1)
+        A.tiles[blockIdx.x] = sum;
+      else
+        s_tiles[0] = sum;
+    }
   }
   for (int k = tid; k < A.n_groups; k += n_threads) {
     const int P = A.prefix_blocks[k];
-    A.bad[k] = broken || P < 0 || P > A.max_blocks;
+    bad[k] = broken || P < 0 || P > A.max_blocks;
   }
   // a member entry's group: the last that starts at or before it
   auto group_at = [&](int e) {
@@ -146,21 +179,21 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
     }
     return lo;
   };
-  cluster_sync();
+  sync();
   // members: in range, named once, long enough, on the first member's blocks.
   // One warp an entry.
-  for (int e = tid >> 5; e < A.n_members; e += n_threads >> 5) {
+  for (int e = e0; e < A.n_members; e += n_threads >> 5) {
     const int k = group_at(e);
-    const int i = A.members[e];
+    const int i = e == e0 ? i0 : A.members[e];
     const bool in = i >= 0 && i < A.B;
     if (lane == 0 && in) {
-      const int before = atomicExch(&A.owner[i], e + 1);
-      if (before) A.bad[k] = A.bad[group_at(before - 1)] = 1;
-      A.group_of[i] = k;  // (either, when named twice: both groups are bad)
+      const int before = atomicExch(&owner[i], e + 1);
+      if (before) bad[k] = bad[group_at(before - 1)] = 1;
+      group_of[i] = k;  // (either, when named twice: both groups are bad)
     }
     const int m0 = A.group_start[k], P = A.prefix_blocks[k];
     if (broken || P < 0 || P > A.max_blocks) continue;
-    const int first = A.members[m0];
+    const int first = k == 0 ? first0 : A.members[m0];
     bool fine = in && first >= 0 && first < A.B;
     if (fine) {
       const int L = A.seq_lens[i];
@@ -180,13 +213,14 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
 #pragma unroll
           for (int y = 0; y < 8; ++y) other |= va[y] ^ vb[y];
         }
+#pragma unroll 4
         for (; x < P; x += 32) other |= a[x] ^ b[x];
       }
       fine = fine && other == 0;
     }
-    if (!__all_sync(0xffffffffu, fine) && lane == 0) A.bad[k] = 1;
+    if (!__all_sync(0xffffffffu, fine) && lane == 0) bad[k] = 1;
   }
-  cluster_sync();
+  sync();
   if (blockIdx.x == 0 && threadIdx.x < 32) {  // the groups' items and units, in group order
     int item = 0;
     long long unit = 0, shared_tiles = 0;
@@ -196,13 +230,13 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
       int items = 0;
       long long units = 0;
       if (k < A.n_groups) {
-        const bool bad = __ldcg(&A.bad[k]) != 0;
-        if (bad) record_error(A.err, PA_ERR_DEVICE_CHECK, k);
+        const bool out = get(&bad[k]) != 0;
+        if (out) record_error(A.err, PA_ERR_DEVICE_CHECK, k);
         g.member0 = A.group_start[k];
         g.blocks = A.prefix_blocks[k];
-        const int members = bad || g.blocks == 0 ? 0 : A.group_start[k + 1] - g.member0;
+        const int members = out || g.blocks == 0 ? 0 : A.group_start[k + 1] - g.member0;
         g.rows = members * A.G;
-        g.chunks = bad ? 0 : (g.blocks + kChunkBlocks - 1) / kChunkBlocks;
+        g.chunks = out ? 0 : (g.blocks + kChunkBlocks - 1) / kChunkBlocks;
         items = (g.rows + kItemRows - 1) / kItemRows;
         units = static_cast<long long>(items) * A.Hkv * g.chunks;
         shared_tiles += static_cast<long long>(members) * g.blocks;
@@ -224,7 +258,7 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
       item += __shfl_sync(0xffffffffu, ii, 31);
       unit += __shfl_sync(0xffffffffu, uu, 31);
     }
-    long long own = lane < kPlanCluster ? __ldcg(&A.tiles[lane]) : 0;
+    long long own = CL > 1 ? (lane < CL ? __ldcg(&A.tiles[lane]) : 0) : (lane == 0 ? s_tiles[0] : 0);
     own -= shared_tiles;
 #pragma unroll
     for (int o = 16; o; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
@@ -241,9 +275,10 @@ __global__ void __cluster_dims__(kPlanCluster, 1, 1) __launch_bounds__(kPlanThre
     }
   }
   for (int i = tid; i < A.B; i += n_threads) {
-    const int e = __ldcg(&A.owner[i]) - 1;
-    const int k = e >= 0 ? __ldcg(&A.group_of[i]) : 0;
-    const int P = e >= 0 && !__ldcg(&A.bad[k]) ? A.prefix_blocks[k] : 0;
+    const int e = get(&owner[i]) - 1;
+    const int k = e >= 0 ? get(&group_of[i]) : 0;
+    const int P = e >= 0 && !get(&bad[k]) ? A.prefix_blocks[k] : 0;
+    if (CL == 1) A.group_of[i] = k;
     A.place[i] = P > 0 ? e : -1;
     A.lens_s[i] = A.seq_lens[i] - P * kBlock;  // (a length out of range is the decode's to report)
     A.offs_s[i] = i * A.max_blocks + P;
@@ -333,6 +368,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -351,7 +391,7 @@ __device__ __forceinline__ void tma_load_half(uint32_t dst, const CUtensorMap* m
 // Pieces of one CTA: the cut of its unit range by segments.
 // ---------------------------------------------------------------------------
 struct SharedPiece {
-  int group, h;
+  int h;
   int row0, rows;      // the item's rows of the group
   int c0, c1;          // chunks
   int blocks;          // the group's prefix blocks
@@ -360,33 +400,47 @@ struct SharedPiece {
   bool both;           // more than 128 rows: every chunk for both warpgroups
 };
 
+// A warp's walk over its CTA's pieces.  It lives in shared memory, written by
+// lane 0: in registers it would push the softmax loop into spills, and with
+// 200 KB of shared memory a spill goes past L1.
 struct SharedPieces {
-  const SharedArgs& A;
   long long cur, end;
-  int cta, k;
   GroupPlan g;
+  int k, more;
+  SharedPiece p;
 
-  __device__ SharedPieces(const SharedArgs& a, int c) : A(a), cta(c) {
+  // All lanes call; the first piece is p when `more`.
+  __device__ void start(const SharedArgs& A, int cta) {
     const GroupPlan all = load_plan(&A.plan[A.n_groups]);
     const long long total = all.unit0, per = units_per_cta(total, all.rows);
-    cur = per * cta;
-    end = cur + per < total ? cur + per : total;
-    k = -1;
-    if (cur < end) {  // the last group that starts at or before cur (warp-wide)
-      const int lane = threadIdx.x & 31;
-      int count = 0;
+    const int lane = threadIdx.x & 31;
+    const long long from = per * cta;
+    int count = 0;
+    if (from < total) {  // the last group that starts at or before it (warp-wide)
       for (int k0 = 0; k0 < A.n_groups; k0 += 32) {
-        const bool before = k0 + lane < A.n_groups && __ldcg(&A.plan[k0 + lane].unit0) <= cur;
+        const bool before = k0 + lane < A.n_groups && __ldcg(&A.plan[k0 + lane].unit0) <= from;
         const int c = __popc(__ballot_sync(0xffffffffu, before));
         count += c;
         if (c < 32) break;
       }
-      k = count - 1;
-      g = load_plan(&A.plan[k]);
     }
+    if (lane == 0) {
+      cur = from;
+      end = from + per < total ? from + per : total;
+      k = count - 1;
+      if (count) g = load_plan(&A.plan[k]);
+      step(A, cta);
+    }
+    __syncwarp();
   }
-  __device__ bool next(SharedPiece& p) {
-    if (cur >= end) return false;
+  __device__ void next(const SharedArgs& A, int cta) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) step(A, cta);
+    __syncwarp();
+  }
+  __device__ void step(const SharedArgs& A, int cta) {
+    more = cur < end;
+    if (!more) return;
     auto units = [&] {
       return static_cast<long long>((g.rows + kItemRows - 1) / kItemRows) * A.Hkv * g.chunks;
     };
@@ -394,7 +448,6 @@ struct SharedPieces {
     const long long u = cur - g.unit0, seg_units = g.chunks;
     const long long seg = u / seg_units;
     const int item = static_cast<int>(seg / A.Hkv);
-    p.group = k;
     p.h = static_cast<int>(seg - static_cast<long long>(item) * A.Hkv);
     p.row0 = item * kItemRows;
     p.rows = g.rows - p.row0 < kItemRows ? g.rows - p.row0 : kItemRows;
@@ -406,21 +459,18 @@ struct SharedPieces {
     p.member0 = g.member0;
     p.rec = static_cast<long long>(g.item0) * A.Hkv + seg + cta;
     cur += p.c1 - p.c0;
-    return true;
   }
 };
 
-// Barrier of the 128 threads of warpgroup w.
-__device__ __forceinline__ void wg_sync(int w) { asm volatile("bar.sync %0, 128;" ::"r"(w + 1) : "memory"); }
-
-// The same, and whether `x` holds for all of them.
-__device__ __forceinline__ bool wg_all(int w, bool x) {
+// Barrier of the 256 threads of team w, and whether `x` holds for all of them.
+__device__ __forceinline__ void team_sync(int w) { asm volatile("bar.sync %0, 256;" ::"r"(w + 1) : "memory"); }
+__device__ __forceinline__ bool vote(int id, int threads, bool x) {
   uint32_t y;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\t"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(y)
-      : "r"(x ? 1u : 0u), "r"(w + 1)
+      : "r"(x ? 1u : 0u), "r"(id), "r"(threads)
       : "memory");
   return y != 0;
 }
@@ -431,6 +481,8 @@ struct __align__(1024) PrefixSmem {
   uint8_t v[kStages][kTile];
   unsigned long long kfull[kStages], kfree[kStages], vfull[kStages], vfree[kStages];
   unsigned long long qfull, qfree, sfull[2], pfull[2][2], ofull[2], drain;
+  SharedPieces pieces[kSoftWarps + 2];
+  float part[2][2][kRows];  // by team and half: a row's maximum, or its sum
   uint32_t mask[kMasks];  // blocks of the chunk that are there
   uint32_t tmem;
   int abort_flag;
@@ -450,8 +502,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
       mbar_init(smem_addr(&S.vfull[s]), 1);
       mbar_init(smem_addr(&S.vfree[s]), 1);
     }
-    mbar_init(smem_addr(&S.qfull), 2 * kRows);
-    mbar_init(smem_addr(&S.qfree), 2 * kRows);
+    mbar_init(smem_addr(&S.qfull), 2 * kTeam);
+    mbar_init(smem_addr(&S.qfree), 2 * kTeam);
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_addr(&S.sfull[w]), 1);
       mbar_init(smem_addr(&S.pfull[w][0]), kRows);
@@ -478,22 +530,24 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
   auto wait = [&](unsigned long long& bar, uint32_t parity, int site) {
     return wait_phase(smem_addr(&bar), parity, abort_flag, limit, A.err, site);
   };
-  SharedPieces pieces(A, blockIdx.x);
-  SharedPiece p;
+  volatile SharedPieces* const walk = &S.pieces[warp];
+  S.pieces[warp].start(A, blockIdx.x);
+  const volatile SharedPiece& p = walk->p;
 
   if (warp == kProducer) {
     // ---- loads: K and V of each chunk, lane 2b + half for block b
     int n = 0, nk = 0, nv = 0;  // chunks, K and V loads issued
     bool ok = true;
-    while (ok && pieces.next(p)) {
+    for (; ok && walk->more; S.pieces[warp].next(A, blockIdx.x)) {
+      const int c0 = p.c0, c1 = p.c1, blocks = p.blocks, h = p.h;
       const int32_t* row = A.tables + static_cast<long long>(A.members[p.member0]) * A.max_blocks;
       int blk = 0;
       auto fetch = [&](int c) {  // a chunk's block id, one chunk ahead
         const int b = c * kChunkBlocks + (lane >> 1);
-        return lane < 2 * kChunkBlocks && c < p.c1 && b < p.blocks ? row[b] : -2;
+        return lane < 2 * kChunkBlocks && c < c1 && b < blocks ? row[b] : -2;
       };
-      blk = fetch(p.c0);
-      for (int c = p.c0; c < p.c1; ++c, ++n) {
+      blk = fetch(c0);
+      for (int c = c0; c < c1; ++c, ++n) {
         const int s = n % kStages;
         const uint32_t use = static_cast<uint32_t>(n / kStages);
         const int ahead = fetch(c + 1);
@@ -503,7 +557,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
         uint32_t mask = 0;
 #pragma unroll
         for (int b = 0; b < kChunkBlocks; ++b) mask |= ((both >> (2 * b)) & 1u) << b;
-        const int y = static_cast<int>((static_cast<long long>(blk) * A.Hkv + p.h) * kBlock);
+        const int y = static_cast<int>((static_cast<long long>(blk) * A.Hkv + h) * kBlock);
         const uint32_t at = (lane & 1) * kHalf + (lane >> 1) * (kBlock * 128);
         const uint32_t bytes = __popc(mask) * kTileBytes;
         // (mask[n % 4] was last read for chunk n - 4, whose scores and values
@@ -561,18 +615,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
     uint32_t p_phase = 0;  // bit w
     bool ok = true;
     auto all = [&](bool x) { return __all_sync(0xffffffffu, x); };
-    while (ok && pieces.next(p)) {
+    for (; ok && walk->more; S.pieces[warp].next(A, blockIdx.x)) {
       const int nc = p.c1 - p.c0;
-      const int steps = p.both ? 2 * nc : nc;
+      const bool both = p.both;
+      const int steps = both ? 2 * nc : nc;
       ok = all(wait(S.qfull, piece_no & 1, 22));
       ++piece_no;
       uint32_t begun = 0;  // bit w: O of w holds something
       auto scores = [&](int t) {
-        const int w = t & 1, n = n0 + (p.both ? t >> 1 : t), s = n % kStages;
-        if (!p.both || w == 0) ok = ok && all(wait(S.kfull[s], (n / kStages) & 1, 23));
+        const int w = t & 1, n = n0 + (both ? t >> 1 : t), s = n % kStages;
+        if (!both || w == 0) ok = ok && all(wait(S.kfull[s], (n / kStages) & 1, 23));
         if (!ok) return;
         tc_fence_after();
-        const uint32_t a = q_lo + (p.both ? w * (kTile >> 4) : 0), b = k_lo + s * (kTile >> 4), d = tmem + w * 128;
+        const uint32_t a = q_lo + (both ? w * (kTile >> 4) : 0), b = k_lo + s * (kTile >> 4), d = tmem + w * 128;
         if (leader) {
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks) {
@@ -580,39 +635,40 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
             mma_ss(d, a + off, b + off, kIdS, ks > 0);
           }
           mma_commit(smem_addr(&S.sfull[w]));
-          if (!p.both || w == 1) mma_commit(smem_addr(&S.kfree[s]));
+          if (!both || w == 1) mma_commit(smem_addr(&S.kfree[s]));
         }
         __syncwarp();
       };
       if (ok) scores(0);
       if (ok && steps > 1) scores(1);
       for (int t = 0; ok && t < steps; ++t) {
-        const int w = t & 1, n = n0 + (p.both ? t >> 1 : t), s = n % kStages;
+        const int w = t & 1, n = n0 + (both ? t >> 1 : t), s = n % kStages;
         const uint32_t phase = (p_phase >> w) & 1;
         p_phase ^= 1u << w;
         ok = all(wait(S.pfull[w][0], phase, 24));
-        if (ok && (!p.both || w == 0)) ok = all(wait(S.vfull[s], (n / kStages) & 1, 25));
+        if (ok && (!both || w == 0)) ok = all(wait(S.vfull[s], (n / kStages) & 1, 25));
         if (!ok) break;
         tc_fence_after();
         const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&S.mask[n % kMasks]);
         const uint32_t b = v_lo + s * (kTile >> 4), d = tmem + 256 + w * 128, pw = tmem + w * 128;
-        // 16 tokens an MMA: P's 8 columns, V's 16 rows; halves of the dims kHalf apart
+        // 16 tokens an MMA: P's 8 columns (and 8 for the low halves), V's 16
+        // rows; halves of the dims kHalf apart
         auto values = [&](auto half) {
           constexpr int kb0 = decltype(half)::value * (kChunkBlocks / 2);
           if (leader) {
             if (mask == 0xffu) {
 #pragma unroll
               for (int kb = kb0; kb < kb0 + kChunkBlocks / 2; ++kb) {
-                mma_ts(d, pw + kb * 8, b + kb * (kBlock * 128 >> 4), kIdO, kb > 0 ? 1u : (begun >> w) & 1);
-                if (kLo) mma_ts(d, pw + 64 + kb * 8, b + kb * (kBlock * 128 >> 4), kIdO, 1);
+                mma_ts(d, pw + kb * 16, b + kb * (kBlock * 128 >> 4), kIdO, kb > 0 ? 1u : (begun >> w) & 1);
+                if (kLo) mma_ts(d, pw + kb * 16 + 8, b + kb * (kBlock * 128 >> 4), kIdO, 1);
               }
             } else {
               uint32_t add = (begun >> w) & 1 || (kb0 && (mask & 15));
               for (int kb = kb0; kb < kb0 + kChunkBlocks / 2; ++kb) {
                 if (!((mask >> kb) & 1)) continue;
-                mma_ts(d, pw + kb * 8, b + kb * (kBlock * 128 >> 4), kIdO, add);
+                mma_ts(d, pw + kb * 16, b + kb * (kBlock * 128 >> 4), kIdO, add);
                 add = 1;
-                if (kLo) mma_ts(d, pw + 64 + kb * 8, b + kb * (kBlock * 128 >> 4), kIdO, 1);
+                if (kLo) mma_ts(d, pw + kb * 16 + 8, b + kb * (kBlock * 128 >> 4), kIdO, 1);
               }
             }
           }
@@ -624,7 +680,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
         tc_fence_after();
         values(std::integral_constant<int, 1>{});
         if (leader) {
-          if (!p.both || w == 1) mma_commit(smem_addr(&S.vfree[s]));
+          if (!both || w == 1) mma_commit(smem_addr(&S.vfree[s]));
           if (t + 2 >= steps) mma_commit(smem_addr(&S.ofull[w]));
         }
         __syncwarp();
@@ -641,25 +697,27 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
     }
     __syncwarp();
   } else {
-    // ---- softmax: warpgroup w, one thread a row
-    const int w = warp >> 2;
-    const int r = threadIdx.x & (kRows - 1);
+    // ---- softmax: team w; row r, tokens 64 hh .. 64 hh + 63 of a chunk
+    const int w = warp >> 3, hh = (warp >> 2) & 1;
+    const int r = (warp & 3) * 32 + lane;
+    const int pair = 3 + (warp & 3) + 4 * w;  // barrier of the two warps of these rows
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lane_base + w * 128, t_o = tmem + lane_base + 256 + w * 128;
+    const uint32_t t_s = tmem + lane_base + w * 128, t_o = tmem + lane_base + 256 + w * 128 + 64 * hh;
     uint32_t s_phase = 0, o_phase = 0;
     int n0 = 0, piece_no = 0;
     bool ok = true;
-    while (ok && pieces.next(p)) {
+    for (; ok && walk->more; S.pieces[warp].next(A, blockIdx.x)) {
       const int nc = p.c1 - p.c0;
-      // Q: rows of this warpgroup, or half the rows of the common tile, once
-      // both warpgroups are done with the piece before (its products with it)
+      // Q: rows of this team, or half the rows of the common tile, once both
+      // teams are done with the piece before (its products with it)
       if (piece_no > 0) ok = __all_sync(0xffffffffu, wait(S.qfree, (piece_no - 1) & 1, 28));
       ++piece_no;
       if (ok) {
+        const int x = threadIdx.x & (kTeam - 1);
         uint8_t* tile = S.q[p.both ? w : 0];
-        const int per = p.both ? 1 : 2;  // threads a row
-        const int row = p.both ? r : (w * 64 + (r >> 1));
-        const int v0 = p.both ? 0 : (r & 1) * 8;
+        const int lg = p.both ? 1 : 2;  // log2 of the threads a row
+        const int row = (p.both ? 0 : w * 64) + (x >> lg);
+        const int per = 16 >> lg, v0 = (x & ((1 << lg) - 1)) * per;
         const int gr = p.row0 + (p.both ? w * kRows : 0) + row;
         const bool have = gr < p.row0 + p.rows;
         const uint4* src = nullptr;
@@ -668,9 +726,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
           src = reinterpret_cast<const uint4*>(
               A.q + (static_cast<long long>(i) * A.Hq + p.h * A.G + gr % A.G) * kHeadDim);
         }
-#pragma unroll 8
-        for (int x = 0; x < 16 / per; ++x) {
-          const int c = v0 + x;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          if (y >= per) break;
+          const int c = v0 + y;
           uint4 v = have ? src[c] : make_uint4(0u, 0u, 0u, 0u);
           v.x ^= A.qflip;
           v.y ^= A.qflip;
@@ -678,40 +737,47 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
           v.w ^= A.qflip;
           *reinterpret_cast<uint4*>(tile + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(smem_addr(&S.qfull));
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(smem_addr(&S.qfull));
 
       float m = -INFINITY, l = 0.f;
       const int step = p.both ? 1 : 2;
       const int j0 = p.both ? 0 : w;
       bool any = false;
       for (int j = j0; ok && j < nc; j += step) {
-        ok = wait(S.sfull[w], s_phase, 26);
+        ok = __all_sync(0xffffffffu, wait(S.sfull[w], s_phase, 26));
         s_phase ^= 1;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
         any = true;
         tc_fence_after();
-        const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&S.mask[(n0 + j) % kMasks]);
-        uint32_t raw[128];
+        uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&S.mask[(n0 + j) % kMasks]);
+        mask = (mask >> (4 * hh)) & 15;  // this half's blocks
+        float mine = -INFINITY;
+        if (ok) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) tmem_ld32(t_s + 32 * x, raw + 32 * x);
-        tmem_wait_ld();
-        if (mask != 0xffu) {  // blocks past the prefix or outside the pool weigh nothing
+          for (int x = 0; x < 2; ++x) {
+            uint32_t s[32];
+            tmem_ld32(t_s + 64 * hh + 32 * x, s);
+            tmem_wait_ld();
+            // (blocks past the prefix or outside the pool weigh nothing)
+            float m0 = -INFINITY, m1 = -INFINITY;
+            if ((mask >> (2 * x)) & 1) {
 #pragma unroll
-          for (int x = 0; x < 128; ++x)
-            if (!((mask >> (x >> 4)) & 1)) raw[x] = 0xff800000u;
+              for (int y = 0; y < 16; y += 2)  // (one three-way maximum)
+                m0 = fmaxf(fmaxf(m0, __uint_as_float(s[y])), __uint_as_float(s[y + 1]));
+            }
+            if ((mask >> (2 * x + 1)) & 1) {
+#pragma unroll
+              for (int y = 16; y < 32; y += 2) m1 = fmaxf(fmaxf(m1, __uint_as_float(s[y])), __uint_as_float(s[y + 1]));
+            }
+            mine = fmaxf(mine, fmaxf(m0, m1));
+          }
+          S.part[w][hh][r] = mine;
         }
-        float mx4[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) mx4[x] = __uint_as_float(raw[x]);
-#pragma unroll
-        for (int x = 4; x < 128; x += 8)
-#pragma unroll
-          for (int y = 0; y < 4; ++y)  // (one three-way maximum each)
-            mx4[y] = fmaxf(fmaxf(mx4[y], __uint_as_float(raw[x + y])), __uint_as_float(raw[(x + 4 + y) & 127]));
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * A.qscale;
+        // the row's other half; a wait that ran out in one of the two warps ends both
+        ok = vote(pair, 64, ok);
+        if (!ok) break;
+        const float mx = fmaxf(mine, S.part[w][hh ^ 1][r]) * A.qscale;
         const bool move = mx > m + kMoveBy;  // (a row of masked scores: -inf, or NaN at scale 0)
         if (__any_sync(0xffffffffu, move)) {
           const float mn = move ? mx : m;
@@ -720,7 +786,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
           m = mn;
           if (j != j0) {  // O holds earlier chunks: their product is done (S came after it)
 #pragma unroll 1
-            for (int x = 0; x < 8; ++x) {
+            for (int x = 0; x < 4; ++x) {
               uint32_t o[16];
               tmem_ld16(t_o + 16 * x, o);
               tmem_wait_ld();
@@ -733,79 +799,82 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
         const float base = m == -INFINITY ? 0.f : m;
         const float2 qs2 = make_float2(A.qscale, A.qscale), mb2 = make_float2(-base, -base);
         float2 sum = make_float2(0.f, 0.f);
+        // a block of 16 tokens at a time, read again; P over its columns of S:
+        // the high halves in the first 8, the low ones in the others
+        uint32_t s[2][16];
+        tmem_ld16(t_s + 64 * hh, s[0]);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {  // 32 tokens each
-          uint32_t hi[16], lo[kLo ? 16 : 1];
+        for (int x = 0; x < 4; ++x) {
+          uint32_t hi[8], lo[8];
+          tmem_wait_ld();
+          if (x < 3) tmem_ld16(t_s + 64 * hh + 16 * (x + 1), s[(x + 1) & 1]);
+          const bool there = (mask >> x) & 1;
 #pragma unroll
-          for (int y = 0; y < 16; ++y) {
-            const int c = 32 * x + 2 * y;
-            float2 e = __ffma2_rn(make_float2(__uint_as_float(raw[c]), __uint_as_float(raw[c + 1])), qs2, mb2);
-            e.x = fast_exp2(e.x);
-            e.y = fast_exp2(e.y);
-            if (mask != 0xffu && !((mask >> (c >> 4)) & 1)) e = make_float2(0.f, 0.f);
+          for (int y = 0; y < 8; ++y) {
+            const uint32_t* v = s[x & 1] + 2 * y;
+            float2 e = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), qs2, mb2);
+            e.x = there ? fast_exp2(e.x) : 0.f;
+            e.y = there ? fast_exp2(e.y) : 0.f;
             sum = __fadd2_rn(sum, e);
             hi[y] = pack_hi<kBf16>(e.x, e.y);
             if constexpr (kLo) lo[y] = pack_lo<kBf16>(e.x, e.y);
           }
-          tmem_st16(t_s + 16 * x, hi);
-          if constexpr (kLo) tmem_st16(t_s + 64 + 16 * x, lo);
-          if (x & 1) {  // half the chunk's weights are there
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(smem_addr(&S.pfull[w][x >> 1]));
-          }
+          tmem_st8(t_s + 64 * hh + 16 * x, hi);
+          if constexpr (kLo) tmem_st8(t_s + 64 * hh + 16 * x + 8, lo);
         }
         l += sum.x + sum.y;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_addr(&S.pfull[w][hh]));
       }
       n0 += nc;
       if (ok && any) ok = __all_sync(0xffffffffu, wait(S.ofull[w], o_phase, 27));
       if (any) o_phase ^= 1;
-      // a wait that ran out in one warp ends the warpgroup, which meets below
-      ok = wg_all(w, ok);
+      // a wait that ran out in one warp ends the team, which meets below
+      ok = vote(w + 1, kTeam, ok);
       if (!ok) break;
-      // ---- the piece's record: 64 dims of the warpgroup's rows at a time, by
-      // way of its Q tile (the common tile's halves when the rows are common),
-      // whose products are done, as one bulk copy of whole rows
+      // ---- the piece's record: 64 dims of the team's rows at a time, by way
+      // of its Q tile (whose products are done; the second team's is free when
+      // the tile is common), as one bulk copy of whole rows
       float* rec = A.rec + p.rec * kRecFloats;
       const int rows = p.both && w ? p.rows - kRows : (p.rows < kRows ? p.rows : kRows);
-      if (r < rows) {
-        rec[kItemRows * kHeadDim + w * kRows + r] = m;
-        rec[kItemRows * kHeadDim + kItemRows + w * kRows + r] = l;
-      }
-      if (any) {
-        tc_fence_after();
-        uint8_t* tile = S.q[w];
-        float4* to = reinterpret_cast<float4*>(tile) + r * 16;
+      if (hh) S.part[w][1][r] = l;
+      uint8_t* tile = S.q[w];
+      float4* to = reinterpret_cast<float4*>(tile) + r * 16;
+      tc_fence_after();
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint32_t o[64];
-          tmem_ld32(t_o + 64 * half, o);
-          tmem_ld32(t_o + 64 * half + 32, o + 32);
-          tmem_wait_ld();
-          if (half) {  // the first half's copy has read the tile
-            if (r == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            wg_sync(w);
-          }
+      for (int half = 0; half < 2; ++half) {
+        if (any && hh == half) {
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) {
+            uint32_t o[32];
+            tmem_ld32(t_o + 32 * x, o);
+            tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            to[c ^ (r & 15)] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                                           __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          wg_sync(w);
-          if (r == 0) {
-            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                             rec + half * (kItemRows * 64) + w * (kRows * 64)),
-                         "r"(smem_addr(tile)), "r"(rows * 256)
-                         : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            for (int c = 0; c < 8; ++c)
+              to[(8 * x + c) ^ (r & 15)] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                                                       __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
           }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        if (r == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        wg_sync(w);
-        tc_fence_before();
+        team_sync(w);
+        if (any && hh == 0 && r == 0) {
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                           rec + half * (kItemRows * 64) + w * (kRows * 64)),
+                       "r"(smem_addr(tile)), "r"(rows * 256)
+                       : "memory");
+          asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+        }
+        team_sync(w);  // the copy has read the tile
+      }
+      tc_fence_before();
+      if (hh == 0 && r < rows) {
+        rec[kItemRows * kHeadDim + w * kRows + r] = m;
+        rec[kItemRows * kHeadDim + kItemRows + w * kRows + r] = l + S.part[w][1][r];
       }
       mbar_arrive(smem_addr(&S.qfree));
     }
+    if (hh == 0 && r == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncthreads();
   tc_fence_after();
@@ -855,11 +924,16 @@ static bool shared_layout(const pa_pool* p, int B, int Hq, int max_blocks, int n
 static size_t prefix_smem_bytes() { return sizeof(PrefixSmem) + 1024; }
 
 template <bool kBf16, bool kLo>
-static int launch_prefix(const SharedArgs& A, cudaStream_t st) {
+static int launch_prefix(const SharedArgs& A, int device, cudaStream_t st) {
   const size_t bytes = prefix_smem_bytes();
-  if (cudaFuncSetAttribute(shared_prefix_kernel<kBf16, kLo>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(bytes)) != cudaSuccess)
-    return PA_ERR_CUDA;
+  static std::atomic<long long> ready{0};  // devices (below 64) whose attribute is set
+  const long long bit = device < 64 ? 1ll << device : 0;
+  if (!(ready.load() & bit)) {
+    if (cudaFuncSetAttribute(shared_prefix_kernel<kBf16, kLo>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(bytes)) != cudaSuccess)
+      return PA_ERR_CUDA;
+    ready |= bit;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(A.ctas));
   cfg.blockDim = dim3(kPrefixThreads);
@@ -933,12 +1007,28 @@ int pa_decode_shared(pa_pool_t p, const void* q, const int32_t* block_tables, in
   A.err = p->err;
   A.wait_limit_ns = wait_limit_ns();
   cudaStream_t st = as_stream(stream);
-  shared_plan_kernel<<<kPlanCluster, kPlanThreads, 0, st>>>(A);
+  // one CTA while its warps compare at most 32 K table entries (64 chats of
+  // 2,400 tokens: 5 us, against 8 us with the cluster)
+  if (num_seqs <= kSmallPlan && n_groups <= kSmallPlan && static_cast<long long>(n_members) * max_blocks_per_seq <= 32768) {
+    shared_plan_kernel<1, kSmallThreads><<<1, kSmallThreads, 0, st>>>(A);
+  } else {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kPlanCluster);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPlanCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, shared_plan_kernel<kPlanCluster, kPlanThreads>, A) != cudaSuccess) return PA_ERR_CUDA;
+  }
   if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
   if (n_groups > 0) {
     const bool bf16 = p->dtype == PA_BF16, lo = out_dtype == PA_FP32;
-    const int rc = bf16 ? (lo ? launch_prefix<true, true>(A, st) : launch_prefix<true, false>(A, st))
-                        : (lo ? launch_prefix<false, true>(A, st) : launch_prefix<false, false>(A, st));
+    const int rc = bf16 ? (lo ? launch_prefix<true, true>(A, p->device, st) : launch_prefix<true, false>(A, p->device, st))
+                        : (lo ? launch_prefix<false, true>(A, p->device, st) : launch_prefix<false, false>(A, p->device, st));
     if (rc != PA_OK) return rc;
   }
   PrefixRecords X{A.place, A.group_of, A.plan, A.rec, n_groups};

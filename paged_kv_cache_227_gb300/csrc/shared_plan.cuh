@@ -59,9 +59,9 @@ struct PrefixRecords {
 // The records of one query row: `count` of them (half-records of an item of
 // at most 128 rows count each).
 struct RowRecords {
-  const float* rec0;
-  int count, sub, row;
-  __device__ RowRecords(const PrefixRecords& X, int entry, int group, int h, int g, int G, int Hkv) {
+  const float* rec0 = nullptr;
+  int count = 0, sub = 1, row = 0;
+  __device__ void find(const PrefixRecords& X, int entry, int group, int h, int g, int G, int Hkv) {
     const GroupPlan p = load_plan(&X.plan[group]), total = load_plan(&X.plan[X.n_groups]);
     const long long per = units_per_cta(total.unit0, total.rows);
     const int r = (entry - p.member0) * G + g;
