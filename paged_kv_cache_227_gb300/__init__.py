@@ -343,12 +343,10 @@ def _at(pool, t, name, dtype):
     """Address of a contiguous `dtype` tensor on the pool's device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on the GPU")
+    if t.device != pool.device:
+        raise ValueError(f"{name} must be on the GPU, on the pool's device {pool.device}, got {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != pool.device:
-        raise ValueError(f"{name} must be on the pool's device {pool.device}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -398,12 +396,10 @@ def _heads(pool, t, name, n_tok, n_heads):
     heads; their address and token stride in elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on the GPU")
+    if t.device != pool.device:
+        raise ValueError(f"{name} must be on the GPU, on the pool's device {pool.device}, got {t.device}")
     if t.dtype != pool.dtype:
         raise TypeError(f"{name} must be {pool.dtype}, got {t.dtype}")
-    if t.device != pool.device:
-        raise ValueError(f"{name} must be on the pool's device {pool.device}, got {t.device}")
     if t.shape != (n_tok, n_heads, HEAD_DIM):
         raise ValueError(f"{name} must be [{n_tok}][{n_heads}][{HEAD_DIM}], got {tuple(t.shape)}")
     s = t.stride()

@@ -15,7 +15,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libpagedattn.so")
 OBJDIR = os.path.join(HERE, "_build")
 
-CU_SOURCES = ["pool.cu", "append.cu", "decode.cu", "rope.cu", "weights.cu", "evict.cu", "shared.cu"]
+CU_SOURCES = ["pool.cu", "append.cu", "decode.cu", "rope.cu", "evict.cu", "shared.cu"]
 CPP_SOURCES = ["alloc.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

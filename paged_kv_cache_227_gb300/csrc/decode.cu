@@ -94,6 +94,13 @@ struct CombineArgs {
   int out_dtype;
 };
 
+// Decode with attention-weight sums.
+struct WeightArgs {
+  float* weights;  // [B][Hkv][max_blocks * 16]
+  float decay;
+  int merge_ctas;  // CTAs of the second kernel that merge; the others sum
+};
+
 struct Params {
   CUtensorMap tmap_kv;      // tile view of the K|V allocation (see pa_pool)
   const uint16_t* q;        // [B][Hq][128]
@@ -126,6 +133,7 @@ struct Params {
   int lean_cost;            // LEAN: units counted ahead of each segment's tiles
   long long wait_limit_ns;
   int launch_flags;         // kLaunch* (host side; kLaunchSecondary also read by the kernel)
+  const WeightArgs* sums;      // host side: the score variant's sums
   const CombineArgs* combine;  // host side: combine with prefix records instead of the plain merge
 };
 
@@ -1260,12 +1268,9 @@ template <int N>
 struct RbTag {
   static constexpr int value = N;
 };
-// (16-column packed segments: short record lists and 3-4x the items, so
-// batches of 4 and 64 registers, 8 CTAs per SM: every item in one wave)
+// The merge items of CTA `block` of `blocks`.
 template <int G, bool kExt>
-__global__ void __launch_bounds__(kMergeThreads, (kExt && G > 8) ? 8 : 4) merge_kernel(const __grid_constant__ Params P) {
-  extern __shared__ int mpfx[];  // [B + 1]
-  block_prefix(P, mpfx, nullptr, false);
+__device__ __forceinline__ void merge_items(const Params& P, const int* mpfx, int block, int blocks) {
   const int lane = threadIdx.x & 31;
   const long long wpb = kMergeThreads / 32;
   const long long n_items = static_cast<long long>(P.B) * P.Hkv * G;
@@ -1273,7 +1278,7 @@ __global__ void __launch_bounds__(kMergeThreads, (kExt && G > 8) ? 8 : 4) merge_
   constexpr bool kFrag = kExt && G > 4;
   constexpr int RB = kExt && G > 8 ? 4 : 16;  // records whose o loads are in flight together (4 for short lists)
   bool waited = false;
-  for (long long it = blockIdx.x * wpb + (threadIdx.x >> 5); it < n_items; it += gridDim.x * wpb) {
+  for (long long it = block * wpb + (threadIdx.x >> 5); it < n_items; it += blocks * wpb) {
     const int g = static_cast<int>(it % G);
     const long long sh = it / G;
     const int h = static_cast<int>(sh % P.Hkv);
@@ -1357,6 +1362,117 @@ __global__ void __launch_bounds__(kMergeThreads, (kExt && G > 8) ? 8 : 4) merge_
       P.lse[static_cast<long long>(i) * P.Hq + h * G + g] = Ls > 0.f ? M + __log2f(Ls) : -INFINITY;
   }
   if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // completes after the decode grid
+}
+
+// (16-column packed segments: short record lists and 3-4x the items, so
+// batches of 4 and 64 registers, 8 CTAs per SM: every item in one wave)
+template <int G, bool kExt>
+__global__ void __launch_bounds__(kMergeThreads, (kExt && G > 8) ? 8 : 4) merge_kernel(const __grid_constant__ Params P) {
+  extern __shared__ int mpfx[];  // [B + 1]
+  block_prefix(P, mpfx, nullptr, false);
+  merge_items<G, kExt>(P, mpfx, blockIdx.x, gridDim.x);
+}
+
+// ---------------------------------------------------------------------------
+// The second half of pa_decode_weights: the merge, and beside it the sums.
+// The decode left every score s (scaled, log2 units) in the workspace; with a
+// query head's log2-sum-exp e the weight of cached token t is p = 2^(s - e), so
+//   weights[i][h][t] = decay * weights[i][h][t] + sum_g p_g,   t < L_i,
+// heads in order, one thread a token: no atomics.  e comes from the decode for
+// a whole segment, and from the records' m and l for a cut one, so the sums
+// need not wait for the merge (one dependent launch instead of two: 4
+// sequences of 8-32K tokens 72.7 -> 67.3 us).
+// Bound: memory (4 G + 8 bytes a token and kv head, against the decode's
+// 512); the scores were just written and come from L2.
+// ---------------------------------------------------------------------------
+constexpr int kSumTokens = 4;                            // tokens a thread
+constexpr int kSumChunk = kMergeThreads * kSumTokens;    // tokens a CTA and item
+
+template <int G>
+__global__ void __launch_bounds__(kMergeThreads, 4) weights_kernel(const __grid_constant__ Params P,
+                                                                   const WeightArgs W) {
+  extern __shared__ int mpfx[];  // [B + 1]
+  __shared__ float s_e[8];
+  block_prefix(P, mpfx, nullptr, false);
+  if (static_cast<int>(blockIdx.x) < W.merge_ctas) {
+    merge_items<G, false>(P, mpfx, blockIdx.x, W.merge_ctas);
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int span = P.max_blocks * kBlock;
+  const int chunks = (span + kSumChunk - 1) / kSumChunk;
+  const long long n_items = static_cast<long long>(P.B) * P.Hkv * chunks;
+  bool waited = false;
+  for (long long it = blockIdx.x - W.merge_ctas; it < n_items; it += gridDim.x - W.merge_ctas) {
+    const long long seg = it / chunks;
+    const int base = static_cast<int>(it - seg * chunks) * kSumChunk;
+    const int i = static_cast<int>(seg / P.Hkv), h = static_cast<int>(seg - static_cast<long long>(i) * P.Hkv);
+    int L = P.seq_lens[i];
+    L = L < 0 ? 0 : (L > span ? span : L);  // (the decode reports a length out of range)
+    if (base >= L) continue;
+    float* w = W.weights + seg * span;
+    float old[kSumTokens];
+#pragma unroll
+    for (int k = 0; k < kSumTokens; ++k) {
+      const int t = base + k * kMergeThreads + tid;
+      old[k] = t < L ? w[t] : 0.f;
+    }
+    if (!waited) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      waited = true;
+    }
+    const float* s = P.scores + seg * span * G;
+    float x[kSumTokens][G];
+#pragma unroll
+    for (int k = 0; k < kSumTokens; ++k) {
+      const long long t = base + k * kMergeThreads + tid;
+#pragma unroll
+      for (int g = 0; g < G; ++g) x[k][g] = t < L ? __ldcg(s + t * G + g) : -INFINITY;
+    }
+    const SegmentRecords recs(P, mpfx, i, h);
+    for (int g = wid; g < G; g += kMergeThreads / 32) {
+      float e;
+      if (recs.count <= 1) {
+        e = __ldcg(&P.lse[seg * G + g]);
+      } else {
+        float M = -INFINITY, Ls = 0.f;
+        for (int c0 = 0; c0 < recs.count; c0 += 32) {
+          float mk = -INFINITY, lk = 0.f;
+          if (c0 + lane < recs.count) {
+            const float* rl = P.ws + recs.at(P, c0 + lane) * record_floats(G) + record_cols(G) * kHeadDim + g;
+            mk = __ldcg(rl);
+            lk = __ldcg(rl + 64);
+          }
+          float mx = mk;
+#pragma unroll
+          for (int msk = 1; msk < 32; msk <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, msk));
+          const float mn = fmaxf(M, mx);
+          float lw = mk == -INFINITY ? 0.f : fast_exp2(mk - mn) * lk;
+#pragma unroll
+          for (int msk = 1; msk < 32; msk <<= 1) lw += __shfl_xor_sync(0xffffffffu, lw, msk);
+          Ls = (M == -INFINITY ? 0.f : Ls * fast_exp2(M - mn)) + lw;
+          M = mn;
+        }
+        e = Ls > 0.f ? M + log2f(Ls) : -INFINITY;
+      }
+      if (lane == 0) s_e[g] = e;
+    }
+    __syncthreads();
+    float e[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) e[g] = s_e[g];
+#pragma unroll
+    for (int k = 0; k < kSumTokens; ++k) {
+      const int t = base + k * kMergeThreads + tid;
+      float sum = 0.f;
+#pragma unroll
+      for (int g = 0; g < G; ++g)  // (a token whose block is out of range: -inf)
+        sum += x[k][g] == -INFINITY ? 0.f : exp2f(x[k][g] - e[g]);
+      if (t < L) w[t] = fmaf(W.decay, old[k], sum);
+    }
+    __syncthreads();  // s_e is read
+  }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -1848,7 +1964,14 @@ static int launch_typed(Params& P, int device, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if constexpr (kExt && G <= PA_MAX_GROUP) {
+    if constexpr (kScores) {
+      WeightArgs W = *P.sums;
+      W.merge_ctas = static_cast<int>(mgrid);
+      const long long chunks = (static_cast<long long>(P.max_blocks) * kBlock + kSumChunk - 1) / kSumChunk;
+      const long long items = chunks * P.B * P.Hkv;
+      cfg.gridDim = dim3(static_cast<unsigned>(mgrid + (items < mcap ? items : mcap)));
+      if (cudaLaunchKernelEx(&cfg, weights_kernel<G>, P, W) != cudaSuccess) return PA_ERR_CUDA;
+    } else if constexpr (kExt && G <= PA_MAX_GROUP) {
       if (P.combine) {
         if (cudaLaunchKernelEx(&cfg, combine_kernel<G>, P, *P.combine) != cudaSuccess) return PA_ERR_CUDA;
       } else if (cudaLaunchKernelEx(&cfg, merge_kernel<G, kExt>, P) != cudaSuccess) {
@@ -1913,7 +2036,7 @@ static int decode_common(pa_pool_t p, const void* q, const void* k_new, const vo
                          const int32_t* table_offs = nullptr, float* lse = nullptr,
                          const int32_t* ext_ntok = nullptr, int ext_g = 0, int launch_flags = 0,
                          const int32_t* ext_qbase = nullptr, int ext_hq = 0, float* scores = nullptr,
-                         const CombineArgs* combine = nullptr) {
+                         const WeightArgs* sums = nullptr, const CombineArgs* combine = nullptr) {
   if (!p || !q || !tables || !seq_lens || !out || B <= 0 || Hq <= 0 || max_blocks <= 0)
     return PA_ERR_INVALID;
   if (out_dtype != PA_FP16 && out_dtype != PA_BF16 && out_dtype != PA_FP32) return PA_ERR_INVALID;
@@ -1928,7 +2051,7 @@ static int decode_common(pa_pool_t p, const void* q, const void* k_new, const vo
     return PA_ERR_INVALID;
   if ((table_offs || lse) && (sched == SCHED_SEGMENT || fused)) return PA_ERR_INVALID;
   // (the score variant returns the log2-sum-exps that its scores go with)
-  if (scores && (table_offs || !lse)) return PA_ERR_INVALID;
+  if (scores && (table_offs || !lse || !sums)) return PA_ERR_INVALID;
   // packed tokens in q / out rows: ext_g columns each in the G, columns past the
   // last whole token empty (no log2-sum-exp out)
   if (ext_qbase && (!table_offs || !ext_ntok || lse || ext_g <= 0 || ext_g > G || ext_hq <= 0 ||
@@ -1958,6 +2081,7 @@ static int decode_common(pa_pool_t p, const void* q, const void* k_new, const vo
   P.ext_qbase = ext_qbase;
   P.ext_hq = ext_hq;
   P.scores = scores;
+  P.sums = sums;
   P.combine = combine;
   P.seq_lens = seq_lens;
   P.out = out;
@@ -2105,12 +2229,12 @@ int pa_decode_weights(pa_pool_t p, const void* q, const int32_t* block_tables, i
   char* ws = static_cast<char*>(workspace);
   float* scores = reinterpret_cast<float*>(ws + L.scores);
   float* lse = reinterpret_cast<float*>(ws + L.lse);
-  const int rc = decode_common(p, q, nullptr, nullptr, block_tables, max_blocks_per_seq, seq_lens, num_seqs,
-                               n_q_heads, scale, out, out_dtype, SCHED_LEAN, 0, ws + L.rec, L.total - L.rec, stream,
-                               nullptr, lse, nullptr, 0, 0, nullptr, 0, scores);
-  if (rc != PA_OK) return rc;
-  return launch_weight_sums(p, scores, lse, weights, decay, seq_lens, num_seqs, n_q_heads, max_blocks_per_seq,
-                            as_stream(stream));
+  WeightArgs W{};
+  W.weights = weights;
+  W.decay = decay;
+  return decode_common(p, q, nullptr, nullptr, block_tables, max_blocks_per_seq, seq_lens, num_seqs, n_q_heads, scale,
+                       out, out_dtype, SCHED_LEAN, 0, ws + L.rec, L.total - L.rec, stream, nullptr, lse, nullptr, 0, 0,
+                       nullptr, 0, scores, &W);
 }
 
 }  // extern "C"
@@ -2128,7 +2252,7 @@ int decode_own_and_combine(pa_pool* p, const void* q, const int32_t* tables, int
   // plan; without, it is the plan itself
   return decode_common(p, q, nullptr, nullptr, tables, max_blocks, lens, B, Hq, scale, o_s, PA_FP32, SCHED_LEAN, 0, ws,
                        ws_bytes, stream, table_offs, lse_s, nullptr, 0, X.n_groups ? kLaunchSecondary : kLaunchAfterPlan,
-                       nullptr, 0, nullptr, &C);
+                       nullptr, 0, nullptr, nullptr, &C);
 }
 
 }  // namespace pa

@@ -72,11 +72,6 @@ int launch_append_tail(void* k_pool, void* v_pool, int n_kv_heads, long long num
                        int device, const void* k_new, const void* v_new, const int32_t* tables,
                        int max_blocks, const int32_t* seq_lens, int B, cudaStream_t stream);
 
-// The second half of pa_decode_weights: adds the attention weights of the
-// decode's scores to the sums (weights.cu).
-int launch_weight_sums(const pa_pool* p, const float* scores, const float* lse, float* weights, float decay,
-                       const int32_t* seq_lens, int B, int Hq, int max_blocks, cudaStream_t stream);
-
 // The second half of pa_decode_shared (decode.cu): the split decode of each
 // sequence's lens[i] own tokens, whose table starts at element table_offs[i]
 // (both written by a kernel that is complete when the kernel before this call
