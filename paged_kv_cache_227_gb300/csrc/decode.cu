@@ -130,6 +130,8 @@ struct Params {
   int sched;
   int partition_blocks;     // PARTITION: tiles per partition
   int lean_units;           // LEAN: number of warps the ranges are cut for
+  const int* lean_taken;    // LEAN, shared-prefix decode: SMs that the prefix product holds, or null
+  int lean_sms;             // with lean_taken: SMs of the device
   int lean_cost;            // LEAN: units counted ahead of each segment's tiles
   long long wait_limit_ns;
   int launch_flags;         // kLaunch* (host side; kLaunchSecondary also read by the kernel)
@@ -285,9 +287,19 @@ __device__ __forceinline__ int clamp_len(const Params& P, int i) {
   return L;
 }
 
+// Warps that the ranges are cut for: all that fit the GPU, or those that fit
+// the SMs which the prefix product leaves (a range for an SM that it holds
+// would start when it ends).
+__device__ __forceinline__ int lean_units_of(const Params& P) {
+  if (!P.lean_taken) return P.lean_units;
+  const int taken = __ldcg(P.lean_taken);
+  return taken < P.lean_sms ? P.lean_units / P.lean_sms * (P.lean_sms - taken) : P.lean_units;
+}
+
 __device__ __forceinline__ long long lean_per(const Params& P, const int* pfx) {
-  const long long num = static_cast<long long>(P.Hkv) * pfx[P.B] + P.lean_units - 1;
-  const long long per = num < 0x7fffffffll ? static_cast<int>(num) / P.lean_units : num / P.lean_units;
+  const int lean_units = lean_units_of(P);
+  const long long num = static_cast<long long>(P.Hkv) * pfx[P.B] + lean_units - 1;
+  const long long per = num < 0x7fffffffll ? static_cast<int>(num) / lean_units : num / lean_units;
   return per < kLeanMinBlocks ? kLeanMinBlocks : per;
 }
 
@@ -403,11 +415,13 @@ struct PieceIter {
 struct SegmentRecords {
   long long c0, s0, per, base;
   int count;
-  __device__ SegmentRecords(const Params& P, const int* pfx, int i, int h) {
+  __device__ SegmentRecords(const Params& P, const int* pfx, int i, int h)
+      : SegmentRecords(P, pfx, i, h, P.sched == SCHED_LEAN ? lean_per(P, pfx) : 0) {}
+  __device__ SegmentRecords(const Params& P, const int* pfx, int i, int h, long long range) {
     if (P.sched == SCHED_LEAN) {
       const int cnt = pfx[i + 1] - pfx[i];
       const int nb = cnt - P.lean_cost;
-      per = lean_per(P, pfx);
+      per = range;
       s0 = static_cast<long long>(P.Hkv) * pfx[i] + static_cast<long long>(h) * cnt;  // segment's units start
       const long long rs = s0 + P.lean_cost;                                          // its tiles start
       const long long last = rs + nb - 1;
@@ -1481,30 +1495,36 @@ __global__ void __launch_bounds__(kMergeThreads, 4) weights_kernel(const __grid_
 // log-sum-exp.  One warp per (sequence, query head); a lane holds 4 dims.  The
 // o loads of up to RB records are in flight together.
 // ---------------------------------------------------------------------------
-struct Combined {
-  float M = -INFINITY, L = 0.f;
-  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  // n records (n <= 32): lane k passes m and l of record k; o(k) loads this
-  // lane's dims of record k < RB's round.  The first RB loads are issued before
-  // the weights are known (a record without tokens holds no output: it is
-  // read, and left out).
-  template <int RB, typename Load, typename Stat>
-  __device__ __forceinline__ void add(int n, const Stat& stat, const Load& o) {
+template <int RB>
+struct Batch {  // the first up to 32 records of a list: their m and l, a lane each, and RB of their o
+  float mk = -INFINITY, lk = 0.f;
+  float4 ob[RB];
+  template <typename Stat, typename Load>
+  __device__ __forceinline__ void load(int n, const Stat& stat, const Load& o) {
     const int lane = threadIdx.x & 31;
-    float mk = -INFINITY, lk = 0.f;
+    mk = -INFINITY;
+    lk = 0.f;
     if (lane < n) stat(lane, mk, lk);
-    float4 ob[RB];
 #pragma unroll
     for (int r = 0; r < RB; ++r)
       if (r < n) ob[r] = o(r);
-    float mx = mk;
+  }
+};
+struct Combined {
+  float M = -INFINITY, L = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  // n loaded records (n <= 32); a record without tokens holds no output: it
+  // was read, and is left out
+  template <int RB, typename Load>
+  __device__ __forceinline__ void add(int n, Batch<RB>& b, const Load& o) {
+    float mx = b.mk;
 #pragma unroll
     for (int msk = 1; msk < 32; msk <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, msk));
     const float mn = fmaxf(M, mx);
     if (mn == -INFINITY) return;  // no token in any record so far
     const float a = M == mn ? 1.f : fast_exp2(M - mn);
-    const float wk = mk == -INFINITY ? 0.f : fast_exp2(mk - mn);
-    float lw = wk * lk;
+    const float wk = b.mk == -INFINITY ? 0.f : fast_exp2(b.mk - mn);
+    float lw = wk * b.lk;
 #pragma unroll
     for (int msk = 1; msk < 32; msk <<= 1) lw += __shfl_xor_sync(0xffffffffu, lw, msk);
     L = L * a + lw;
@@ -1517,16 +1537,16 @@ struct Combined {
       if (b0) {
 #pragma unroll
         for (int r = 0; r < RB; ++r)
-          if (b0 + r < n) ob[r] = o(b0 + r);
+          if (b0 + r < n) b.ob[r] = o(b0 + r);
       }
 #pragma unroll
       for (int r = 0; r < RB; ++r) {
         const float w = __shfl_sync(0xffffffffu, wk, (b0 + r) & 31);
         if (b0 + r < n && w != 0.f) {
-          O.x = fmaf(w, ob[r].x, O.x);
-          O.y = fmaf(w, ob[r].y, O.y);
-          O.z = fmaf(w, ob[r].z, O.z);
-          O.w = fmaf(w, ob[r].w, O.w);
+          O.x = fmaf(w, b.ob[r].x, O.x);
+          O.y = fmaf(w, b.ob[r].y, O.y);
+          O.z = fmaf(w, b.ob[r].z, O.z);
+          O.w = fmaf(w, b.ob[r].w, O.w);
         }
       }
     }
@@ -1546,6 +1566,9 @@ __global__ void __launch_bounds__(kMergeThreads, 8) combine_kernel(const __grid_
   constexpr bool kFrag = G > 4;  // the decode's records are in fragment order
   // lane's dims: 4 lane .. + 3, or in fragment order 32 (lane / 8) + lane % 8 + {0, 8, 16, 24}
   const int d0 = kFrag ? 32 * (lane >> 3) + (lane & 7) : 4 * lane;
+  const long long per = lean_per(P, mpfx);
+  GroupPlan total{};
+  if (C.X.n_groups) total = load_plan(&C.X.plan[C.X.n_groups]);
   bool waited = false;
   for (long long it = blockIdx.x * wpb + (threadIdx.x >> 5); it < n_items; it += gridDim.x * wpb) {
     const int g = static_cast<int>(it % G);
@@ -1553,48 +1576,66 @@ __global__ void __launch_bounds__(kMergeThreads, 8) combine_kernel(const __grid_
     const int h = static_cast<int>(sh % P.Hkv);
     const int i = static_cast<int>(sh / P.Hkv);
     const long long row = static_cast<long long>(i) * P.Hq + h * G + g;
+    // all that the index math needs is complete before the wait
     const int entry = C.X.n_groups ? __ldcg(&C.X.place[i]) : -1;
     RowRecords shared;
-    if (entry >= 0) shared.find(C.X, entry, __ldcg(&C.X.group_of[i]), h, g, G, P.Hkv);
+    if (entry >= 0) shared.find(C.X, entry, __ldcg(&C.X.group_of[i]), h, g, G, P.Hkv, total);
+    const bool own = mpfx[i + 1] != mpfx[i];
+    const SegmentRecords recs(P, mpfx, i, h, per);
     Combined R;
     if (!waited) {
       asm volatile("griddepcontrol.wait;" ::: "memory");
       waited = true;
     }
-    if (mpfx[i + 1] != mpfx[i]) {
-      const SegmentRecords recs(P, mpfx, i, h);
-      if (recs.count <= 1) {  // a whole segment: the decode's normalised row
-        R.template add<1>(1, [&](int, float& m, float& l) {
-          m = __ldcg(&P.lse[row]);
-          l = 1.f;
-        }, [&](int) {
+    // both lists' first loads go out together
+    const int n_own = own ? (recs.count < 1 ? 1 : recs.count) : 0;
+    const bool whole = n_own == 1;  // a whole segment: the decode's normalised row
+    auto own_stat = [&](int c0) {
+      return [&, c0](int k, float& m, float& l) {
+        const float* rl = P.ws + recs.at(P, c0 + k) * record_floats(G) + record_cols(G) * kHeadDim + g;
+        m = whole ? __ldcg(&P.lse[row]) : __ldcg(rl);
+        l = whole ? 1.f : __ldcg(rl + 64);
+      };
+    };
+    auto own_load = [&](int c0) {
+      return [&, c0](int k) {
+        if (whole) {
           const float* o = static_cast<const float*>(P.out) + row * kHeadDim + d0;
           if (kFrag) return make_float4(__ldcg(o), __ldcg(o + 8), __ldcg(o + 16), __ldcg(o + 24));
           return __ldcg(reinterpret_cast<const float4*>(o));
-        });
-      } else {
-        for (int c0 = 0; c0 < recs.count; c0 += 32)
-          R.template add<2>(recs.count - c0 < 32 ? recs.count - c0 : 32, [&](int k, float& m, float& l) {
-            const float* rl = P.ws + recs.at(P, c0 + k) * record_floats(G) + record_cols(G) * kHeadDim + g;
-            m = __ldcg(rl);
-            l = __ldcg(rl + 64);
-          }, [&](int k) {
-            const float4* r4p = reinterpret_cast<const float4*>(P.ws + recs.at(P, c0 + k) * record_floats(G));
-            return __ldcg(r4p + (kFrag ? frag_record_index(g, lane) : g * (kHeadDim / 4) + lane));
-          });
-      }
+        }
+        const float4* r4p = reinterpret_cast<const float4*>(P.ws + recs.at(P, c0 + k) * record_floats(G));
+        return __ldcg(r4p + (kFrag ? frag_record_index(g, lane) : g * (kHeadDim / 4) + lane));
+      };
+    };
+    auto pre_stat = [&](int c0) {
+      return [&, c0](int k, float& m, float& l) {
+        const float* at = shared.m(c0 + k);
+        m = __ldcg(at);
+        l = __ldcg(at + kItemRows);
+      };
+    };
+    auto pre_load = [&](int c0) {
+      return [&, c0](int k) {
+        if (!kFrag) return __ldcg(shared.o(c0 + k, lane));
+        auto dim = [&](int d) { return __ldcg(reinterpret_cast<const float*>(shared.o(c0 + k, d >> 2)) + (d & 3)); };
+        return make_float4(dim(d0), dim(d0 + 8), dim(d0 + 16), dim(d0 + 24));
+      };
+    };
+    auto at_most = [](int n) { return n < 32 ? n : 32; };
+    Batch<2> b_own;
+    Batch<4> b_pre;
+    if (entry >= 0) b_pre.load(at_most(shared.count), pre_stat(0), pre_load(0));
+    if (own) b_own.load(at_most(n_own), own_stat(0), own_load(0));
+    for (int c0 = 0; c0 < n_own; c0 += 32) {
+      if (c0) b_own.load(at_most(n_own - c0), own_stat(c0), own_load(c0));
+      R.add(at_most(n_own - c0), b_own, own_load(c0));
     }
     if (entry >= 0)
-      for (int c0 = 0; c0 < shared.count; c0 += 32)
-        R.template add<4>(shared.count - c0 < 32 ? shared.count - c0 : 32, [&](int k, float& m, float& l) {
-          const float* at = shared.m(c0 + k);
-          m = __ldcg(at);
-          l = __ldcg(at + kItemRows);
-        }, [&](int k) {
-          if (!kFrag) return __ldcg(shared.o(c0 + k, lane));
-          auto dim = [&](int d) { return __ldcg(reinterpret_cast<const float*>(shared.o(c0 + k, d >> 2)) + (d & 3)); };
-          return make_float4(dim(d0), dim(d0 + 8), dim(d0 + 16), dim(d0 + 24));
-        });
+      for (int c0 = 0; c0 < shared.count; c0 += 32) {
+        if (c0) b_pre.load(at_most(shared.count - c0), pre_stat(c0), pre_load(c0));
+        R.add(at_most(shared.count - c0), b_pre, pre_load(c0));
+      }
     const float inv = R.L == 0.f ? 0.f : 1.f / R.L;
     const long long at = row * kHeadDim + d0;
     if constexpr (kFrag) {
@@ -2083,6 +2124,10 @@ static int decode_common(pa_pool_t p, const void* q, const void* k_new, const vo
   P.scores = scores;
   P.sums = sums;
   P.combine = combine;
+  if (combine && combine->X.n_groups > 0) {
+    P.lean_taken = &combine->X.plan[combine->X.n_groups].rows;
+    P.lean_sms = sm_count(p->device);
+  }
   P.seq_lens = seq_lens;
   P.out = out;
   P.ws = static_cast<float*>(ws);

@@ -550,15 +550,9 @@ extern "C" int pa_evict(pa_pool_t p, const float* weights, float* weights_out, c
   if (span <= 256 * 8) e = launch_select<256, 8, 1>(A, st);
   else if (span <= 256 * 16) e = launch_select<256, 16, 1>(A, st);
   else if (span <= 512 * 16) e = launch_select<512, 16, 1>(A, st);
-  else if (span <= 512 * 16 * 8) {
-    // CTAs of a row: enough for its tokens, and more while two a SM are not
-    // reached (32 rows of up to 32K tokens: 8 CTAs each, not 4)
-    int cl = 2;
-    while (512 * 16 * cl < span) cl *= 2;
-    while (cl < 8 && 2ll * cl * A.Hkv * num_seqs <= 2 * sm_count(p->device)) cl *= 2;
-    e = cl == 2 ? launch_select<512, 16, 2>(A, st)
-                : (cl == 4 ? launch_select<512, 16, 4>(A, st) : launch_select<512, 16, 8>(A, st));
-  }
+  else if (span <= 512 * 16 * 2) e = launch_select<512, 16, 2>(A, st);
+  else if (span <= 512 * 16 * 4) e = launch_select<512, 16, 4>(A, st);
+  else if (span <= 512 * 16 * 8) e = launch_select<512, 16, 8>(A, st);
   else evict_select_long_kernel<<<dim3(A.Hkv, A.B), 1024, 0, st>>>(A);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
   // CTAs of a row group: about 4,096 in all (64 sequences of 8 heads: 4 each,

@@ -62,18 +62,17 @@ constexpr int kStages = 2;
 constexpr float kLog2eF = 1.4426950408889634f;
 constexpr float kMoveBy = 8.f;         // log2 units the maximum may lag behind
 
-constexpr int kPlanCluster = 8, kPlanThreads = 512, kSmallThreads = 1024;
+constexpr int kPlanCluster = 8, kPlanThreads = 1024, kSmallThreads = 1024;
 constexpr int kSoftWarps = 16;
 constexpr int kTeam = 256;             // threads of a team: two a row
 constexpr int kPrefixThreads = (kSoftWarps + 2) * 32;  // + producer warp, + MMA warp
 constexpr int kMasks = 4;              // chunk masks in flight
-// The work of the two halves, in ns of one SM, to divide the SMs by: a chunk
-// of the product with its share of a piece's start and record, and a tile of
-// 16 tokens of the decode of short sequences.  The division was swept from 4
-// to 152 SMs for the product: 64 chats of 2,048 + about 280 tokens are flat
-// within 16-32 (20 chosen), 16 multi-head sequences best at 64 (63 chosen),
-// 256 samples of a 16K document at 96 (92 chosen).
-constexpr int kChunkNs = 2600, kTileNs = 300;
+// Estimates, in ns, to divide the SMs by: a chunk of the product on its SM, a
+// CTA's start and records; a tile of 16 tokens of the decode on one SM, and its
+// start.  Measured on 64 chats of 2,048 + about 280 tokens, 16 multi-head
+// sequences of two prompts, and 256 samples of a 16K document (a chunk 1.8 us,
+// a piece 10 us; tiles 0.16-0.22 us).
+constexpr float kChunkNs = 1800.f, kPieceNs = 12000.f, kTileNs = 200.f, kDecodeNs = 4000.f;
 
 struct SharedArgs {
   CUtensorMap tmap;               // [K|V][half][rows][64] boxes of 16 rows x 64 elements
@@ -203,17 +202,16 @@ __global__ void __launch_bounds__(T) shared_plan_kernel(const __grid_constant__ 
       int other = 0;
       if (i != first) {
         int x = lane;
-        for (; x + 7 * 32 < P; x += 8 * 32) {  // 16 loads in flight
-          int va[8], vb[8];
-#pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            va[y] = a[x + 32 * y];
-            vb[y] = b[x + 32 * y];
-          }
-#pragma unroll
-          for (int y = 0; y < 8; ++y) other |= va[y] ^ vb[y];
-        }
+        if (A.max_blocks % 4 == 0 && reinterpret_cast<uintptr_t>(A.tables) % 16 == 0) {  // 4 entries a load
+          const int4 *a4 = reinterpret_cast<const int4*>(a), *b4 = reinterpret_cast<const int4*>(b);
 #pragma unroll 4
+          for (int y = lane; y < P / 4; y += 32) {
+            const int4 u = a4[y], v = b4[y];
+            other |= (u.x ^ v.x) | (u.y ^ v.y) | (u.z ^ v.z) | (u.w ^ v.w);
+          }
+          x += P / 4 * 4;
+        }
+#pragma unroll 8
         for (; x < P; x += 32) other |= a[x] ^ b[x];
       }
       fine = fine && other == 0;
@@ -262,15 +260,33 @@ __global__ void __launch_bounds__(T) shared_plan_kernel(const __grid_constant__ 
     own -= shared_tiles;
 #pragma unroll
     for (int o = 16; o; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
+    // SMs of the product: those with which the later of the two halves ends
+    // first; or all of them, and the decode after it
+    const float product = static_cast<float>(unit) * kChunkNs, decode = static_cast<float>(own) * A.Hkv * kTileNs;
+    float best = 3e38f;
+    int best_n = A.ctas;
+    for (int n = 1 + lane; n <= A.ctas; n += 32) {
+      const float x = product / n + kPieceNs, y = decode / (A.ctas - n) + kDecodeNs;
+      const float time = n < A.ctas ? fmaxf(x, y) : x + decode / n + kDecodeNs;
+      if (time < best) {
+        best = time;
+        best_n = n;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const float t = __shfl_xor_sync(0xffffffffu, best, o);
+      const int n = __shfl_xor_sync(0xffffffffu, best_n, o);
+      if (t < best || (t == best && n < best_n)) {
+        best = t;
+        best_n = n;
+      }
+    }
     if (lane == 0) {
       GroupPlan g{};
       g.unit0 = unit;
       g.item0 = item;
-      // SMs of the product: its share of the work
-      const float a = static_cast<float>(unit) * kChunkNs, b = static_cast<float>(own) * A.Hkv * kTileNs;
-      int n = unit ? static_cast<int>(A.ctas * (a / (a + b)) + 0.5f) : 0;
-      n = n < 1 ? 1 : (n > A.ctas ? A.ctas : n);
-      g.rows = unit < n ? static_cast<int>(unit) : n;
+      g.rows = unit < best_n ? static_cast<int>(unit) : best_n;
       A.plan[A.n_groups] = g;
     }
   }
@@ -541,12 +557,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
     for (; ok && walk->more; S.pieces[warp].next(A, blockIdx.x)) {
       const int c0 = p.c0, c1 = p.c1, blocks = p.blocks, h = p.h;
       const int32_t* row = A.tables + static_cast<long long>(A.members[p.member0]) * A.max_blocks;
-      int blk = 0;
-      auto fetch = [&](int c) {  // a chunk's block id, one chunk ahead
+      auto fetch = [&](int c) {  // a chunk's block id
         const int b = c * kChunkBlocks + (lane >> 1);
         return lane < 2 * kChunkBlocks && c < c1 && b < blocks ? row[b] : -2;
       };
-      blk = fetch(c0);
+      int blk = fetch(c0);
       for (int c = c0; c < c1; ++c, ++n) {
         const int s = n % kStages;
         const uint32_t use = static_cast<uint32_t>(n / kStages);
@@ -645,11 +660,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
         const int w = t & 1, n = n0 + (both ? t >> 1 : t), s = n % kStages;
         const uint32_t phase = (p_phase >> w) & 1;
         p_phase ^= 1u << w;
-        ok = all(wait(S.pfull[w][0], phase, 24));
-        if (ok && (!both || w == 0)) ok = all(wait(S.vfull[s], (n / kStages) & 1, 25));
+        // (V first: it came long ago, and what follows P's arrival is on the
+        // way of the next products)
+        if (!both || w == 0) ok = wait(S.vfull[s], (n / kStages) & 1, 25);
+        const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&S.mask[n % kMasks]);
+        ok = all(ok && wait(S.pfull[w][0], phase, 24));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&S.mask[n % kMasks]);
         const uint32_t b = v_lo + s * (kTile >> 4), d = tmem + 256 + w * 128, pw = tmem + w * 128;
         // 16 tokens an MMA: P's 8 columns (and 8 for the low halves), V's 16
         // rows; halves of the dims kHalf apart

@@ -61,8 +61,9 @@ struct PrefixRecords {
 struct RowRecords {
   const float* rec0 = nullptr;
   int count = 0, sub = 1, row = 0;
-  __device__ void find(const PrefixRecords& X, int entry, int group, int h, int g, int G, int Hkv) {
-    const GroupPlan p = load_plan(&X.plan[group]), total = load_plan(&X.plan[X.n_groups]);
+  __device__ void find(const PrefixRecords& X, int entry, int group, int h, int g, int G, int Hkv,
+                       const GroupPlan& total) {
+    const GroupPlan p = load_plan(&X.plan[group]);
     const long long per = units_per_cta(total.unit0, total.rows);
     const int r = (entry - p.member0) * G + g;
     const int item = r / kItemRows;
