@@ -95,31 +95,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
   const int v0 = turn && !A.interleaved ? j : 2 * j;
   const int v1 = turn && !A.interleaved ? j + A.half_vecs : 2 * j + 1;
 
-  long long slot = A.slots[t];
-  const bool to_cache = slot >= 0 && slot < A.num_slots;
-  if (slot >= A.num_slots && lane == 0) record_error(A.err, PA_ERR_DEVICE_CHECK, slot);
-
+  // every row is loaded before the slot is known; a token that keeps out of
+  // the cache just does not store its K and V
+  const long long slot = A.slots[t];
   uint4 x[U][2];
-  uint4* dst[U];
   const int r0 = chunk * 4 * U + sub;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int r = r0 + 4 * u;
-    dst[u] = nullptr;
     if (r >= rows) continue;
-    const uint4* src;
-    if (r < A.Hq) {
-      src = reinterpret_cast<const uint4*>(A.q + t * A.q_stride + r * kHeadDim);
-      dst[u] = reinterpret_cast<uint4*>(A.q_out + t * A.q_out_stride + r * kHeadDim);
-    } else {
-      if (!to_cache) continue;
-      const bool is_v = r >= A.Hq + A.Hkv;
-      const int h = is_v ? r - A.Hq - A.Hkv : r - A.Hq;
-      src = is_v ? reinterpret_cast<const uint4*>(A.v + t * A.v_stride + h * kHeadDim)
-                 : reinterpret_cast<const uint4*>(A.k + t * A.k_stride + h * kHeadDim);
-      const long long row = ((slot >> 4) * A.Hkv + h) * kBlock + (slot & 15);
-      dst[u] = reinterpret_cast<uint4*>((is_v ? A.v_pool : A.k_pool) + row * kHeadDim);
-    }
+    const int h = r < A.Hq ? r : (r < A.Hq + A.Hkv ? r - A.Hq : r - A.Hq - A.Hkv);
+    const uint16_t* base = r < A.Hq ? A.q + t * A.q_stride
+                                    : (r < A.Hq + A.Hkv ? A.k + t * A.k_stride : A.v + t * A.v_stride);
+    const uint4* src = reinterpret_cast<const uint4*>(base + h * kHeadDim);
     x[u][0] = src[v0];
     x[u][1] = src[v1];
   }
@@ -142,12 +130,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     for (int e = 0; e < 8; ++e) cs[e] = s_cs[wib][8 * j + e];
   }
 
+  const bool to_cache = slot >= 0 && slot < A.num_slots;
+  if (slot >= A.num_slots && lane == 0) record_error(A.err, PA_ERR_DEVICE_CHECK, slot);
+  const long long row = (slot >> 4) * A.Hkv * kBlock + (slot & 15);  // of kv head 0
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    if (!dst[u]) continue;
+    const int r = r0 + 4 * u;
+    if (r >= rows || (r >= A.Hq && !to_cache)) continue;
+    uint16_t* to = r < A.Hq ? A.q_out + t * A.q_out_stride + r * kHeadDim
+                            : (r < A.Hq + A.Hkv ? A.k_pool + (row + (r - A.Hq) * kBlock) * kHeadDim
+                                                : A.v_pool + (row + (r - A.Hq - A.Hkv) * kBlock) * kHeadDim);
+    uint4* dst = reinterpret_cast<uint4*>(to);
     uint32_t a[4] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w};
     uint32_t b[4] = {x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
-    if (turn && r0 + 4 * u < A.Hq + A.Hkv) {
+    if (turn && r < A.Hq + A.Hkv) {
       if (A.interleaved) {  // word k of vector e holds pair 8j + 4e + k
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -166,8 +162,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
         }
       }
     }
-    dst[u][v0] = make_uint4(a[0], a[1], a[2], a[3]);
-    dst[u][v1] = make_uint4(b[0], b[1], b[2], b[3]);
+    dst[v0] = make_uint4(a[0], a[1], a[2], a[3]);
+    dst[v1] = make_uint4(b[0], b[1], b[2], b[3]);
   }
 }
 
@@ -234,8 +230,8 @@ extern "C" int pa_rope_append(pa_pool_t p, const void* q, int64_t q_stride, int 
   A.interleaved = interleaved != 0;
   A.err = p->err;
   // rows a warp: 4 while that leaves the GPU partly empty (64 tokens of 48 heads:
-  // 2.9 us, against 3.3 with 12), then 12, which share a token's angles
-  // (8,192 tokens of 48 heads: 37.2 us, against 53.4 with 4 and 38.6 with 16)
+  // 2.8 us, against 3.1 with 12), then 12, which share a token's angles
+  // (8,192 tokens of 48 heads: 35.8 us, against 56.2 with 4 and 36.5 with 16)
   const long long quads = A.n_tok * ((A.Hq + 2 * A.Hkv + 3) / 4);
   if (quads <= 32ll * sm_count(p->device))
     launch_rope<1>(A, p->dtype == PA_BF16, as_stream(stream));
