@@ -142,8 +142,9 @@ int pa_cache_append(pa_pool_t pool, const void* k_new, const void* v_new,
  *                  still turned.
  * Pointers are 16-byte aligned and strides multiples of 8 elements that hold
  * a token's heads (else INVALID).  rot_dim is a multiple of 16 up to 128, 1 <=
- * n_axes <= PA_MAX_ROPE_AXES, n_q_heads <= PA_MAX_ROPE_HEADS (else
- * UNSUPPORTED).  Arithmetic is fp32, rounded once to the pool's type.
+ * n_axes <= PA_MAX_ROPE_AXES, n_q_heads <= PA_MAX_ROPE_HEADS, and the rows
+ * fit one launch (2^31 blocks of 16 rows or more: else UNSUPPORTED).  Tokens
+ * that name one slot race, as for pa_cache_append.  Arithmetic is fp32, rounded once to the pool's type.
  * n_tok == 0 is a no-op. */
 enum { PA_MAX_ROPE_AXES = 4, PA_MAX_ROPE_HEADS = 65536 };
 int pa_rope_append(pa_pool_t pool, const void* q, int64_t q_stride, int n_q_heads, const void* k_new,
@@ -301,8 +302,10 @@ int pa_decode_cascade(pa_pool_t pool, const void* q, const int32_t* block_tables
  * out they are carried as a high and a low half (2^-17).  The result does not
  * depend on timing.
  * num_seqs and n_groups <= 4096 (else UNSUPPORTED); n_members <= num_seqs,
- * num_seqs * max_blocks_per_seq < 2^31 (else INVALID).  workspace: device, >=
- * pa_decode_shared_workspace_bytes(...), 256-byte aligned, caller-owned. */
+ * num_seqs * max_blocks_per_seq < 2^31, a finite scale (else INVALID).
+ * workspace: device, >= pa_decode_shared_workspace_bytes(...), 256-byte
+ * aligned, caller-owned; its contents on entry do not matter, and calls that
+ * share one must not overlap on the GPU. */
 size_t pa_decode_shared_workspace_bytes(pa_pool_t pool, int num_seqs, int n_q_heads,
                                         int max_blocks_per_seq, int n_groups);
 int pa_decode_shared(pa_pool_t pool, const void* q, const int32_t* block_tables,
@@ -324,8 +327,9 @@ int pa_decode_shared(pa_pool_t pool, const void* q, const int32_t* block_tables,
  * A position whose block id is out of range counts as not attended (reported
  * by pa_check).  workspace: device, >= pa_decode_weights_workspace_bytes(...),
  * 256-byte aligned, caller-owned; it holds the scores (4 bytes a query head
- * and table position) and the split's records.  num_seqs <= 4096 (else
- * UNSUPPORTED). */
+ * and table position) and the split's records; its contents on entry do not
+ * matter, and calls that share one must not overlap on the GPU.  num_seqs <=
+ * 4096 (else UNSUPPORTED). */
 size_t pa_decode_weights_workspace_bytes(pa_pool_t pool, int num_seqs, int n_q_heads,
                                          int max_blocks_per_seq);
 int pa_decode_weights(pa_pool_t pool, const void* q, const int32_t* block_tables,

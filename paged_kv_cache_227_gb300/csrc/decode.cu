@@ -1480,8 +1480,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) weights_kernel(const __grid_
       const int t = base + k * kMergeThreads + tid;
       float sum = 0.f;
 #pragma unroll
-      for (int g = 0; g < G; ++g)  // (a token whose block is out of range: -inf)
-        sum += x[k][g] == -INFINITY ? 0.f : exp2f(x[k][g] - e[g]);
+      for (int g = 0; g < G; ++g)  // (a token whose block is out of range: -inf; a sum that is NaN has no e)
+        sum += x[k][g] == -INFINITY ? 0.f : (e[g] == -INFINITY ? NAN : exp2f(x[k][g] - e[g]));
       if (t < L) w[t] = fmaf(W.decay, old[k], sum);
     }
     __syncthreads();  // s_e is read
@@ -1514,13 +1514,15 @@ struct Combined {
   float M = -INFINITY, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
   // n loaded records (n <= 32); a record without tokens holds no output: it
-  // was read, and is left out
+  // was read, and is left out.  A sum that is NaN makes the row NaN, whatever
+  // the maxima say (they pass NaN over).
   template <int RB, typename Load>
   __device__ __forceinline__ void add(int n, Batch<RB>& b, const Load& o) {
     float mx = b.mk;
 #pragma unroll
     for (int msk = 1; msk < 32; msk <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, msk));
     const float mn = fmaxf(M, mx);
+    if (__any_sync(0xffffffffu, isnan(b.lk))) L = NAN;
     if (mn == -INFINITY) return;  // no token in any record so far
     const float a = M == mn ? 1.f : fast_exp2(M - mn);
     const float wk = b.mk == -INFINITY ? 0.f : fast_exp2(b.mk - mn);
@@ -1636,6 +1638,12 @@ __global__ void __launch_bounds__(kMergeThreads, 8) combine_kernel(const __grid_
         if (c0) b_pre.load(at_most(shared.count - c0), pre_stat(c0), pre_load(c0));
         R.add(at_most(shared.count - c0), b_pre, pre_load(c0));
       }
+    if (whole && R.M == -INFINITY) {  // the decode saw nothing but NaN, or no block in range (zeros)
+      R.O.x += 0.f * b_own.ob[0].x;
+      R.O.y += 0.f * b_own.ob[0].y;
+      R.O.z += 0.f * b_own.ob[0].z;
+      R.O.w += 0.f * b_own.ob[0].w;
+    }
     const float inv = R.L == 0.f ? 0.f : 1.f / R.L;
     const long long at = row * kHeadDim + d0;
     if constexpr (kFrag) {

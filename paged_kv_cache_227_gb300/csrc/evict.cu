@@ -157,6 +157,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
   const EvictRow R(A, blockIdx.y, h, rank == 0 && tid == 0);
   const int used = (R.L + 32 * NW * CL - 1) / (32 * NW * CL);  // tokens a thread, at most K
   const int t0 = (rank * NW + wid) * 32 * used + lane;         // token of bit k: t0 + 32 k
+  // the tokens in use, in steps of four (all K in turn would issue the unused)
+  auto each = [&](const auto& f) {
+#pragma unroll
+    for (int k0 = 0; k0 < K; k0 += 4)
+      if (k0 < used) {
+#pragma unroll
+        for (int k = k0; k < k0 + 4; ++k) f(k);
+      }
+  };
   auto sync = [] {
     if (CL > 1) cluster_barrier(); else __syncthreads();
   };
@@ -180,21 +189,19 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
   };
 
   float x[K];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
+  each([&](int k) {
     const int t = t0 + 32 * k;
     x[k] = k < used && t < R.L ? R.w[t] : 0.f;
-  }
+  });
   uint32_t key[K];
   uint32_t stay = 0, open = 0;
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
+  each([&](int k) {
     const int t = t0 + 32 * k;
     key[k] = weight_key(x[k]);
     const bool inside = k < used && t >= R.lo && t < R.hi;
     stay |= static_cast<uint32_t>(k < used && t < R.L && !inside) << k;
     open |= static_cast<uint32_t>(inside) << k;
-  }
+  });
   if (R.r == R.hi - R.lo) stay |= open;
   if (R.contest()) {
     int r = R.r;
@@ -206,10 +213,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t ones = pass < 2 ? 2047 : 1023;
       if (__any_sync(0xffffffffu, open)) {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
+        each([&](int k) {
           if ((open >> k) & 1)
             atomicAdd(&s_hist[((key[k] >> shift) & ones) * kCopies + (lane & (kCopies - 1))], 1);
+        });
       }
       __syncthreads();
       int c[BPT];  // of bins kBins - 1 - BPT tid - q
@@ -237,13 +244,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
       const uint32_t bin = s_found[0];
       r -= s_found[1];
       if (__any_sync(0xffffffffu, open)) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
+        each([&](int k) {
           const uint32_t digit = (key[k] >> shift) & ones;
           const uint32_t bit = open & (1u << k);
           if (digit > bin) stay |= bit;
           if (digit != bin) open &= ~bit;
-        }
+        });
       }
       if (s_found[2] == r || s_found[2] <= kList) break;
     }
@@ -253,9 +259,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
     } else if (left <= kList) {
       // few keys left: a thread each counts those that come before it
       for (int e = tid; e < NW * K; e += THREADS) s_ranked[e] = 0;
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if ((open >> k) & 1) s_list[atomicAdd(&s_n, 1)] = make_uint2(key[k], t0 + 32 * k);
+      if (__any_sync(0xffffffffu, open))
+        each([&](int k) {
+          if ((open >> k) & 1) s_list[atomicAdd(&s_n, 1)] = make_uint2(key[k], t0 + 32 * k);
+        });
       sync();
       const uint2* list = s_list;
       if (CL > 1) {
@@ -283,8 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
           atomicOr(&s_ranked[at / (32 * used) * K + at / 32 % used], 1u << (at & 31));
       }
       __syncthreads();
-#pragma unroll
-      for (int k = 0; k < K; ++k) stay |= ((s_ranked[wid * K + k] >> lane) & 1) << k;
+      each([&](int k) { stay |= ((s_ranked[wid * K + k] >> lane) & 1) << k; });
     } else {  // many equal keys: the first r of them stay
       const int mine = __reduce_add_sync(0xffffffffu, __popc(open));
       if (lane == 0) s_warp[wid] = mine;
@@ -293,12 +299,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
       sync();
       first += before(&s_equal);
       uint32_t some = 0;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
+      each([&](int k) {
         const uint32_t m = __ballot_sync(0xffffffffu, (open >> k) & 1);
         if (((open >> k) & 1) && first + __popc(m & ((1u << lane) - 1)) < r) some |= 1u << k;
         first += __popc(m);
-      }
+      });
       stay |= some;
       __syncthreads();  // s_warp is read
     }
@@ -306,17 +311,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
 
   // the stayers' sums again (a key does not tell -0 from 0 or one NaN from
   // another), read before any is written: w_out may be w
-#pragma unroll
-  for (int k = 0; k < K; ++k) x[k] = (stay >> k) & 1 ? R.w[t0 + 32 * k] : 0.f;
+  each([&](int k) { x[k] = (stay >> k) & 1 ? R.w[t0 + 32 * k] : 0.f; });
   const int mine = __reduce_add_sync(0xffffffffu, __popc(stay));
   if (lane == 0) s_warp[wid] = mine;
   __syncthreads();
   int at = warp_scan(&s_stay);
   sync();
   at += before(&s_stay);
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if (k >= used) continue;
+  each([&](int k) {
     const bool mine = (stay >> k) & 1;
     const uint32_t m = __ballot_sync(0xffffffffu, mine);
     if (mine) {
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(c
       R.w_out[j] = x[k];
     }
     at += __popc(m);
-  }
+  });
   for (int t = R.n + rank * THREADS + tid; t < R.L; t += THREADS * CL) R.w_out[t] = 0.f;
   if (CL > 1) cluster_barrier();  // s_stay may still be read by the other CTAs
 }

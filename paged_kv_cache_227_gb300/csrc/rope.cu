@@ -20,7 +20,7 @@
 namespace pa {
 
 constexpr int kMaxPairs = kHeadDim / 2;
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 struct RopeArgs {
   const uint16_t* q;   // token stride q_stride, heads [n_q_heads][128]
@@ -38,7 +38,7 @@ struct RopeArgs {
   int interleaved;
   int chunks;                // warps a token's rows are cut into
   long long* err;
-  uint8_t axis[kMaxPairs];
+  uint32_t axis[kMaxPairs / 16];  // two bits a pair (a byte each would be 32 reads of constant memory a warp)
 };
 
 // Angle of position p and frequency f as turns in [-1/2, 1/2], computed in
@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
   for (int e = 0; e < 2; ++e) {
     const int f = lane + 32 * e;
     if (f < 8 * A.half_vecs) {
-      const int p = A.positions[A.axis[f] * A.n_tok + t];
+      const uint32_t word = lane < 16 ? A.axis[2 * e] : A.axis[2 * e + 1];
+      const int p = A.positions[((word >> (2 * (lane & 15))) & 3) * A.n_tok + t];
       float c, s;
       sincospif(2.f * turns(p, A.inv_freq[f]), &s, &c);
       s_cs[wib][f] = make_float2(c, s);
@@ -168,20 +169,23 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
 }
 
 template <int U>
-static void launch_rope(RopeArgs& A, bool bf16, cudaStream_t st) {
+static int launch_rope(RopeArgs& A, bool bf16, cudaStream_t st) {
   const int rows = A.Hq + 2 * A.Hkv;
   A.chunks = (rows + 4 * U - 1) / (4 * U);
-  const long long warps = A.n_tok * A.chunks;
-  const unsigned grid = static_cast<unsigned>((warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32));
+  const long long grid = (A.n_tok * A.chunks + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  if (grid > 0x7fffffffll) return PA_ERR_UNSUPPORTED;
   if (bf16)
-    rope_append_kernel<true, U><<<grid, kRopeThreads, 0, st>>>(A);
+    rope_append_kernel<true, U><<<static_cast<unsigned>(grid), kRopeThreads, 0, st>>>(A);
   else
-    rope_append_kernel<false, U><<<grid, kRopeThreads, 0, st>>>(A);
+    rope_append_kernel<false, U><<<static_cast<unsigned>(grid), kRopeThreads, 0, st>>>(A);
+  return cuda_status(cudaGetLastError());
 }
 
 }  // namespace pa
 
 using namespace pa;
+
+static_assert(PA_MAX_ROPE_AXES <= 4, "an axis is two bits");
 
 extern "C" int pa_rope_append(pa_pool_t p, const void* q, int64_t q_stride, int n_q_heads, const void* k_new,
                               int64_t k_stride, const void* v_new, int64_t v_stride, const int32_t* positions,
@@ -195,7 +199,7 @@ extern "C" int pa_rope_append(pa_pool_t p, const void* q, int64_t q_stride, int 
   RopeArgs A{};
   for (int f = 0; f < rot_dim / 2; ++f) {
     if (axis_of_pair[f] >= n_axes) return PA_ERR_INVALID;
-    A.axis[f] = axis_of_pair[f];
+    A.axis[f / 16] |= static_cast<uint32_t>(axis_of_pair[f]) << (2 * (f % 16));
   }
   if (n_tok == 0) return PA_OK;
   if (!q || !k_new || !v_new || !positions || !inv_freq || !slot_mapping || !q_out) return PA_ERR_INVALID;
@@ -230,12 +234,10 @@ extern "C" int pa_rope_append(pa_pool_t p, const void* q, int64_t q_stride, int 
   A.interleaved = interleaved != 0;
   A.err = p->err;
   // rows a warp: 4 while that leaves the GPU partly empty (64 tokens of 48 heads:
-  // 2.8 us, against 3.1 with 12), then 12, which share a token's angles
-  // (8,192 tokens of 48 heads: 35.8 us, against 56.2 with 4 and 36.5 with 16)
+  // 2.3 us), then 12, which share a token's angles (8,192 tokens of 48 heads:
+  // 32.9 us, 6.1 TB/s; with 4 rows a warp 1.6 times that, with 16 a little more)
   const long long quads = A.n_tok * ((A.Hq + 2 * A.Hkv + 3) / 4);
   if (quads <= 32ll * sm_count(p->device))
-    launch_rope<1>(A, p->dtype == PA_BF16, as_stream(stream));
-  else
-    launch_rope<3>(A, p->dtype == PA_BF16, as_stream(stream));
-  return cuda_status(cudaGetLastError());
+    return launch_rope<1>(A, p->dtype == PA_BF16, as_stream(stream));
+  return launch_rope<3>(A, p->dtype == PA_BF16, as_stream(stream));
 }

@@ -983,6 +983,7 @@ int pa_decode_shared(pa_pool_t p, const void* q, const int32_t* block_tables, in
   if (!p || !q || !block_tables || !seq_lens || !out || num_seqs <= 0 || n_groups < 0 || n_members < 0 ||
       (n_groups > 0 && (!group_start || !members || !prefix_blocks)))
     return PA_ERR_INVALID;
+  if (!std::isfinite(scale)) return PA_ERR_INVALID;
   if (n_members > num_seqs || (n_groups == 0) != (n_members == 0)) return PA_ERR_INVALID;
   if (out_dtype != PA_FP16 && out_dtype != PA_BF16 && out_dtype != PA_FP32) return PA_ERR_INVALID;
   if (num_seqs > kMaxSharedSeqs || n_groups > kMaxSharedSeqs) return PA_ERR_UNSUPPORTED;

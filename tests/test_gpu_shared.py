@@ -170,6 +170,39 @@ def test_unused_slots_hold_nan(pa):
     c.pool.close()
 
 
+def test_nan_reaches_the_rows_that_attend_it_and_no_others(pa):
+    """As in the plain decode: a NaN query, a NaN key of a sequence's last
+    token, a NaN value of the prefix."""
+    c = Shared(pa, [(12, [20, 40, 0, 500])], [30], 8, 2, torch.bfloat16, seed=11)
+    i, j = int(c.members[0]), int(c.members[1])
+    clean = c.call()
+    c.q[i, 3] = float("nan")
+    out = c.call()
+    assert torch.isnan(out[i, 3]).all()
+    out[i, 3] = clean[i, 3]
+    assert torch.equal(out, clean)
+    c.q[i, 3] = 0.5
+    clean = c.call()
+    t = int(c.lens[j]) - 1
+    c.pool.k[int(c.tables[j, t // BS]), 1, t % BS] = float("nan")
+    out = c.call()
+    # (a sequence whose whole cache is the prefix ends in a token of every member)
+    seen = torch.tensor(c.members.tolist() if t < 12 * BS else [j], device="cuda")
+    assert torch.isnan(out[seen, 4:]).all()
+    out[seen, 4:] = clean[seen, 4:]
+    assert torch.equal(out, clean)
+    c.pool.k[int(c.tables[j, t // BS]), 1, t % BS] = 0.5
+    clean = c.call()
+    c.pool.v[int(c.tables[i, 2]), 0, 5, 7] = float("nan")
+    out = c.call()
+    m = torch.from_numpy(c.members).long().cuda()
+    assert torch.isnan(out[m, :4, 7]).all()
+    out[m, :4, 7] = clean[m, :4, 7]
+    assert torch.equal(out, clean)
+    ok(pa, c.pool)
+    c.pool.close()
+
+
 def test_broken_groups_are_reported_and_ignored(pa):
     c = Shared(pa, [(4, [20, 5, 1]), (6, [30, 2])], [100], 8, 2, torch.bfloat16, seed=6)
     i32 = lambda x: cuda(np.array(x, np.int32))  # noqa: E731
@@ -277,6 +310,7 @@ def test_refusals(pa):
                           (dict(q=z(2, 18, D, t=torch.bfloat16), out=z(2, 18, D, t=torch.float32)), pa.PagedAttentionError),
                           (dict(out=z(2, 4, D, t=torch.float64)), ValueError),
                           (dict(workspace=z(4096, t=torch.uint8)), pa.PagedAttentionError),
+                          (dict(scale=float("nan")), pa.PagedAttentionError), (dict(scale=float("inf")), pa.PagedAttentionError),
                           (dict(members=torch.zeros(2, dtype=torch.int32)), ValueError)]:
         with pytest.raises(error):
             pa.pa_decode_shared(pool, **{**good, **change})
