@@ -287,19 +287,20 @@ __device__ __forceinline__ int clamp_len(const Params& P, int i) {
   return L;
 }
 
-// Warps that the ranges are cut for: all that fit the GPU, or those that fit
-// the SMs which the prefix product leaves (a range for an SM that it holds
-// would start when it ends).
-__device__ __forceinline__ int lean_units_of(const Params& P) {
-  if (!P.lean_taken) return P.lean_units;
-  const int taken = __ldcg(P.lean_taken);
-  return taken < P.lean_sms ? P.lean_units / P.lean_sms * (P.lean_sms - taken) : P.lean_units;
+__device__ __forceinline__ long long lean_per(const Params& P, const int* pfx) {
+  const long long num = static_cast<long long>(P.Hkv) * pfx[P.B] + P.lean_units - 1;
+  const long long per = num < 0x7fffffffll ? static_cast<int>(num) / P.lean_units : num / P.lean_units;
+  return per < kLeanMinBlocks ? kLeanMinBlocks : per;
 }
 
-__device__ __forceinline__ long long lean_per(const Params& P, const int* pfx) {
-  const int lean_units = lean_units_of(P);
-  const long long num = static_cast<long long>(P.Hkv) * pfx[P.B] + lean_units - 1;
-  const long long per = num < 0x7fffffffll ? static_cast<int>(num) / lean_units : num / lean_units;
+// The same for the shared-prefix decode, whose prefix product holds some SMs:
+// the ranges are cut for the warps that fit the others (a range for an SM that
+// the product holds would start when it ends).
+__device__ __forceinline__ long long lean_per_beside(const Params& P, const int* pfx) {
+  if (!P.lean_taken) return lean_per(P, pfx);
+  const int taken = __ldcg(P.lean_taken);
+  const int units = taken < P.lean_sms ? P.lean_units / P.lean_sms * (P.lean_sms - taken) : P.lean_units;
+  const long long per = (static_cast<long long>(P.Hkv) * pfx[P.B] + units - 1) / units;
   return per < kLeanMinBlocks ? kLeanMinBlocks : per;
 }
 
@@ -324,12 +325,12 @@ struct PieceIter {
   int li, lh;
   bool first;
 
-  __device__ PieceIter(const Params& p, const int* prefix, const int* lengths, int u, int nu)
+  __device__ PieceIter(const Params& p, const int* prefix, const int* lengths, int u, int nu, bool beside)
       : P(p), pfx(prefix), lens(lengths), unit(u), n_units(nu) {
     first = true;
     if (P.sched == SCHED_LEAN) {
       long long T = static_cast<long long>(P.Hkv) * pfx[P.B];
-      long long per = lean_per(P, pfx);
+      long long per = beside ? lean_per_beside(P, pfx) : lean_per(P, pfx);
       cur = per * unit;
       end = cur + per < T ? cur + per : T;
       if (cur < end) {
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(Shape<G>::kThreads, Shape<G>::kMinCtas) decode
   // on the table.  Entering a piece also prefetches the piece after it's q
   // rows (and new K/V rows) into L2.
   const uint64_t kv_policy = evict_first_policy();
-  PieceIter iss(P, S.pfx, S_lens, unit, n_units);
+  PieceIter iss(P, S.pfx, S_lens, unit, n_units, kExt);
   PieceIter cit = iss;  // the consumer walks the same list
   Piece ip, inx;  // current and next piece of the issue side
   bool ihave = iss.next(ip);
@@ -1469,7 +1470,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) weights_kernel(const __grid_
         }
         e = Ls > 0.f ? M + log2f(Ls) : -INFINITY;
       }
-      if (lane == 0) s_e[g] = e;
+      // (-inf: every token is out of range and none uses e, or a score is NaN)
+      if (lane == 0) s_e[g] = e == -INFINITY ? NAN : e;
     }
     __syncthreads();
     float e[G];
@@ -1480,8 +1482,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) weights_kernel(const __grid_
       const int t = base + k * kMergeThreads + tid;
       float sum = 0.f;
 #pragma unroll
-      for (int g = 0; g < G; ++g)  // (a token whose block is out of range: -inf; a sum that is NaN has no e)
-        sum += x[k][g] == -INFINITY ? 0.f : (e[g] == -INFINITY ? NAN : exp2f(x[k][g] - e[g]));
+      for (int g = 0; g < G; ++g)  // (a token whose block is out of range: -inf)
+        sum += x[k][g] == -INFINITY ? 0.f : exp2f(x[k][g] - e[g]);
       if (t < L) w[t] = fmaf(W.decay, old[k], sum);
     }
     __syncthreads();  // s_e is read
@@ -1568,7 +1570,7 @@ __global__ void __launch_bounds__(kMergeThreads, 8) combine_kernel(const __grid_
   constexpr bool kFrag = G > 4;  // the decode's records are in fragment order
   // lane's dims: 4 lane .. + 3, or in fragment order 32 (lane / 8) + lane % 8 + {0, 8, 16, 24}
   const int d0 = kFrag ? 32 * (lane >> 3) + (lane & 7) : 4 * lane;
-  const long long per = lean_per(P, mpfx);
+  const long long per = lean_per_beside(P, mpfx);
   GroupPlan total{};
   if (C.X.n_groups) total = load_plan(&C.X.plan[C.X.n_groups]);
   bool waited = false;
