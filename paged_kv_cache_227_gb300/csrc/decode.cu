@@ -1406,9 +1406,10 @@ constexpr int kSumChunk = kMergeThreads * kSumTokens;    // tokens a CTA and ite
 template <int G>
 __global__ void __launch_bounds__(kMergeThreads, 4) weights_kernel(const __grid_constant__ Params P,
                                                                    const WeightArgs W) {
-  extern __shared__ int mpfx[];  // [B + 1]
+  extern __shared__ int mpfx[];  // [B + 1], then the clamped lengths [B]
   __shared__ float s_e[8];
-  block_prefix(P, mpfx, nullptr, false);
+  int* const lens = mpfx + P.B + 1;
+  block_prefix(P, mpfx, lens, false);  // (the decode reports a length out of range)
   if (static_cast<int>(blockIdx.x) < W.merge_ctas) {
     merge_items<G, false>(P, mpfx, blockIdx.x, W.merge_ctas);
     return;
@@ -1422,9 +1423,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) weights_kernel(const __grid_
     const long long seg = it / chunks;
     const int base = static_cast<int>(it - seg * chunks) * kSumChunk;
     const int i = static_cast<int>(seg / P.Hkv), h = static_cast<int>(seg - static_cast<long long>(i) * P.Hkv);
-    int L = P.seq_lens[i];
-    L = L < 0 ? 0 : (L > span ? span : L);  // (the decode reports a length out of range)
-    if (base >= L) continue;
+    const int L = lens[i];
+    if (base >= L) continue;  // (most items, when lengths are ragged: no load on the way)
     float* w = W.weights + seg * span;
     float old[kSumTokens];
 #pragma unroll
@@ -2021,6 +2021,7 @@ static int launch_typed(Params& P, int device, cudaStream_t stream) {
       const long long chunks = (static_cast<long long>(P.max_blocks) * kBlock + kSumChunk - 1) / kSumChunk;
       const long long items = chunks * P.B * P.Hkv;
       cfg.gridDim = dim3(static_cast<unsigned>(mgrid + (items < mcap ? items : mcap)));
+      cfg.dynamicSmemBytes = sizeof(int) * static_cast<size_t>(2 * P.B + 1);
       if (cudaLaunchKernelEx(&cfg, weights_kernel<G>, P, W) != cudaSuccess) return PA_ERR_CUDA;
     } else if constexpr (kExt && G <= PA_MAX_GROUP) {
       if (P.combine) {
