@@ -143,8 +143,8 @@ int pa_cache_append(pa_pool_t pool, const void* k_new, const void* v_new,
  * Pointers are 16-byte aligned and strides multiples of 8 elements that hold
  * a token's heads (else INVALID).  rot_dim is a multiple of 16 up to 128, 1 <=
  * n_axes <= PA_MAX_ROPE_AXES, n_q_heads <= PA_MAX_ROPE_HEADS, and the rows
- * fit one launch (2^31 blocks of 16 rows or more: else UNSUPPORTED).  Tokens
- * that name one slot race, as for pa_cache_append.  Arithmetic is fp32, rounded once to the pool's type.
+ * fit one launch (2^31 CTAs of 16 rows; else UNSUPPORTED).  Tokens that name
+ * one slot race, as for pa_cache_append.  Arithmetic is fp32, rounded once to the pool's type.
  * n_tok == 0 is a no-op. */
 enum { PA_MAX_ROPE_AXES = 4, PA_MAX_ROPE_HEADS = 65536 };
 int pa_rope_append(pa_pool_t pool, const void* q, int64_t q_stride, int n_q_heads, const void* k_new,
