@@ -139,3 +139,46 @@ def test_prompts_steps_eviction_and_on():
     for _ in range(2):
         step(shared=False)
     pool.close()
+
+
+def test_top_blocks_of_a_large_pool():
+    """Offsets past 2^32 bytes (4.6 GB an array): each operator gives the bits
+    that it gives at the bottom of the pool."""
+    import paged_kv_cache_227_gb300 as pa
+    torch.cuda.set_device(0)
+    N, hkv, hq, L = 140000, 8, 16, 150
+    pool = pa.Pool(N, hkv, DTYPE)
+    n = -(-L // BS)
+    results = []
+    for base in (0, N - 64):
+        rng = np.random.default_rng(23)
+        perm = base + rng.permutation(64).astype(np.int32)
+        shared, rest = perm[:4], perm[4:]
+        tables = np.stack([np.concatenate([shared, rest[i * (n - 4):(i + 1) * (n - 4)]]) for i in range(3)]).astype(np.int32)
+        fresh = rest[3 * (n - 4):3 * (n - 4) + 9].reshape(3, 3)
+        slots = np.concatenate([t.astype(np.int64)[:, None] * BS + np.arange(BS) for t in tables]).reshape(3, -1)[:, :L]
+        qkv = rand16(rng, DTYPE, 3 * L, hq + 2 * hkv, D).cuda()
+        # the shared blocks hold one prompt: every sequence writes the same rows there
+        qkv.view(3, L, -1)[:, :64] = qkv.view(3, L, -1)[0, :64].clone()
+        pos = np.tile(np.arange(L), 3).astype(np.int32)[None]
+        qo = torch.empty(3 * L, hq, D, dtype=DTYPE, device="cuda")
+        pa.pa_rope_append(pool, qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], cuda(pos), cuda(INV), [0] * 64,
+                          cuda(slots.reshape(-1)), qo)
+        q = qo.view(3, L, hq, D)[:, -1].contiguous()
+        bt, sl = cuda(tables), cuda(np.full(3, L, np.int32))
+        out, again = torch.empty(3, hq, D, device="cuda"), torch.empty(3, hq, D, device="cuda")
+        w = torch.zeros(3, hkv, n * BS, device="cuda")
+        pa.pa_decode_weights(pool, q, bt, sl, D ** -0.5, out, w)
+        i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        pa.pa_decode_shared(pool, q, bt, sl, D ** -0.5, again, i32(0, 3), i32(0, 1, 2), i32(4))
+        kept = torch.zeros(3, hkv, n * BS, dtype=torch.int32, device="cuda")
+        n_out = i32(0, 0, 0)
+        summed = w.clone()
+        pa.pa_evict(pool, w, bt, sl, i32(40, 41, 48), n_out, kept, n_sink=2, n_recent=8, dst_tables=cuda(fresh))
+        ok(pa, pool)
+        at = torch.from_numpy(fresh.astype(np.int64)).cuda()
+        results.append([x.clone() for x in (qo, out, again, summed, w, kept, n_out, pool.k[at][:, :2], pool.v[at][:, :2])])
+        assert (out - again).abs().max() < 1e-4
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    pool.close()

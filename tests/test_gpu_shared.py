@@ -203,8 +203,10 @@ def test_nan_reaches_the_rows_that_attend_it_and_no_others(pa):
     c.pool.close()
 
 
-def test_broken_groups_are_reported_and_ignored(pa):
-    c = Shared(pa, [(4, [20, 5, 1]), (6, [30, 2])], [100], 8, 2, torch.bfloat16, seed=6)
+@pytest.mark.parametrize("spare_width", [1, 9000, 9001, 9002])
+def test_broken_groups_are_reported_and_ignored(pa, spare_width):
+    """(Wide tables are checked by a cluster, four entries at a time when rows allow it.)"""
+    c = Shared(pa, [(4, [20, 5, 1]), (6, [30, 2])], [100], 8, 2, torch.bfloat16, seed=6, spare_width=spare_width)
     i32 = lambda x: cuda(np.array(x, np.int32))  # noqa: E731
     m, s = c.members.tolist(), c.start.tolist()
     other = int(np.argmax(c.lens))
