@@ -555,6 +555,9 @@ extern "C" int pa_evict(pa_pool_t p, const float* weights, float* weights_out, c
   cudaStream_t st = as_stream(stream);
   const int span = max_blocks_per_seq * kBlock;
   cudaError_t e = cudaSuccess;
+  // the smallest CTAs that hold a row's keys in registers; from 8,192 tokens on
+  // a cluster of them (32 rows of up to 32K: 4 CTAs each 17 us; 8 CTAs add 8 us,
+  // one CTA that reads its row again for each pass takes 44)
   if (span <= 256 * 8) e = launch_select<256, 8, 1>(A, st);
   else if (span <= 256 * 16) e = launch_select<256, 16, 1>(A, st);
   else if (span <= 512 * 16) e = launch_select<512, 16, 1>(A, st);

@@ -1039,9 +1039,10 @@ int pa_decode_shared(pa_pool_t p, const void* q, const int32_t* block_tables, in
   A.err = p->err;
   A.wait_limit_ns = wait_limit_ns();
   cudaStream_t st = as_stream(stream);
-  // one CTA while its warps compare at most 32 K table entries (64 chats of
-  // 2,400 tokens: 5 us, against 8 us with the cluster)
-  if (num_seqs <= kSmallPlan && n_groups <= kSmallPlan && static_cast<long long>(n_members) * max_blocks_per_seq <= 32768) {
+  // one CTA while its warps compare at most 16 K table entries (whole calls with
+  // it and with the cluster: 4 sequences 19.3 and 21.5 us, 16 of about 170 blocks
+  // 53.3 and 55.4, 64 of about 190 blocks 39.8 and 39.7)
+  if (num_seqs <= kSmallPlan && n_groups <= kSmallPlan && static_cast<long long>(n_members) * max_blocks_per_seq <= 16384) {
     shared_plan_kernel<1, kSmallThreads><<<1, kSmallThreads, 0, st>>>(A);
   } else {
     cudaLaunchConfig_t cfg = {};
