@@ -490,8 +490,10 @@ struct SharedPieces {
   }
 };
 
-// Barrier of the 256 threads of team w, and whether `x` holds for all of them.
+// Barrier of the 256 threads of team w, of the 64 threads of a pair of warps, and
+// whether `x` holds for all threads of a barrier.
 __device__ __forceinline__ void team_sync(int w) { asm volatile("bar.sync %0, 256;" ::"r"(w + 1) : "memory"); }
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool vote(int id, int threads, bool x) {
   uint32_t y;
   asm volatile(
@@ -825,6 +827,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
               for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
               tmem_st16(t_o + 16 * x, o);
             }
+            // the first half of the value product adds to all 128 columns of
+            // O on the first half's arrivals alone: they come when both warps
+            // have rescaled (m and the maximum are the pair's, so is the branch)
+            tmem_wait_st();
+            tc_fence_before();
+            pair_sync(pair);
+            tc_fence_after();
           }
         }
         const float base = m == -INFINITY ? 0.f : m;
