@@ -1640,7 +1640,9 @@ __global__ void __launch_bounds__(kMergeThreads, 8) combine_kernel(const __grid_
         if (c0) b_pre.load(at_most(shared.count - c0), pre_stat(c0), pre_load(c0));
         R.add(at_most(shared.count - c0), b_pre, pre_load(c0));
       }
-    if (whole && R.M == -INFINITY) {  // the decode saw nothing but NaN, or no block in range (zeros)
+    // a whole segment's log-sum-exp of -inf: a score was NaN (and so is the
+    // row, whatever the prefix holds), or no block was in range (zeros)
+    if (whole && __shfl_sync(0xffffffffu, b_own.mk, 0) == -INFINITY) {
       R.O.x += 0.f * b_own.ob[0].x;
       R.O.y += 0.f * b_own.ob[0].y;
       R.O.z += 0.f * b_own.ob[0].z;
