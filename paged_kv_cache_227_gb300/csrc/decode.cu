@@ -1515,9 +1515,10 @@ struct Batch {  // the first up to 32 records of a list: their m and l, a lane e
 struct Combined {
   float M = -INFINITY, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  // n loaded records (n <= 32); a record without tokens holds no output: it
-  // was read, and is left out.  A sum that is NaN makes the row NaN, whatever
-  // the maxima say (they pass NaN over).
+  // n loaded records (n <= 32); a record without tokens (m = -inf) holds no
+  // output: it was read, and is left out (weight -1).  One whose weight
+  // underflows is not: a NaN or infinite value in it reaches the row.  A sum
+  // that is NaN makes the row NaN, whatever the maxima say (they pass NaN over).
   template <int RB, typename Load>
   __device__ __forceinline__ void add(int n, Batch<RB>& b, const Load& o) {
     float mx = b.mk;
@@ -1527,8 +1528,8 @@ struct Combined {
     if (__any_sync(0xffffffffu, isnan(b.lk))) L = NAN;
     if (mn == -INFINITY) return;  // no token in any record so far
     const float a = M == mn ? 1.f : fast_exp2(M - mn);
-    const float wk = b.mk == -INFINITY ? 0.f : fast_exp2(b.mk - mn);
-    float lw = wk * b.lk;
+    const float wk = b.mk == -INFINITY ? -1.f : fast_exp2(b.mk - mn);
+    float lw = wk < 0.f ? 0.f : wk * b.lk;
 #pragma unroll
     for (int msk = 1; msk < 32; msk <<= 1) lw += __shfl_xor_sync(0xffffffffu, lw, msk);
     L = L * a + lw;
@@ -1546,7 +1547,7 @@ struct Combined {
 #pragma unroll
       for (int r = 0; r < RB; ++r) {
         const float w = __shfl_sync(0xffffffffu, wk, (b0 + r) & 31);
-        if (b0 + r < n && w != 0.f) {
+        if (b0 + r < n && !(w < 0.f)) {
           O.x = fmaf(w, b.ob[r].x, O.x);
           O.y = fmaf(w, b.ob[r].y, O.y);
           O.z = fmaf(w, b.ob[r].z, O.z);
