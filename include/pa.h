@@ -297,10 +297,11 @@ int pa_decode_cascade(pa_pool_t pool, const void* q, const int32_t* block_tables
  * group, is reported and no group takes part.  A shared block id out of range
  * is skipped for every member (reported).
  * q, out, block_tables, seq_lens as for pa_decode.  With a 16-bit out the
- * prefix's weights are rounded to the pool's 16 bits for the value product
- * (2^-9 or 2^-12 of each, against an output rounded by as much); with fp32
- * out they are carried as a high and a low half (2^-17).  The result does not
- * depend on timing.
+ * prefix's weights are rounded to the pool's 16 bits for the value product;
+ * with fp32 out they are carried as a high and a low half.  A weight is then
+ * off by at most 2^-8 (bf16; 2^-17 with fp32 out) of itself, or by the larger of
+ * 2^-11 (fp16; 2^-23 with fp32 out) of itself and 2^-32 of the row's largest.
+ * The weights' sum takes them unrounded.  The result does not depend on timing.
  * num_seqs and n_groups <= 4096 (else UNSUPPORTED); n_members <= num_seqs,
  * num_seqs * max_blocks_per_seq < 2^31, a finite scale (else INVALID).
  * workspace: device, >= pa_decode_shared_workspace_bytes(...), 256-byte

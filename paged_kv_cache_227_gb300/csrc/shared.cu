@@ -42,7 +42,9 @@
 //  - a weight is rounded to the pool's 16 bits for the value product when the
 //    output has 16 bits (half a step of each weight, averaged over the tokens,
 //    against half a step of the output); with a 32-bit output it is carried as
-//    a high and a low half, in two products.
+//    a high and a low half, in two products.  fp16 has five bits of exponent, so
+//    its weights are taken times 2^7: up to 2^15 while the maximum lags, and
+//    full steps down to 2^-21 of the maximum's weight (2^-14 without).
 //
 // Measured (2,070 MHz): a chunk of two tiles takes 3,500 cycles, of which the
 // tensor cores could do with 2,048 (8 KB of operands from shared memory each 64
@@ -73,6 +75,10 @@ constexpr int kHalf = kTile / 2;           // dims 0-63 | 64-127
 constexpr int kStages = 2;
 constexpr float kLog2eF = 1.4426950408889634f;
 constexpr float kMoveBy = 8.f;         // log2 units the maximum may lag behind
+// log2 of the weight at the maximum (a lagging one adds kMoveBy: below 2^16, where fp16 ends)
+template <bool kBf16>
+constexpr float kTopWeight = kBf16 ? 0.f : 7.f;
+static_assert(kTopWeight<false> + kMoveBy < 16.f, "a weight is past fp16");
 
 constexpr int kPlanCluster = 8, kPlanThreads = 1024, kSmallThreads = 1024;
 constexpr int kSoftWarps = 16;
@@ -836,7 +842,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
             tc_fence_after();
           }
         }
-        const float base = m == -INFINITY ? 0.f : m;
+        const float base = m == -INFINITY ? 0.f : m - kTopWeight<kBf16>;
         const float2 qs2 = make_float2(A.qscale, A.qscale), mb2 = make_float2(-base, -base);
         float2 sum = make_float2(0.f, 0.f);
         // a block of 16 tokens at a time, read again; P over its columns of S:
@@ -909,7 +915,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
       }
       tc_fence_before();
       if (hh == 0 && r < rows) {
-        rec[kItemRows * kHeadDim + w * kRows + r] = m;
+        rec[kItemRows * kHeadDim + w * kRows + r] = m - kTopWeight<kBf16>;
         rec[kItemRows * kHeadDim + kItemRows + w * kRows + r] = l + S.part[w][1][r];
       }
       mbar_arrive(smem_addr(&S.qfree));
