@@ -1451,6 +1451,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) weights_kernel(const __grid_
         e = __ldcg(&P.lse[seg * G + g]);
       } else {
         float M = -INFINITY, Ls = 0.f;
+        bool nan = false;
         for (int c0 = 0; c0 < recs.count; c0 += 32) {
           float mk = -INFINITY, lk = 0.f;
           if (c0 + lane < recs.count) {
@@ -1462,13 +1463,14 @@ __global__ void __launch_bounds__(kMergeThreads, 4) weights_kernel(const __grid_
 #pragma unroll
           for (int msk = 1; msk < 32; msk <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, msk));
           const float mn = fmaxf(M, mx);
+          nan = nan || __any_sync(0xffffffffu, isnan(lk));  // (a piece of NaN scores alone has no maximum)
           float lw = mk == -INFINITY ? 0.f : fast_exp2(mk - mn) * lk;
 #pragma unroll
           for (int msk = 1; msk < 32; msk <<= 1) lw += __shfl_xor_sync(0xffffffffu, lw, msk);
           Ls = (M == -INFINITY ? 0.f : Ls * fast_exp2(M - mn)) + lw;
           M = mn;
         }
-        e = Ls > 0.f ? M + log2f(Ls) : -INFINITY;
+        e = Ls > 0.f && !nan ? M + log2f(Ls) : -INFINITY;
       }
       // (-inf: every token is out of range and none uses e, or a score is NaN)
       if (lane == 0) s_e[g] = e == -INFINITY ? NAN : e;
