@@ -429,6 +429,17 @@ int pa_profile_stop(float* ms, int cap);
  * Nothing traps or hangs. */
 int pa_selftest_wait_timeout(pa_pool_t pool, long long limit_ns, void* stream);
 
+/* The same for pa_decode_shared's prefix product, with its arguments: its
+ * loads do not come, its waits give up after limit_ns (0 < limit_ns <= 1e9),
+ * every warp leaves, and PA_ERR_TIMEOUT is in the error word (n_groups == 0 has
+ * no product and no wait).  out and workspace are written, with nothing of use. */
+int pa_selftest_shared_timeout(pa_pool_t pool, const void* q, const int32_t* block_tables,
+                               int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs,
+                               int n_q_heads, float scale, const int32_t* group_start,
+                               const int32_t* members, int n_members, const int32_t* prefix_blocks,
+                               int n_groups, void* out, int out_dtype, void* workspace,
+                               size_t workspace_bytes, long long limit_ns, void* stream);
+
 /* Synchronises `stream`, reads and clears the pool's device error word.
  * Returns PA_OK, PA_ERR_DEVICE_CHECK or PA_ERR_TIMEOUT; *detail (may be NULL)
  * receives the offending block id / slot (or the wait site for a timeout). */

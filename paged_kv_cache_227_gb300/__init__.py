@@ -52,6 +52,8 @@ def _load():
         "pa_decode_weights": (i32, [vp, vp, vp, i32, vp, i32, i32, f32, vp, i32, vp, f32, vp, sz, vp]),
         "pa_decode_shared_workspace_bytes": (sz, [vp, i32, i32, i32, i32]),
         "pa_decode_shared": (i32, [vp, vp, vp, i32, vp, i32, i32, f32, vp, vp, i32, vp, i32, vp, i32, vp, sz, vp]),
+        "pa_selftest_shared_timeout": (i32, [vp, vp, vp, i32, vp, i32, i32, f32, vp, vp, i32, vp, i32, vp, i32, vp, sz,
+                                             ctypes.c_longlong, vp]),
         "pa_evict": (i32, [vp, vp, vp, vp, i32, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp]),
         "pa_alloc_evict": (i32, [vp, vp, vp, i32]),
         "pa_decode": (i32, [vp, vp, vp, i32, vp, i32, i32, f32, vp, i32, vp]),
@@ -446,11 +448,8 @@ def shared_workspace_for(pool, q, block_tables, prefix_blocks, stream=None):
     return _workspace(n, "pa_decode_shared_workspace_bytes", pool.device, stream)
 
 
-def pa_decode_shared(pool, q, block_tables, seq_lens, scale, out, group_start, members, prefix_blocks, workspace=None,
-                     stream=None):
-    """pa_decode with each group's shared prefix attended once for all of its
-    members, groups of any size (see include/pa.h); the group arrays are int32
-    device tensors (cascade_groups with max_members=B finds them)."""
+def _shared_args(pool, q, block_tables, seq_lens, scale, out, group_start, members, prefix_blocks, workspace, stream):
+    """Checks of pa_decode_shared; the C call's arguments up to the stream."""
     qa, ta, la, oa, code, B, Hq, W = _decode_at(pool, q, block_tables, seq_lens, out)
     ga = _at(pool, group_start, "group_start", torch.int32)
     ma = _at(pool, members, "members", torch.int32)
@@ -460,9 +459,28 @@ def pa_decode_shared(pool, q, block_tables, seq_lens, scale, out, group_start, m
         raise ValueError("shapes: group_start [n_groups+1], members [n_members], prefix_blocks [n_groups]")
     if workspace is None:
         workspace = shared_workspace_for(pool, q, block_tables, prefix_blocks, stream)
-    _check(lib.pa_decode_shared(pool.handle, qa, ta, W, la, B, Hq, float(scale), ga, ma, nm, pa_, ng, oa, code,
-                                _at(pool, workspace, "workspace", torch.uint8), workspace.numel(),
-                                _raw_stream(pool, stream)), "pa_decode_shared")
+    wa = _at(pool, workspace, "workspace", torch.uint8)
+    return (pool.handle, qa, ta, W, la, B, Hq, float(scale), ga, ma, nm, pa_, ng, oa, code, wa, workspace.numel()), workspace
+
+
+def pa_decode_shared(pool, q, block_tables, seq_lens, scale, out, group_start, members, prefix_blocks, workspace=None,
+                     stream=None):
+    """pa_decode with each group's shared prefix attended once for all of its
+    members, groups of any size (see include/pa.h); the group arrays are int32
+    device tensors (cascade_groups with max_members=B finds them)."""
+    args, _own = _shared_args(pool, q, block_tables, seq_lens, scale, out, group_start, members, prefix_blocks, workspace,
+                              stream)  # (_own: a workspace made for this call lives until it is launched)
+    _check(lib.pa_decode_shared(*args, _raw_stream(pool, stream)), "pa_decode_shared")
+
+
+def pa_selftest_shared_timeout(pool, q, block_tables, seq_lens, scale, out, group_start, members, prefix_blocks, limit_ns,
+                               workspace=None, stream=None):
+    """pa_decode_shared whose prefix product gets no loads: its waits give up
+    after limit_ns and PA_ERR_TIMEOUT is recorded (read it with pa_check).
+    Returns the launch status."""
+    args, _own = _shared_args(pool, q, block_tables, seq_lens, scale, out, group_start, members, prefix_blocks, workspace,
+                              stream)
+    return lib.pa_selftest_shared_timeout(*args, int(limit_ns), _raw_stream(pool, stream))
 
 
 def weights_workspace_for(pool, q, block_tables, stream=None):

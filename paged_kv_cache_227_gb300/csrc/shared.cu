@@ -85,6 +85,7 @@ constexpr int kSoftWarps = 16;
 constexpr int kTeam = 256;             // threads of a team: two a row
 constexpr int kPrefixThreads = (kSoftWarps + 2) * 32;  // + producer warp, + MMA warp
 constexpr int kMasks = 4;              // chunk masks in flight
+constexpr long long kDrainNs = 2000000000ll;  // limit of the last waits of a CTA that gives up
 // Estimates, in ns, to divide the SMs by: a chunk of the product on its SM, a
 // CTA's start and records; a tile of 16 tokens of the decode on one SM, and its
 // start.  Measured on 64 chats of 2,048 + about 280 tokens, 16 multi-head
@@ -117,6 +118,7 @@ struct SharedArgs {
   int ctas;                       // of the prefix product: at most this many work
   long long* err;
   long long wait_limit_ns;
+  int hold;                       // self-test: nothing is loaded, so that the waits run out
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -522,6 +524,7 @@ struct __align__(1024) PrefixSmem {
   uint32_t mask[kMasks];  // blocks of the chunk that are there
   uint32_t tmem;
   int abort_flag;
+  int begun[2];  // K and V loads issued
 };
 
 template <bool kBf16, bool kLo>
@@ -574,7 +577,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
     // ---- loads: K and V of each chunk, lane 2b + half for block b
     int n = 0, nk = 0, nv = 0;  // chunks, K and V loads issued
     bool ok = true;
-    for (; ok && walk->more; S.pieces[warp].next(A, blockIdx.x)) {
+    for (; ok && walk->more && !A.hold; S.pieces[warp].next(A, blockIdx.x)) {
       const int c0 = p.c0, c1 = p.c1, blocks = p.blocks, h = p.h;
       const int32_t* row = A.tables + static_cast<long long>(A.members[p.member0]) * A.max_blocks;
       auto fetch = [&](int c) {  // a chunk's block id
@@ -623,17 +626,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
         blk = ahead;
       }
     }
-    // never leave a load in flight into this CTA's shared memory
-    if (lane == 0 && *abort_flag) {
-      auto drain = [&](unsigned long long* full, int issued) {
-        for (int k = issued > kStages ? issued - kStages : 0; k < issued; ++k) {
-          const long long t0 = global_ns();
-          while (!mbar_try_wait(smem_addr(&full[k % kStages]), (k / kStages) & 1) && global_ns() - t0 < limit) {
-          }
-        }
-      };
-      drain(S.kfull, nk);
-      drain(S.vfull, nv);
+    if (lane == 0) {
+      S.begun[0] = nk;
+      S.begun[1] = nv;
     }
   } else if (warp == kMma) {
     // ---- products.  Step t of a piece serves warpgroup t & 1; S of step
@@ -726,13 +721,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
       }
       n0 += nc;
     }
-    if (!ok && leader) {  // wait for the products in flight before the TMEM goes
-      mma_commit(smem_addr(&S.drain));
-      const long long t0 = global_ns();
-      while (!mbar_try_wait(smem_addr(&S.drain), 0) && global_ns() - t0 < limit) {
-      }
-    }
-    __syncwarp();
   } else {
     // ---- softmax: team w; row r, tokens 64 hh .. 64 hh + 63 of a chunk
     const int w = warp >> 3, hh = (warp >> 2) & 1;
@@ -749,7 +737,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
       // teams are done with the piece before (its products with it)
       // (a wait that ran out in one warp is one for the team: its warps meet in
       // the pair barriers below)
-      if (piece_no > 0) ok = vote(w + 1, kTeam, wait(S.qfree, (piece_no - 1) & 1, 28));
+      if (piece_no > 0) ok = vote(w + 1, kTeam, __all_sync(0xffffffffu, wait(S.qfree, (piece_no - 1) & 1, 28)));
       ++piece_no;
       if (ok) {
         const int x = threadIdx.x & (kTeam - 1);
@@ -924,6 +912,28 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) shared_prefix_kernel(const 
   }
   __syncthreads();
   tc_fence_after();
+  if (*abort_flag) {  // a wait ran out, in whichever warp: what is in flight here ends before the memory goes
+    auto drained = [&](unsigned long long& bar, uint32_t parity) {
+      const long long t0 = global_ns();
+      while (!mbar_try_wait(smem_addr(&bar), parity) && global_ns() - t0 < kDrainNs) {
+      }
+    };
+    if (warp == kProducer && lane == 0) {
+      for (int v = 0; v < 2; ++v) {
+        const int issued = S.begun[v];
+        for (int k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
+          drained(v ? S.vfull[k % kStages] : S.kfull[k % kStages], (k / kStages) & 1);
+      }
+    }
+    if (warp == kMma) {
+      if (elect_one()) {  // (the lane that issued the products)
+        mma_commit(smem_addr(&S.drain));
+        drained(S.drain, 0);
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+  }
   if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
@@ -1005,10 +1015,13 @@ size_t pa_decode_shared_workspace_bytes(pa_pool_t p, int num_seqs, int n_q_heads
   return shared_layout(p, num_seqs, n_q_heads, max_blocks_per_seq, n_groups, &L) ? L.total : 0;
 }
 
-int pa_decode_shared(pa_pool_t p, const void* q, const int32_t* block_tables, int max_blocks_per_seq,
-                     const int32_t* seq_lens, int num_seqs, int n_q_heads, float scale, const int32_t* group_start,
-                     const int32_t* members, int n_members, const int32_t* prefix_blocks, int n_groups, void* out,
-                     int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+}  // extern "C"
+
+// hold_ns: 0, or (self-test) the limit of the product's waits, for loads that do not come.
+static int decode_shared(pa_pool_t p, const void* q, const int32_t* block_tables, int max_blocks_per_seq,
+                         const int32_t* seq_lens, int num_seqs, int n_q_heads, float scale, const int32_t* group_start,
+                         const int32_t* members, int n_members, const int32_t* prefix_blocks, int n_groups, void* out,
+                         int out_dtype, void* workspace, size_t workspace_bytes, void* stream, long long hold_ns) {
   if (!p || !q || !block_tables || !seq_lens || !out || num_seqs <= 0 || n_groups < 0 || n_members < 0 ||
       (n_groups > 0 && (!group_start || !members || !prefix_blocks)))
     return PA_ERR_INVALID;
@@ -1052,7 +1065,8 @@ int pa_decode_shared(pa_pool_t p, const void* q, const int32_t* block_tables, in
   A.num_blocks = p->num_blocks;
   A.ctas = sm_count(p->device);
   A.err = p->err;
-  A.wait_limit_ns = wait_limit_ns();
+  A.wait_limit_ns = hold_ns ? hold_ns : wait_limit_ns();
+  A.hold = hold_ns != 0;
   cudaStream_t st = as_stream(stream);
   // one CTA while its warps compare at most 16 K table entries (whole calls with
   // it and with the cluster: 4 sequences 19.3 and 21.5 us, 16 of about 170 blocks
@@ -1083,6 +1097,28 @@ int pa_decode_shared(pa_pool_t p, const void* q, const int32_t* block_tables, in
   return decode_own_and_combine(p, q, block_tables, max_blocks_per_seq, A.lens_s, A.offs_s, num_seqs, n_q_heads, scale,
                                 reinterpret_cast<float*>(ws + L.o_s), reinterpret_cast<float*>(ws + L.lse_s), out,
                                 out_dtype, X, ws + L.dec, L.dec_bytes, stream);
+}
+
+extern "C" {
+
+int pa_decode_shared(pa_pool_t p, const void* q, const int32_t* block_tables, int max_blocks_per_seq,
+                     const int32_t* seq_lens, int num_seqs, int n_q_heads, float scale, const int32_t* group_start,
+                     const int32_t* members, int n_members, const int32_t* prefix_blocks, int n_groups, void* out,
+                     int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  return decode_shared(p, q, block_tables, max_blocks_per_seq, seq_lens, num_seqs, n_q_heads, scale, group_start,
+                       members, n_members, prefix_blocks, n_groups, out, out_dtype, workspace, workspace_bytes, stream,
+                       0);
+}
+
+int pa_selftest_shared_timeout(pa_pool_t p, const void* q, const int32_t* block_tables, int max_blocks_per_seq,
+                               const int32_t* seq_lens, int num_seqs, int n_q_heads, float scale,
+                               const int32_t* group_start, const int32_t* members, int n_members,
+                               const int32_t* prefix_blocks, int n_groups, void* out, int out_dtype, void* workspace,
+                               size_t workspace_bytes, long long limit_ns, void* stream) {
+  if (limit_ns <= 0 || limit_ns > 1000000000ll) return PA_ERR_INVALID;
+  return decode_shared(p, q, block_tables, max_blocks_per_seq, seq_lens, num_seqs, n_q_heads, scale, group_start,
+                       members, n_members, prefix_blocks, n_groups, out, out_dtype, workspace, workspace_bytes, stream,
+                       limit_ns);
 }
 
 }  // extern "C"
