@@ -432,7 +432,8 @@ def pa_rope_append(pool, q, k_new, v_new, positions, inv_freq, axis_of_pair, slo
     ka, ks = _heads(pool, k_new, "k_new", kv_rows)
     va, vs = _heads(pool, v_new, "v_new", kv_rows)
     oa, os_ = _heads(pool, q_out, "q_out", q_rows)
-    axes = bytes(axis_of_pair)  # (ValueError outside 0 .. 255)
+    # (ValueError outside 0 .. 255; an array's own bytes are not its numbers)
+    axes = bytes(axis_of_pair if isinstance(axis_of_pair, (list, tuple, bytes, bytearray)) else list(axis_of_pair))
     if positions.dim() != 2 or positions.shape[1] != n:
         raise ValueError("positions must be [n_axes][n_tok]")
     if inv_freq.shape != (len(axes),):
