@@ -330,7 +330,8 @@ int pa_decode_shared(pa_pool_t pool, const void* q, const int32_t* block_tables,
  * 256-byte aligned, caller-owned; it holds the scores (4 bytes a query head
  * and table position) and the split's records; its contents on entry do not
  * matter, and calls that share one must not overlap on the GPU.  num_seqs <=
- * 4096 (else UNSUPPORTED). */
+ * 4096 and max_blocks_per_seq <= PA_MAX_WALKED_BLOCKS (else UNSUPPORTED). */
+enum { PA_MAX_WALKED_BLOCKS = (1 << 27) - (1 << 16) }; /* 2^31 - 2^20 tokens */
 size_t pa_decode_weights_workspace_bytes(pa_pool_t pool, int num_seqs, int n_q_heads,
                                          int max_blocks_per_seq);
 int pa_decode_weights(pa_pool_t pool, const void* q, const int32_t* block_tables,
@@ -365,7 +366,8 @@ int pa_decode_weights(pa_pool_t pool, const void* q, const int32_t* block_tables
  *                  <- the kept positions, ascending, in [0, n); the rest is
  *                  left as it is.
  * A row whose source or destination block is out of range is not moved
- * (reported).  num_seqs == 0 is a no-op; num_seqs <= 65535 (else UNSUPPORTED). */
+ * (reported).  num_seqs == 0 is a no-op; num_seqs <= 65535 and both widths <=
+ * PA_MAX_WALKED_BLOCKS (else UNSUPPORTED). */
 int pa_evict(pa_pool_t pool, const float* weights, float* weights_out, const int32_t* block_tables,
              int max_blocks_per_seq, const int32_t* dst_tables, int dst_blocks_per_seq,
              const int32_t* seq_lens, const int32_t* keep, int num_seqs, int n_sink, int n_recent,

@@ -2259,7 +2259,7 @@ struct WeightsLayout {
 static bool weights_layout(const pa_pool* p, int B, int Hq, int max_blocks, WeightsLayout* L) {
   WorkspaceLayout rw{};
   if (!workspace_layout(p, B, Hq, max_blocks, 0, &rw)) return false;
-  if (max_blocks > 0x7fffffff / kBlock) return false;
+  if (max_blocks > kMaxWalkedBlocks) return false;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -2282,7 +2282,7 @@ int pa_decode_weights(pa_pool_t p, const void* q, const int32_t* block_tables, i
                       const int32_t* seq_lens, int num_seqs, int n_q_heads, float scale, void* out, int out_dtype,
                       float* weights, float decay, void* workspace, size_t workspace_bytes, void* stream) {
   if (!p || !weights || (reinterpret_cast<uintptr_t>(weights) & 15)) return PA_ERR_INVALID;
-  if (num_seqs > kMaxSplitSeqs) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > kMaxSplitSeqs || max_blocks_per_seq > kMaxWalkedBlocks) return PA_ERR_UNSUPPORTED;
   WeightsLayout L{};
   if (!weights_layout(p, num_seqs, n_q_heads, max_blocks_per_seq, &L)) return PA_ERR_INVALID;
   if (!workspace || workspace_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 255))

@@ -529,7 +529,7 @@ extern "C" int pa_evict(pa_pool_t p, const float* weights, float* weights_out, c
                         int32_t* seq_lens_out, int32_t* kept, void* stream) {
   if (!p || num_seqs < 0 || max_blocks_per_seq <= 0 || n_sink < 0 || n_recent < 0) return PA_ERR_INVALID;
   if (dst_tables && dst_blocks_per_seq <= 0) return PA_ERR_INVALID;
-  if (max_blocks_per_seq > 0x7fffffff / kBlock || dst_blocks_per_seq > 0x7fffffff / kBlock) return PA_ERR_INVALID;
+  if (max_blocks_per_seq > kMaxWalkedBlocks || dst_blocks_per_seq > kMaxWalkedBlocks) return PA_ERR_UNSUPPORTED;
   if (num_seqs > 65535 || p->n_kv_heads > 65535) return PA_ERR_UNSUPPORTED;  // a grid dimension each
   if (num_seqs == 0) return PA_OK;
   if (!weights || !weights_out || !block_tables || !seq_lens || !keep || !seq_lens_out || !kept) return PA_ERR_INVALID;

@@ -32,6 +32,9 @@ constexpr int kBlock = PA_BLOCK_SIZE;     // tokens per block
 constexpr int kHeadDim = PA_HEAD_DIM;     // elements per K/V row
 constexpr int kRowBytes = kHeadDim * 2;   // one 16-bit row: 256 B
 constexpr int kTileBytes = kBlock * kRowBytes;  // one (block, head) tile: 4 KiB
+// Widest table of the operators that walk its positions in steps of up to 2^19
+// with 32-bit ints: a step past the end stays below 2^31.
+constexpr int kMaxWalkedBlocks = PA_MAX_WALKED_BLOCKS;
 
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
