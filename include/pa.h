@@ -302,11 +302,20 @@ int pa_decode_cascade(pa_pool_t pool, const void* q, const int32_t* block_tables
  * off by at most 2^-8 (bf16; 2^-17 with fp32 out) of itself, or by the larger of
  * 2^-11 (fp16; 2^-23 with fp32 out) of itself and 2^-32 of the row's largest.
  * The weights' sum takes them unrounded.  The result does not depend on timing.
+ * It pays where the plain split decode reads much of the prefix again: the
+ * call is four kernels, about 19 us at the least.  Measured on one GB300 with
+ * 8 and with 40 kv heads, the two break even where the members' prefixes come
+ * to 130-300 MB (members * prefix tokens * n_kv_heads * 512 bytes), with two
+ * members only past that; below it pa_decode_split is faster, also where
+ * pa_cascade_groups finds groups.
  * num_seqs and n_groups <= 4096 (else UNSUPPORTED); n_members <= num_seqs,
  * num_seqs * max_blocks_per_seq < 2^31, a finite scale (else INVALID).
  * workspace: device, >= pa_decode_shared_workspace_bytes(...), 256-byte
  * aligned, caller-owned; its contents on entry do not matter, and calls that
- * share one must not overlap on the GPU. */
+ * share one must not overlap on the GPU.  It holds a record of 133,120 bytes
+ * for each SM and for each kv head of n_groups + num_seqs * G / 256 items of up
+ * to 256 rows (256 groups of four with 40 kv heads of G = 1: 1.4 GB), and the
+ * split decode's records. */
 size_t pa_decode_shared_workspace_bytes(pa_pool_t pool, int num_seqs, int n_q_heads,
                                         int max_blocks_per_seq, int n_groups);
 int pa_decode_shared(pa_pool_t pool, const void* q, const int32_t* block_tables,

@@ -12,10 +12,10 @@
 // Two kernels.  The selection finds the r-th largest sum exactly, by radix
 // (the sums as order-preserving 32-bit keys, 11 + 11 + 10 bits, and direct
 // ranking as soon as few keys are left), and compacts in position order;
-// counts in shared memory only, so the result does not depend on timing.  The move copies rows.  Into fresh blocks every
-// row is independent.  In place it is safe because batch c (rows j of [a, b))
-// is written after batches up to c are read, and later batches read positions
-// t_j >= j >= b only.
+// counts in shared memory only, so the result does not depend on timing.  The
+// move copies rows.  Into fresh blocks every row is independent.  In place it
+// is safe because batch c (rows j of [a, b)) is written after batches up to c
+// are read, and later batches read positions t_j >= j >= b only.
 //
 // Bound: the move by memory (64 sequences of 8 heads, 1,024 of about 4,000
 // tokens kept: 537 MB in 85 us, 6.3 TB/s, 0.93 of this GPU's copy rate), the
@@ -30,8 +30,14 @@ namespace pa {
 // the mantissa: sums of attention weights spread over about 50 bins, so one
 // pass mostly leaves few enough keys to rank directly).
 constexpr int kBins = 2048;
-constexpr int kCopies = 2;    // of each bin, by lane: equal keys of a warp meet 16 at a time
-constexpr int kList = 64;     // keys ranked directly: two warps' work, less than a pass
+// Copies of each bin, by lane: equal keys of a warp meet 16 at a time.  That
+// does not pay: with one copy (half the counts to clear and read) the whole call
+// takes 105.5 us instead of 106.6 for 64 sequences of 4,000, and 103.1 instead of
+// 105.8 where all sums are equal.
+constexpr int kCopies = 2;
+// Keys ranked directly: two warps' work, less than a pass.  64 sequences of 2,000
+// tokens: 57.3 us with 32, 56.2 with 64, 55.9 with 128; of 4,000: 106.4, 106.6 and 106.9.
+constexpr int kList = 64;
 constexpr int kLongBins = 256, kLongCopies = 8;  // the long rows' four passes of 8 bits
 constexpr int kMoveThreads = 256;
 
@@ -144,6 +150,10 @@ __device__ __forceinline__ void find_bin(int r, const int (&c)[BPT], int bins, i
 // and a warp's are contiguous, so ranks grow with lane, warp and CTA).  A thread's tokens are bits of two masks: those that
 // stay for sure, and those whose key agrees with the cut so far; a pass costs
 // a token only while its bit is in the second.
+// (1,024 threads an SM are 64 registers each.  Three CTAs of 256 threads instead
+// of four, with more registers, are no faster: 64 sequences of 4,000 tokens, 16 a
+// thread, which spill 56 bytes, 333.2 us against 332.4 with nearly all kept; of
+// 2,000, 8 a thread, 58.8 against 56.2)
 template <int THREADS, int K, int CL>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(const EvictArgs A) {
   constexpr int NW = THREADS / 32;
@@ -555,9 +565,12 @@ extern "C" int pa_evict(pa_pool_t p, const float* weights, float* weights_out, c
   cudaStream_t st = as_stream(stream);
   const int span = max_blocks_per_seq * kBlock;
   cudaError_t e = cudaSuccess;
-  // the smallest CTAs that hold a row's keys in registers; from 8,192 tokens on
-  // a cluster of them (32 rows of up to 32K: 4 CTAs each 17 us; 8 CTAs add 8 us,
-  // one CTA that reads its row again for each pass takes 44)
+  // the smallest CTAs that hold a row's keys in registers, 16 a thread at most (64
+  // sequences of up to 6,500 tokens, whole calls: 512 threads of 16 106.6 us, 256
+  // of 32 111.7, 1,024 of 8 109.6); from 8,192 tokens on a cluster of them (32 rows
+  // of up to 32K: 4 CTAs each 17 us; 8 CTAs add 8 us, one CTA that reads its row
+  // again for each pass takes 44).  The lengths are on the device: the width of
+  // the table stands for them
   if (span <= 256 * 8) e = launch_select<256, 8, 1>(A, st);
   else if (span <= 256 * 16) e = launch_select<256, 16, 1>(A, st);
   else if (span <= 512 * 16) e = launch_select<512, 16, 1>(A, st);
@@ -566,11 +579,12 @@ extern "C" int pa_evict(pa_pool_t p, const float* weights, float* weights_out, c
   else if (span <= 512 * 16 * 8) e = launch_select<512, 16, 8>(A, st);
   else evict_select_long_kernel<<<dim3(A.Hkv, A.B), 1024, 0, st>>>(A);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
-  // CTAs of a row group: about 4,096 in all (with 64 sequences of 8 heads 4
-  // each, 7 us less than 1 and 10 less than 16; with 4 long ones 48, against 125
-  // us with 1), at most one a batch of the longest row.  Slices: about 512 CTAs
-  // that move in order (in place, 4 long sequences: 8 slices 60 us, 1 slice 142;
-  // 64 sequences: 165 and 157).  Whole calls, with the selection of then.
+  // CTAs of a row group: about 4,096 in all (64 sequences of 8 heads 106.6 us with
+  // 4 a group, 113.6 with 1, 117.4 with 16; 4 long ones, 63 a group, 41.0-41.4 us
+  // from 16 a group on), at most one a batch of the longest row.  Slices: about
+  // 512 CTAs that move in order (in place, 4 long sequences: 8 slices 53.9 us, 4
+  // slices 61.6; 64 sequences: 1 slice 118.6, 2 slices 111.0, which this rule
+  // does not take).  Whole calls.
   const long long groups = 2ll * A.Hkv * num_seqs;
   int lg = 0;
   while (lg < 3 && (groups << lg) < 512) ++lg;

@@ -234,9 +234,12 @@ extern "C" int pa_rope_append(pa_pool_t p, const void* q, int64_t q_stride, int 
   A.half_vecs = rot_dim / 16;
   A.interleaved = interleaved != 0;
   A.err = p->err;
-  // rows a warp: 4 while that leaves the GPU partly empty (64 tokens of 48 heads:
-  // 2.3 us), then 12, which share a token's angles (8,192 tokens of 48 heads:
-  // 32.9 us, 6.1 TB/s; with 4 rows a warp 1.6 times that, with 16 a little more)
+  // rows a warp: 4 while that leaves the GPU partly empty, then 12, which share a
+  // token's angles.  us with 4 and with 12 rows, captured calls: 48 rows a token
+  // (the switch is at 405 tokens) 64 tokens 2.19 and 2.30, 128 2.43 and 2.35, 400
+  // 3.55 and 3.17, 512 4.31 and 3.59, 8,192 49.1 and 33.0; 16 rows a token (1,216)
+  // 64 tokens 2.23 and 2.40, 400 2.60 and 2.60, 1,024 3.35 and 3.18, 2,048 5.31
+  // and 4.00; 120 rows a token (162) 64 tokens 2.83 and 2.67, 128 3.39 and 3.11
   const long long quads = A.n_tok * ((A.Hq + 2 * A.Hkv + 3) / 4);
   if (quads <= 32ll * sm_count(p->device))
     return launch_rope<1>(A, p->dtype == PA_BF16, as_stream(stream));

@@ -52,7 +52,9 @@
 // idle for about 100); a piece costs 10 us (its queries, the first load, its
 // record).  256 samples of a 16K document, 32 query and 8 kv heads: 125 us for
 // 69 GFLOP and 259 MB, the product on 96 SMs for 100 us and the decode of 188 MB
-// on the others; 64 chats behind 2,048 tokens: 37.8 us for 81 MB.
+// on the others; 64 chats behind 2,048 tokens: 39 us for 81 MB.  18 warps an SM
+// leave 96 registers a thread: the form with two halves and bf16 spills 40 bytes,
+// the others 4 to 12.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
