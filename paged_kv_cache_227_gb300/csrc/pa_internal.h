@@ -26,6 +26,19 @@ struct pa_pool {
   CUtensorMap tmap_half;  // the same view, loaded half a row at a time: boxes of 16 rows x 64 elements
 };
 
+// One 8-bit pool: codes [num_blocks][n_kv_heads][K|V][16][128], so that a
+// (block, head)'s K and V, which a decode reads together, are 4 KiB on end, and
+// exponent bytes [num_blocks][n_kv_heads][K|V].
+struct pa_pool8 {
+  int num_blocks;
+  int n_kv_heads;
+  int dtype;          // PA_E4M3 | PA_INT8
+  int device;
+  uint8_t* codes;     // device
+  uint8_t* exps;      // device
+  long long* err;     // device: [0] = status code, [1] = detail
+};
+
 namespace pa {
 
 constexpr int kBlock = PA_BLOCK_SIZE;     // tokens per block
@@ -59,11 +72,15 @@ int sm_count(int device);
 // memory, so a call from another device is refused before anything is
 // launched).  It also clears a pending non-sticky error of an earlier runtime
 // call, so that the launch checks that follow report this call's launches.
-inline bool on_pool_device(const pa_pool* p) {
+template <class Pool>
+inline bool on_pool_device(const Pool* p) {
   (void)cudaGetLastError();
   int cur = -1;
   return cudaGetDevice(&cur) == cudaSuccess && cur == p->device;
 }
+
+// pa_check and pa_check8: synchronises the stream, reads and clears an error word.
+int check_error_word(long long* err, void* stream, int64_t* detail);
 
 // Wait limit for bounded in-kernel waits, in nanoseconds.
 long long wait_limit_ns();

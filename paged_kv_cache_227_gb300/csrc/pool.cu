@@ -85,6 +85,18 @@ __global__ void copy_blocks_kernel(uint4* k, uint4* v, const int32_t* src, const
   for (int x = threadIdx.x; x < vec_per_block; x += blockDim.x) to[x] = from[x];
 }
 
+int check_error_word(long long* err, void* stream, int64_t* detail) {
+  if (cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) return PA_ERR_CUDA;
+  long long host[2] = {0, 0};
+  if (cudaMemcpy(host, err, sizeof host, cudaMemcpyDeviceToHost) != cudaSuccess) return PA_ERR_CUDA;
+  if (host[0] != 0) {
+    const long long zero[2] = {0, 0};
+    if (cudaMemcpy(err, zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess) return PA_ERR_CUDA;
+  }
+  if (detail) *detail = host[1];
+  return static_cast<int>(host[0]);
+}
+
 }  // namespace pa
 
 using namespace pa;
@@ -181,15 +193,7 @@ int pa_copy_blocks(pa_pool_t p, const int32_t* src, const int32_t* dst, int n, v
 
 int pa_check(pa_pool_t p, void* stream, int64_t* detail) {
   if (!p) return PA_ERR_INVALID;
-  if (cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) return PA_ERR_CUDA;
-  long long host[2] = {0, 0};
-  if (cudaMemcpy(host, p->err, sizeof host, cudaMemcpyDeviceToHost) != cudaSuccess) return PA_ERR_CUDA;
-  if (host[0] != 0) {
-    const long long zero[2] = {0, 0};
-    if (cudaMemcpy(p->err, zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess) return PA_ERR_CUDA;
-  }
-  if (detail) *detail = host[1];
-  return static_cast<int>(host[0]);
+  return check_error_word(p->err, stream, detail);
 }
 
 const char* pa_strerror(int code) {
