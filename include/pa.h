@@ -54,7 +54,13 @@ extern "C" {
 /* Element types.  K/V pools, q, k_new and v_new are FP16 or BF16; the output
  * may also be FP32 (fp32 output isolates the kernel's arithmetic from the
  * final rounding to 16 bits). */
-typedef enum { PA_FP16 = 0, PA_BF16 = 1, PA_FP32 = 2 } pa_dtype;
+typedef enum {
+  PA_FP16 = 0,
+  PA_BF16 = 1,
+  PA_FP32 = 2,
+  PA_E4M3 = 3, /* 8-bit pools only: float, 448 largest */
+  PA_INT8 = 4  /* 8-bit pools only: -127 .. 127         */
+} pa_dtype;
 
 enum {
   PA_OK = 0,
@@ -152,6 +158,22 @@ int pa_rope_append(pa_pool_t pool, const void* q, int64_t q_stride, int n_q_head
                    int n_axes, const uint8_t* axis_of_pair, const float* inv_freq, int rot_dim,
                    int interleaved, const int64_t* slot_mapping, int n_tok, void* q_out,
                    int64_t q_out_stride, void* stream);
+
+/* pa_rope_append with the RMS norm of each query and key head before the
+ * rotation, in the same pass: over a row's 128 dims,
+ *   x_d <- x_d / sqrt(mean(x^2) + eps) * weight_d.
+ *   q_weight, k_weight : device [128] of the pool's dtype, 16-byte aligned, or
+ *                  NULL: rows of that kind are not normed (both NULL is
+ *                  pa_rope_append).
+ *   eps          : finite, >= 0 (else INVALID).
+ * Everything else as for pa_rope_append; value rows are not normed.  fp32
+ * throughout, rounded once. */
+int pa_norm_rope_append(pa_pool_t pool, const void* q, int64_t q_stride, int n_q_heads, const void* k_new,
+                        int64_t k_stride, const void* v_new, int64_t v_stride, const void* q_weight,
+                        const void* k_weight, float eps, const int32_t* positions, int n_axes,
+                        const uint8_t* axis_of_pair, const float* inv_freq, int rot_dim, int interleaved,
+                        const int64_t* slot_mapping, int n_tok, void* q_out, int64_t q_out_stride,
+                        void* stream);
 
 /* ---------------------------------------------------------------------------
  * Decode attention over the paged cache ("Serving" 23.2 and 23.4).
@@ -381,6 +403,97 @@ int pa_evict(pa_pool_t pool, const float* weights, float* weights_out, const int
              int max_blocks_per_seq, const int32_t* dst_tables, int dst_blocks_per_seq,
              const int32_t* seq_lens, const int32_t* keep, int num_seqs, int n_sink, int n_recent,
              int32_t* seq_lens_out, int32_t* kept, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The cache in 8 bits: half the memory of a 16-bit pool, and half of what a
+ * decode reads.  A pool holds codes [num_blocks][n_kv_heads][2][16][128] (K, then
+ * V, of each (block, kv head) on end), PA_E4M3 or PA_INT8, and an exponent
+ * byte [num_blocks][n_kv_heads][2] for each such tile: a code c stands for
+ *   c * 2^(exponent - 127), for NaN where the exponent is 255.
+ * Scales are powers of two, so scaling is exact and a value is rounded once.  The
+ * calls below that write a tile give it the smallest exponent >= 1 whose largest
+ * code (448, 127) holds the tile's largest magnitude: e4m3 is then off by at most
+ * 2^-4 of a value (or 2^-10 of the scale), int8 by half a scale, at most 2^-7 of
+ * the tile's largest magnitude.  A row with an infinity or a NaN makes the
+ * tile's exponent 255.  The other calls of this library take 16-bit pools only.
+ * ------------------------------------------------------------------------- */
+typedef struct pa_pool8* pa_pool8_t;
+
+/* Bytes of the K (or V) codes alone; 0 for invalid or unsupported sizes. */
+size_t pa_pool8_bytes(int num_blocks, int block_size, int n_kv_heads, int d_head, int dtype);
+/* As pa_pool_create and pa_pool_destroy; dtype is PA_E4M3 or PA_INT8.  Codes and
+ * exponents start at zero. */
+int pa_pool8_create(int num_blocks, int block_size, int n_kv_heads, int d_head, int dtype, pa_pool8_t* out);
+int pa_pool8_destroy(pa_pool8_t pool);
+/* Device addresses of the codes and the exponents (either pointer may be NULL). */
+int pa_pool8_info(pa_pool8_t pool, void** codes, void** exponents);
+/* pa_check for an 8-bit pool's error word. */
+int pa_check8(pa_pool8_t pool, void* stream, int64_t* detail);
+
+/* Cache write in 8 bits; k_new and v_new [n_tok][n_kv_heads][128] of dtype
+ * PA_FP16 or PA_BF16, slots as for pa_cache_append.  A run is a stretch of
+ * consecutive rows of the call whose slots follow each other inside one block:
+ * what a sequence's next tokens are, however many.  For each kv head, K and V
+ * apart:
+ *  - a run that starts at a block's first row starts the block afresh: its rows
+ *    alone set the scale (the codes of the rows behind it stay as they are, and
+ *    what they stood for is lost);
+ *  - any other run keeps the block's scale if that holds its rows too; if not, the
+ *    scale grows and the codes of the block's other rows are rounded to it.
+ * The rows of one block have to be one run of the call: a block that two runs
+ * name, or a slot named twice, ends up with the codes and the scale of either
+ * (no other block is touched).  Slots out of range are skipped and reported by
+ * pa_check8. */
+int pa_cache_append8(pa_pool8_t pool, int dtype, const void* k_new, const void* v_new, const int64_t* slot_mapping,
+                     int n_tok, void* stream);
+
+/* pa_norm_rope_append into an 8-bit pool: query rows to q_out in the rows' dtype
+ * (PA_FP16 or PA_BF16, weights too), K rows normed and turned in fp32, then K and
+ * V rows written as pa_cache_append8 writes them, rounded once. */
+int pa_norm_rope_append8(pa_pool8_t pool, int dtype, const void* q, int64_t q_stride, int n_q_heads,
+                         const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                         const void* q_weight, const void* k_weight, float eps, const int32_t* positions,
+                         int n_axes, const uint8_t* axis_of_pair, const float* inv_freq, int rot_dim,
+                         int interleaved, const int64_t* slot_mapping, int n_tok, void* q_out,
+                         int64_t q_out_stride, void* stream);
+
+/* Decode attention over an 8-bit pool (the balanced split of pa_decode_split):
+ *   out[i][h] = softmax(scale * K_i q[i][h]) V_i
+ * over the values that the codes stand for.  q [num_seqs][n_q_heads][128] of
+ * q_dtype PA_FP16 or PA_BF16; block_tables, seq_lens, out as for pa_decode.  A
+ * head's query elements below 2^-28 of its largest may lose bits (bf16); weights
+ * are carried to 2^-22 of themselves or 2^-35 of the row's largest, sums in
+ * fp32.  Codes and exponents past a sequence's end may be anything.  A block id
+ * out of range counts as not attended (reported by pa_check8).  n_q_heads /
+ * n_kv_heads <= 8, num_seqs <= 4096, max_blocks_per_seq <= PA_MAX_WALKED_BLOCKS,
+ * (max_blocks_per_seq + 1) times num_seqs or n_kv_heads below 2^31 - 1 and times
+ * both below 2^41 (else UNSUPPORTED); a finite scale (else INVALID).  workspace:
+ * device, >= pa_decode8_workspace_bytes(...), 256-byte aligned, caller-owned; its
+ * contents on entry do not matter, and calls that share one must not overlap on
+ * the GPU.  The result does not depend on timing. */
+size_t pa_decode8_workspace_bytes(pa_pool8_t pool, int num_seqs, int n_q_heads, int max_blocks_per_seq);
+int pa_decode8(pa_pool8_t pool, const void* q, int q_dtype, const int32_t* block_tables, int max_blocks_per_seq,
+               const int32_t* seq_lens, int num_seqs, int n_q_heads, float scale, void* out, int out_dtype,
+               void* workspace, size_t workspace_bytes, void* stream);
+
+/* pa_copy_blocks for an 8-bit pool (codes and exponents). */
+int pa_copy_blocks8(pa_pool8_t pool, const int32_t* src, const int32_t* dst, int n, void* stream);
+
+/* Pages from a 16-bit pool into an 8-bit one and back, blocks src[j] to dst[j], j <
+ * n (device int32), all kv heads, K and V: a paused sequence parked in half the
+ * memory, a prompt's blocks moved into an 8-bit cache.  The pools have the same
+ * n_kv_heads and device (else INVALID).
+ *   rows : device int32 [n], how many rows of block j count (a partial last block:
+ *          what is behind its end then neither enters the scale nor is written;
+ *          out of range is clamped and reported), or NULL: all 16.
+ * To 8 bits each tile gets its own scale, as a block that is started afresh; back,
+ * code times scale is rounded to the pool's dtype, a value past its largest number
+ * to that number.  Destinations are distinct (a block named twice gets either).
+ * Block ids out of range are skipped and reported by pa_check8 on pool8. */
+int pa_quantize_blocks(pa_pool_t pool, const int32_t* src, pa_pool8_t pool8, const int32_t* dst,
+                       const int32_t* rows, int n, void* stream);
+int pa_dequantize_blocks(pa_pool8_t pool8, const int32_t* src, pa_pool_t pool, const int32_t* dst, int n,
+                         void* stream);
 
 /* Split-KV decode that allocates nothing (the pages have no counterpart; this
  * is a deployment convenience).  Some callers cannot call cudaMalloc at the

@@ -15,7 +15,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpagedattn.so")
 
-PA_FP16, PA_BF16, PA_FP32 = 0, 1, 2
+PA_FP16, PA_BF16, PA_FP32, PA_E4M3, PA_INT8 = 0, 1, 2, 3, 4
 PA_OK = 0
 PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_OOM = -1, -2, -3
 PA_ERR_CUDA, PA_ERR_DEVICE_CHECK, PA_ERR_TIMEOUT = -4, -5, -6
@@ -25,6 +25,7 @@ BLOCK_SIZE, HEAD_DIM, MAX_GROUP = 16, 128, 8
 
 _DTYPE_CODE = {torch.float16: PA_FP16, torch.bfloat16: PA_BF16, torch.float32: PA_FP32}
 _CODE_DTYPE = {v: k for k, v in _DTYPE_CODE.items()}
+_DTYPE8_CODE = {torch.float8_e4m3fn: PA_E4M3, torch.int8: PA_INT8}
 
 
 class PagedAttentionError(RuntimeError):
@@ -48,6 +49,21 @@ def _load():
         "pa_pool_shape": (i32, [vp] + [ctypes.POINTER(i32)] * 4),
         "pa_cache_append": (i32, [vp, vp, vp, vp, i32, vp]),
         "pa_rope_append": (i32, [vp, vp, i64, i32, vp, i64, vp, i64, vp, i32, vp, vp, i32, i32, vp, i32, vp, i64, vp]),
+        "pa_norm_rope_append": (i32, [vp, vp, i64, i32, vp, i64, vp, i64, vp, vp, f32, vp, i32, vp, vp, i32, i32, vp, i32,
+                                      vp, i64, vp]),
+        "pa_pool8_bytes": (sz, [i32, i32, i32, i32, i32]),
+        "pa_pool8_create": (i32, [i32, i32, i32, i32, i32, ctypes.POINTER(vp)]),
+        "pa_pool8_destroy": (i32, [vp]),
+        "pa_pool8_info": (i32, [vp, ctypes.POINTER(vp), ctypes.POINTER(vp)]),
+        "pa_check8": (i32, [vp, vp, ctypes.POINTER(i64)]),
+        "pa_cache_append8": (i32, [vp, i32, vp, vp, vp, i32, vp]),
+        "pa_norm_rope_append8": (i32, [vp, i32, vp, i64, i32, vp, i64, vp, i64, vp, vp, f32, vp, i32, vp, vp, i32, i32, vp,
+                                       i32, vp, i64, vp]),
+        "pa_decode8_workspace_bytes": (sz, [vp, i32, i32, i32]),
+        "pa_decode8": (i32, [vp, vp, i32, vp, i32, vp, i32, i32, f32, vp, i32, vp, sz, vp]),
+        "pa_copy_blocks8": (i32, [vp, vp, vp, i32, vp]),
+        "pa_quantize_blocks": (i32, [vp, vp, vp, vp, vp, i32, vp]),
+        "pa_dequantize_blocks": (i32, [vp, vp, vp, vp, i32, vp]),
         "pa_decode_weights_workspace_bytes": (sz, [vp, i32, i32, i32]),
         "pa_decode_weights": (i32, [vp, vp, vp, i32, vp, i32, i32, f32, vp, i32, vp, f32, vp, sz, vp]),
         "pa_decode_shared_workspace_bytes": (sz, [vp, i32, i32, i32, i32]),
@@ -133,15 +149,16 @@ def _need(t, name, dtype=None, device=True):
 
 
 class _PoolHandle:
-    """Destroys its pa_pool_t when nothing refers to it any more: the Pool, and
-    every tensor that views its memory."""
+    """Destroys its pa_pool_t (or pa_pool8_t) when nothing refers to it any more:
+    the Pool, and every tensor that views its memory."""
 
-    def __init__(self):
+    def __init__(self, destroy=lib.pa_pool_destroy):
         self.ptr = ctypes.c_void_p()
+        self._destroy = destroy
 
     def destroy(self):
         if self.ptr:
-            lib.pa_pool_destroy(self.ptr)
+            self._destroy(self.ptr)
             self.ptr = ctypes.c_void_p()
 
     def __del__(self):
@@ -190,6 +207,39 @@ class Pool:
     def close(self):
         if self._h.ptr:
             self.k = self.v = None
+            self._h.destroy()
+
+
+class Pool8:
+    """Owns one pa_pool8_t, a cache in 8 bits: codes k and v [num_blocks][n_kv_heads]
+    [16][128] (torch.float8_e4m3fn or torch.int8; strided views, a tile's K and
+    V lie on end) and their scales k_scale and v_scale [num_blocks][n_kv_heads]
+    (torch.float8_e8m0fnu, powers of two): a code stands for code * scale.
+    close() and dropping it: as for Pool."""
+
+    def __init__(self, num_blocks, n_kv_heads, dtype=torch.float8_e4m3fn, block_size=BLOCK_SIZE, d_head=HEAD_DIM):
+        self._h = _PoolHandle(lib.pa_pool8_destroy)
+        code = lib.pa_pool8_create(num_blocks, block_size, n_kv_heads, d_head, _DTYPE8_CODE[dtype],
+                                   ctypes.byref(self._h.ptr))
+        _check(code, "pa_pool8_create")
+        self.num_blocks, self.n_kv_heads, self.dtype = num_blocks, n_kv_heads, dtype
+        self.device = torch.device("cuda", torch.cuda.current_device())
+        codes, exps = ctypes.c_void_p(), ctypes.c_void_p()
+        _check(lib.pa_pool8_info(self._h.ptr, ctypes.byref(codes), ctypes.byref(exps)), "pa_pool8_info")
+        shape = (num_blocks, n_kv_heads, 2, BLOCK_SIZE, HEAD_DIM)
+        kv = torch.as_tensor(_CudaArray(codes.value, shape, "|u1", self._h), device=self.device).view(dtype)
+        scale = torch.as_tensor(_CudaArray(exps.value, shape[:3], "|u1", self._h), device=self.device)
+        scale = scale.view(torch.float8_e8m0fnu)
+        self.k, self.v = kv[:, :, 0], kv[:, :, 1]
+        self.k_scale, self.v_scale = scale[:, :, 0], scale[:, :, 1]
+
+    @property
+    def handle(self):
+        return self._h.ptr
+
+    def close(self):
+        if self._h.ptr:
+            self.k = self.v = self.k_scale = self.v_scale = None
             self._h.destroy()
 
 
@@ -368,9 +418,10 @@ def _raw_stream(pool, stream):
     return torch._C._cuda_getCurrentRawStream(pool.device.index) if stream is None else stream.cuda_stream
 
 
-def _decode_at(pool, q, block_tables, seq_lens, out):
-    """Checks of a decode's tensors (as _decode_args); their addresses and sizes."""
-    qa = _at(pool, q, "q", pool.dtype)
+def _decode_at(pool, q, block_tables, seq_lens, out, dtype=None):
+    """Checks of a decode's tensors (as _decode_args), q of `dtype` or the pool's;
+    their addresses and sizes."""
+    qa = _at(pool, q, "q", pool.dtype if dtype is None else dtype)
     ta = _at(pool, block_tables, "block_tables", torch.int32)
     la = _at(pool, seq_lens, "seq_lens", torch.int32)
     code = _DTYPE_CODE.get(out.dtype) if isinstance(out, torch.Tensor) else 0
@@ -397,11 +448,11 @@ def _workspace(nbytes, what, device, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _heads(pool, t, name, shape):
-    """Checks [n_tok][n_heads][128] rows of the pool's type with contiguous
-    heads; their address and token stride in elements."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is pool.dtype and t.device == pool.device):
-        _refuse(pool, t, name, pool.dtype)
+def _heads(pool, dtype, t, name, shape):
+    """Checks [n_tok][n_heads][128] rows of `dtype` with contiguous heads; their
+    address and token stride in elements."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == pool.device):
+        _refuse(pool, t, name, dtype)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     tok, head, dim = t.stride()
@@ -410,14 +461,9 @@ def _heads(pool, t, name, shape):
     return t.data_ptr(), (tok if shape[0] > 1 else shape[1] * HEAD_DIM)
 
 
-def pa_rope_append(pool, q, k_new, v_new, positions, inv_freq, axis_of_pair, slot_mapping, q_out, interleaved=False,
-                   stream=None):
-    """Rotary positions of one or several axes on new tokens' q and k, with the
-    cache write of k and v (see include/pa.h).  q and q_out [n][Hq][128], k_new
-    and v_new [n][Hkv][128] with any token stride (slices of a fused projection
-    work), positions int32 [n_axes][n], inv_freq fp32 [rot_dim/2],
-    axis_of_pair: rot_dim/2 ints on the host (bytes are taken as they are),
-    slot_mapping int64 [n].  q_out may be q."""
+def _rope_at(pool, dtype, q, k_new, v_new, positions, inv_freq, axis_of_pair, slot_mapping, q_out):
+    """Checks of the rotary appends' tensors, rows of `dtype`; the C calls' arguments
+    up to the norms, and behind them."""
     sa = _at(pool, slot_mapping, "slot_mapping", torch.int64)
     pos = _at(pool, positions, "positions", torch.int32)
     fa = _at(pool, inv_freq, "inv_freq", torch.float32)
@@ -428,18 +474,147 @@ def pa_rope_append(pool, q, k_new, v_new, positions, inv_freq, axis_of_pair, slo
         raise ValueError("q must be [n_tok][Hq][128]")
     Hq = q.shape[1]
     q_rows, kv_rows = (n, Hq, HEAD_DIM), (n, pool.n_kv_heads, HEAD_DIM)
-    qa, qs = _heads(pool, q, "q", q_rows)
-    ka, ks = _heads(pool, k_new, "k_new", kv_rows)
-    va, vs = _heads(pool, v_new, "v_new", kv_rows)
-    oa, os_ = _heads(pool, q_out, "q_out", q_rows)
+    qa, qs = _heads(pool, dtype, q, "q", q_rows)
+    ka, ks = _heads(pool, dtype, k_new, "k_new", kv_rows)
+    va, vs = _heads(pool, dtype, v_new, "v_new", kv_rows)
+    oa, os_ = _heads(pool, dtype, q_out, "q_out", q_rows)
     # (ValueError outside 0 .. 255; an array's own bytes are not its numbers)
     axes = bytes(axis_of_pair if isinstance(axis_of_pair, (list, tuple, bytes, bytearray)) else list(axis_of_pair))
     if positions.dim() != 2 or positions.shape[1] != n:
         raise ValueError("positions must be [n_axes][n_tok]")
     if inv_freq.shape != (len(axes),):
         raise ValueError("inv_freq and axis_of_pair must have rot_dim / 2 entries each")
-    _check(lib.pa_rope_append(pool.handle, qa, qs, Hq, ka, ks, va, vs, pos, positions.shape[0], axes, fa, 2 * len(axes),
-                              1 if interleaved else 0, sa, n, oa, os_, _raw_stream(pool, stream)), "pa_rope_append")
+    return (qa, qs, Hq, ka, ks, va, vs), (pos, positions.shape[0], axes, fa, 2 * len(axes)), (sa, n, oa, os_)
+
+
+def pa_rope_append(pool, q, k_new, v_new, positions, inv_freq, axis_of_pair, slot_mapping, q_out, interleaved=False,
+                   stream=None):
+    """Rotary positions of one or several axes on new tokens' q and k, with the
+    cache write of k and v (see include/pa.h).  q and q_out [n][Hq][128], k_new
+    and v_new [n][Hkv][128] with any token stride (slices of a fused projection
+    work), positions int32 [n_axes][n], inv_freq fp32 [rot_dim/2],
+    axis_of_pair: rot_dim/2 ints on the host (bytes are taken as they are),
+    slot_mapping int64 [n].  q_out may be q."""
+    rows, turn, to = _rope_at(pool, pool.dtype, q, k_new, v_new, positions, inv_freq, axis_of_pair, slot_mapping, q_out)
+    _check(lib.pa_rope_append(pool.handle, *rows, *turn, 1 if interleaved else 0, *to, _raw_stream(pool, stream)),
+           "pa_rope_append")
+
+
+def _norm_at(pool, dtype, weight, name):
+    if weight is None:
+        return None
+    a = _at(pool, weight, name, dtype)
+    if weight.shape != (HEAD_DIM,):
+        raise ValueError(f"{name} must be [128]")
+    return a
+
+
+def pa_norm_rope_append(pool, q, k_new, v_new, q_weight, k_weight, positions, inv_freq, axis_of_pair, slot_mapping, q_out,
+                        eps=1e-6, interleaved=False, stream=None):
+    """pa_rope_append with the RMS norm of each q and k head before the rotation
+    (see include/pa.h): q_weight and k_weight [128] of the pool's dtype, or None:
+    rows of that kind are not normed."""
+    rows, turn, to = _rope_at(pool, pool.dtype, q, k_new, v_new, positions, inv_freq, axis_of_pair, slot_mapping, q_out)
+    _check(lib.pa_norm_rope_append(pool.handle, *rows, _norm_at(pool, pool.dtype, q_weight, "q_weight"),
+                                   _norm_at(pool, pool.dtype, k_weight, "k_weight"), float(eps), *turn,
+                                   1 if interleaved else 0, *to, _raw_stream(pool, stream)), "pa_norm_rope_append")
+
+
+def _row_dtype(t, name):
+    """The type of 16-bit rows next to an 8-bit pool."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float16:
+        raise TypeError(f"{name} must be fp16 or bf16, got {t.dtype}")
+    return t.dtype
+
+
+def pa_norm_rope_append8(pool, q, k_new, v_new, q_weight, k_weight, positions, inv_freq, axis_of_pair, slot_mapping, q_out,
+                         eps=1e-6, interleaved=False, stream=None):
+    """pa_norm_rope_append into a Pool8 (see include/pa.h for how blocks get their
+    scales): rows, weights and q_out all fp16 or all bf16.  The rows of one block
+    are consecutive, in the order of their slots."""
+    dtype = _row_dtype(q, "q")
+    rows, turn, to = _rope_at(pool, dtype, q, k_new, v_new, positions, inv_freq, axis_of_pair, slot_mapping, q_out)
+    _check(lib.pa_norm_rope_append8(pool.handle, _DTYPE_CODE[dtype], *rows, _norm_at(pool, dtype, q_weight, "q_weight"),
+                                    _norm_at(pool, dtype, k_weight, "k_weight"), float(eps), *turn,
+                                    1 if interleaved else 0, *to, _raw_stream(pool, stream)), "pa_norm_rope_append8")
+
+
+def pa_cache_append8(pool, k_new, v_new, slot_mapping, stream=None):
+    """Writes k_new and v_new [n][Hkv][128] (fp16 or bf16) into a Pool8 at
+    slot_mapping int64 [n] (see include/pa.h)."""
+    dtype = _row_dtype(k_new, "k_new")
+    ka, va = _at(pool, k_new, "k_new", dtype), _at(pool, v_new, "v_new", dtype)
+    sa = _at(pool, slot_mapping, "slot_mapping", torch.int64)
+    n = slot_mapping.numel()
+    if k_new.shape != (n, pool.n_kv_heads, HEAD_DIM) or v_new.shape != k_new.shape:
+        raise ValueError("k_new/v_new must be [n_tok][n_kv_heads][128]")
+    _check(lib.pa_cache_append8(pool.handle, _DTYPE_CODE[dtype], ka, va, sa, n, _raw_stream(pool, stream)),
+           "pa_cache_append8")
+
+
+def decode8_workspace_for(pool, q, block_tables, stream=None):
+    """Workspace of pa_decode8 for these sizes."""
+    n = lib.pa_decode8_workspace_bytes(pool.handle, q.shape[0], q.shape[1], block_tables.shape[1])
+    return _workspace(n, "pa_decode8_workspace_bytes", pool.device, stream)
+
+
+def pa_decode8(pool, q, block_tables, seq_lens, scale, out, workspace=None, stream=None):
+    """Decode attention over a Pool8: q [B][Hq][128] fp16 or bf16, out [B][Hq][128]
+    of fp16, bf16 or fp32, tables and lengths as for pa_decode."""
+    dtype = _row_dtype(q, "q")
+    qa, ta, la, oa, code, B, Hq, W = _decode_at(pool, q, block_tables, seq_lens, out, dtype)
+    if workspace is None:
+        workspace = decode8_workspace_for(pool, q, block_tables, stream)
+    _check(lib.pa_decode8(pool.handle, qa, _DTYPE_CODE[dtype], ta, W, la, B, Hq, float(scale), oa, code,
+                          _at(pool, workspace, "workspace", torch.uint8), workspace.numel(), _raw_stream(pool, stream)),
+           "pa_decode8")
+
+
+def _block_ids(pool, t, name, n=None):
+    a = _at(pool, t, name, torch.int32)
+    if t.dim() != 1 or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be [n], as long as src")
+    return a
+
+
+def _both_pools(pool, pool8):
+    if not isinstance(pool8, Pool8) or isinstance(pool, Pool8):
+        raise TypeError("one Pool and one Pool8 are needed")
+
+
+def pa_copy_blocks8(pool, src, dst, stream=None):
+    """pa_copy_blocks for a Pool8."""
+    sa = _block_ids(pool, src, "src")
+    _check(lib.pa_copy_blocks8(pool.handle, sa, _block_ids(pool, dst, "dst", src.numel()), src.numel(),
+                               _raw_stream(pool, stream)), "pa_copy_blocks8")
+
+
+def pa_quantize_blocks(pool, src, pool8, dst, rows=None, stream=None):
+    """Blocks src of a Pool into blocks dst of a Pool8; rows int32 [n]: how many
+    rows of each count (None: all 16; see include/pa.h)."""
+    _both_pools(pool, pool8)
+    sa = _block_ids(pool8, src, "src")
+    da = _block_ids(pool8, dst, "dst", src.numel())
+    ra = None if rows is None else _block_ids(pool8, rows, "rows", src.numel())
+    _check(lib.pa_quantize_blocks(pool.handle, sa, pool8.handle, da, ra, src.numel(), _raw_stream(pool8, stream)),
+           "pa_quantize_blocks")
+
+
+def pa_dequantize_blocks(pool8, src, pool, dst, stream=None):
+    """Blocks src of a Pool8 into blocks dst of a Pool."""
+    _both_pools(pool, pool8)
+    sa = _block_ids(pool8, src, "src")
+    _check(lib.pa_dequantize_blocks(pool8.handle, sa, pool.handle, _block_ids(pool8, dst, "dst", src.numel()), src.numel(),
+                                    _raw_stream(pool8, stream)), "pa_dequantize_blocks")
+
+
+def pa_check8(pool, stream=None):
+    """pa_check for a Pool8."""
+    detail = ctypes.c_int64()
+    code = lib.pa_check8(pool.handle, _stream(stream), ctypes.byref(detail))
+    return code, detail.value
 
 
 def shared_workspace_for(pool, q, block_tables, prefix_blocks, stream=None):

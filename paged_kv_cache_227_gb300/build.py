@@ -15,7 +15,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libpagedattn.so")
 OBJDIR = os.path.join(HERE, "_build")
 
-CU_SOURCES = ["pool.cu", "append.cu", "decode.cu", "rope.cu", "evict.cu", "shared.cu"]
+CU_SOURCES = ["pool.cu", "append.cu", "decode.cu", "rope.cu", "evict.cu", "shared.cu", "pool8.cu", "append8.cu",
+              "decode8.cu"]
 CPP_SOURCES = ["alloc.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -31,7 +32,8 @@ def _nvcc():
 def _sources():
     srcs = [os.path.join(CSRC, f) for f in CU_SOURCES + CPP_SOURCES]
     deps = srcs + [os.path.join(CSRC, "pa_internal.h"), os.path.join(CSRC, "device_utils.cuh"),
-                   os.path.join(CSRC, "shared_plan.cuh"), os.path.join(INCLUDE, "pa.h")]
+                   os.path.join(CSRC, "shared_plan.cuh"), os.path.join(CSRC, "rope_rows.cuh"),
+                   os.path.join(CSRC, "codes8.cuh"), os.path.join(INCLUDE, "pa.h")]
     return srcs, deps
 
 
