@@ -13,24 +13,24 @@
 // that a cut divides leaves a record a piece, which a second kernel joins by
 // log-sum-exp, in their order.
 //
-// A lane copies exactly the bytes that it will read (cp.async, 16 bytes each),
-// so the ring needs no barrier: the lane's own wait is enough.  Which bytes those
-// are follows from the operands of mma.sync m16n8k16, with the query heads as
-// the rows of both products:
-//   scores  S (heads x tokens) = Q K^T: as an operand, lane (g, c) = (lane / 4,
-//           lane % 4) holds token g's dims; any 32 will do as long as Q's lanes
-//           hold the same ones, so it takes bytes 16c .. 16c + 15 and 64 + 16c ..
-//           of the rows of tokens g and g + 8;
-//   values  O (heads x dims) = P V: the scores' fragment, as it comes out, is P's
-//           operand; lane (g, c) holds tokens 2c, 2c + 1, 2c + 8, 2c + 9 of
-//           column g, and the columns may stand for any dims: dims 16g .. 16g +
-//           15, 16 bytes a token.
-// A head fills 8 of the product's 16 rows.  In the scores the other 8 stay zero;
-// in the values they carry what rounding the weights to 16 bits left, so high
-// and low half (23 bits) go through one product.  Codes become fp16 exactly, q in
-// bf16 too after a power of two per head (its elements 2^28 below the largest
-// lose bits), and the tile's scales are applied in fp32: K's to the scores, V's
-// to the tile's 16-token product as it is added to O.
+// A tile is one TMA box, 32 rows of 128 bytes in the 128-byte swizzle, so that the
+// operand loads below meet no bank conflict.  Per tile, with mma.sync m16n8k16 (16
+// tokens against at most 8 heads are far below what tcgen05 takes) and the codes
+// as fp16, which is exact:
+//   scores  S (tokens x heads) = K Q^T: ldmatrix hands lane (g, c) = (lane / 4,
+//           lane % 4) four codes of token g (g + 8) a matrix, dims 16 j + 4c .. + 3;
+//           Q's lanes hold the same dims in the same order.
+//   values  O (dims x heads) = V^T P: lane (g, c) reads 16 bytes, dims 16 g .., of tokens
+//           2c, 2c + 1, 2c + 8, 2c + 9, pairs the tokens' bytes and has two dims a
+//           product as its rows; no transposition but that of P (movmatrix).
+// The weights P go in as a high and a low 16-bit half (22 bits): with up to 4 heads
+// the columns 4 .. 7 repeat the heads and carry the low halves, with more the
+// product is made twice.
+// Scales: K's multiplies the scores.  V's, a power of two 2^ev, is carried by O: O
+// is kept in units of 2^E, E the largest ev so far, and the weights are multiplied
+// by 2^(ev - E) before they are rounded, so the products add up in the accumulators
+// themselves; a tile with ev < E - 4, whose weights would lose bits that way,
+// is multiplied by itself and added in fp32.
 #include <atomic>
 
 #include "codes8.cuh"
@@ -38,58 +38,97 @@
 
 namespace pa {
 
-constexpr int kWarps8 = 16;    // warps of a CTA, one CTA an SM
-constexpr int kStages8 = 3;    // tiles in flight of a warp: 192 KiB an SM
+#ifndef W8
+#define W8 12
+#define S8 3
+#endif
+constexpr int kWarps8 = W8;    // warps of a CTA, one CTA an SM
+constexpr int kStages8 = S8;   // tiles in flight of a warp
 constexpr int kSeqs8 = 4096;   // sequences of a call (their prefix lives in shared memory)
 constexpr int kMinUnits8 = 2;  // smallest range of a warp
+constexpr int kWholeBlocks8 = 8 * kWarps8;  // widest table of the plan with a CTA a segment
 constexpr float kLog2e8 = 1.4426950408889634f;
 // The running maximum moves when a score passes it by 2^4; weights are carried
 // at 2^11 times their size, below 2^15, so that the low half's smallest step
-// (2^-24) is 2^-35 of the row's largest weight.
+// (2^-24) is 2^-35 of the row's largest weight, 2^-31 with V's scales.
 constexpr float kMove8 = 4.f, kUp8 = 11.f;
+constexpr int kNear8 = 4;
 
-// Record of a piece: O as 8 float4 a lane (number k * 32 + lane: head lane / 4,
-// dims 32 (lane % 4) + 4 k ..), then the heads' maxima (log2 units) and sums.
-constexpr int kRec8 = 8 * 32 * 4 + 2 * 8;
+// Record of a piece: O as float4 number k * kLanes + r, then the heads' maxima (log2
+// units) and sums.  Lane (g, c) of a warp has k = 4e + q: head 2c + e, dims 16g + 4q
+// .. + 3; with up to 4 heads only c < 2 do (kLanes = 16).
+template <bool kTwice>
+struct Record8 {
+  static constexpr int kLanes = kTwice ? 16 : 32;
+  static constexpr int kVecs = 8 * kLanes;
+  static constexpr int kFloats = 4 * kVecs + 16;
+  static constexpr int kBytes = 4 * kFloats;
+  static constexpr int kParts = kVecs / 32;  // warps that take a float4 a lane
+  float4 o[kVecs];
+  float m[8], l[8];
+  __device__ static int place(int k, int g, int c) { return k * kLanes + (kTwice ? 2 * g + c : 4 * g + c); }
+  __device__ static int head(int f) { return 2 * (f & (kTwice ? 1 : 3)) + (f / kLanes >> 2); }
+  __device__ static int dim(int f) { return 16 * ((f % kLanes) / (kTwice ? 2 : 4)) + 4 * (f / kLanes & 3); }
+};
 
 struct Decode8Args {
-  const uint8_t* codes;
+  CUtensorMap tmap;
   const uint8_t* exps;
   const uint16_t* q;          // [B][Hq][128]
   const int32_t* tables;
   const int32_t* seq_lens;
   void* out;
-  float* rec;
+  void* rec;
   long long* err;
   int num_blocks, max_blocks;
   int B, Hq, Hkv, G;
   int out_dtype;
-  int units;                  // warps that the ranges are cut for
+  int whole;                  // a CTA a segment, instead of equal ranges
   float qscale;               // scale * log2(e)
+  long long wait_limit_ns;
 };
 
 // A segment (i, h) is one unit for its start (its query rows, its record) and
 // one for each of its tiles; pfx[i] counts the units of one kv head before
-// sequence i.
-struct Ranges8 {
-  long long per;
-  __device__ Ranges8(const Decode8Args& A, const int* pfx) {
-    per = (static_cast<long long>(A.Hkv) * pfx[A.B] + A.units - 1) / A.units;
-    if (per < kMinUnits8) per = kMinUnits8;
-  }
+// sequence i.  A CTA's range is cut into equal ones for its warps.
+struct Place8 {
+  int i, h, j;  // tile j of the segment, -1: the unit that starts it
 };
+__device__ __forceinline__ Place8 place8(const Decode8Args& A, const int* pfx, long long u) {
+  int lo = 0, hi = A.B - 1;  // the last sequence that starts at or before u (never an empty one)
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (static_cast<long long>(A.Hkv) * pfx[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  const int r = static_cast<int>(u - static_cast<long long>(A.Hkv) * pfx[lo]), cnt = pfx[lo + 1] - pfx[lo];
+  const int h = r / cnt;
+  return {lo, h, r - h * cnt - 1};
+}
+// Units of segment (i, h): [s0, s0 + cnt).
+struct Segment8 {
+  long long s0;
+  int cnt;
+  __device__ Segment8(const Decode8Args& A, const int* pfx, int i, int h)
+      : s0(static_cast<long long>(A.Hkv) * pfx[i] + static_cast<long long>(h) * (pfx[i + 1] - pfx[i])),
+        cnt(pfx[i + 1] - pfx[i]) {}
+};
+// Units of a warp in the balanced split over `ctas` CTAs.
+__device__ __forceinline__ long long per_warp8(const Decode8Args& A, const int* pfx, int ctas) {
+  const long long warps = static_cast<long long>(ctas) * kWarps8;
+  const long long per = (static_cast<long long>(A.Hkv) * pfx[A.B] + warps - 1) / warps;
+  return per < kMinUnits8 ? kMinUnits8 : per;
+}
 
-// pfx[0 .. B] and, with lens, the clamped lengths; a whole CTA.
-__device__ void prefix8(const Decode8Args& A, int* pfx, int* lens, bool report) {
+__device__ __forceinline__ int length8(const Decode8Args& A, int i) {
+  return min(max(A.seq_lens[i], 0), A.max_blocks * kBlock);
+}
+
+// pfx[0 .. B], by a whole CTA.
+__device__ void prefix8(const Decode8Args& A, int* pfx, bool report) {
   const int lane = threadIdx.x & 31;
-  const int cap = A.max_blocks * kBlock;
   for (int i = threadIdx.x; i < A.B; i += blockDim.x) {
-    int L = A.seq_lens[i];
-    if (L < 0 || L > cap) {
-      if (report) record_error(A.err, PA_ERR_DEVICE_CHECK, L);
-      L = L < 0 ? 0 : cap;
-    }
-    lens[i] = L;
+    const int L = length8(A, i);
+    if (report && L != A.seq_lens[i]) record_error(A.err, PA_ERR_DEVICE_CHECK, A.seq_lens[i]);
     pfx[i + 1] = L ? 1 + (L + kBlock - 1) / kBlock : 0;
   }
   __syncthreads();
@@ -111,16 +150,24 @@ __device__ void prefix8(const Decode8Args& A, int* pfx, int* lens, bool report) 
   __syncthreads();
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t to, const uint8_t* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ uint4 lds16(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
   return v;
+}
+__device__ __forceinline__ uint4 ldmatrix4(uint32_t at) {
+  uint4 v;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t transposed8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -129,55 +176,56 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The K and V tile number `tile` of the pool into shared memory.
+__device__ __forceinline__ void load_tile8(uint32_t to, const CUtensorMap* map, int tile, uint32_t bar) {
+  const int z = 0;
+  mbar_arrive_expect_tx(bar, kPair8);
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3}], [%4];" ::"r"(to),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(z), "r"(tile), "r"(bar)
+      : "memory");
+}
 
-// A lane's view of 32 units of the warp's range, one a lane: its tile's sequence,
-// kv head, number in the sequence (-1: the unit starts a segment, or is past the
-// range), place in the pool (-1: none, or out of range) and scales.
+// A lane's view of 32 units of the warp's range, one a lane: the tile's place in
+// the pool (-1: none), K's scale, and packed: how many of its tokens count (0: no
+// tile), whether a piece starts with the unit (kNew8) and V's exponent from bit 8 on.
+constexpr int kNew8 = 32;
 struct Window8 {
-  int i, h, j, tile;
-  float ks, vs;
+  int tile, what;
+  float ks;
 };
-__device__ __forceinline__ Window8 window8(const Decode8Args& A, const int* pfx, long long u, long long end) {
-  Window8 w{0, 0, -1, -1, 0.f, 0.f};
+__device__ __forceinline__ Window8 window8(const Decode8Args& A, const int* pfx, long long u, long long u0,
+                                           long long end) {
+  Window8 w{-1, 0, 0.f};
   if (u >= end) return w;
-  int lo = 0, hi = A.B - 1;  // the last sequence that starts at or before u (never an empty one)
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<long long>(A.Hkv) * pfx[mid] <= u) lo = mid; else hi = mid - 1;
-  }
-  const int r = static_cast<int>(u - static_cast<long long>(A.Hkv) * pfx[lo]), cnt = pfx[lo + 1] - pfx[lo];
-  w.i = lo;
-  w.h = r / cnt;
-  w.j = r - w.h * cnt - 1;
-  if (w.j >= 0) {
-    const int blk = A.tables[static_cast<long long>(lo) * A.max_blocks + w.j];
-    if (blk >= 0 && blk < A.num_blocks) {
-      w.tile = blk * A.Hkv + w.h;
-      const uint16_t e = reinterpret_cast<const uint16_t*>(A.exps)[w.tile];
-      w.ks = scale_of(e & 0xff);
-      w.vs = scale_of(e >> 8) * (1.f / (1 << static_cast<int>(kUp8)));
-    } else {
-      record_error(A.err, PA_ERR_DEVICE_CHECK, blk);
-    }
+  const Place8 p = place8(A, pfx, u);
+  if (p.j < 0) return w;
+  if (p.j == 0 || u == u0) w.what = kNew8;
+  const int blk = A.tables[static_cast<long long>(p.i) * A.max_blocks + p.j];
+  if (blk >= 0 && blk < A.num_blocks) {
+    w.tile = blk * A.Hkv + p.h;
+    const int e = reinterpret_cast<const uint16_t*>(A.exps)[w.tile];
+    w.ks = scale_of(e & 0xff);
+    w.what |= min(length8(A, p.i) - p.j * kBlock, kBlock) | (e & 0xff00);
+  } else {
+    record_error(A.err, PA_ERR_DEVICE_CHECK, blk);
   }
   return w;
 }
 
-// The query rows of (i, h) as the scores' operand: lane (g, c) holds head g's dims
-// 16c + 4w + {0, 1}, {2, 3} in qa[2w], qa[2w + 1], and from 64 on in qa[8 + ..].
-// Returns what the products have to be multiplied by.
-template <bool kBf16>
+// The query rows of (i, h) as the scores' operand: lane (g, c) holds column g's dims
+// 16j + 4c + {0, 1} and {2, 3} in qa[2j] and qa[2j + 1]; column g is head g, or g % 4
+// where the columns repeat the heads.  Returns what the column's products have to be
+// multiplied by.
+template <bool kBf16, bool kTwice>
 __device__ __forceinline__ float load_q8(const Decode8Args& A, int i, int h, int g, int c, uint32_t (&qa)[16]) {
-  uint4 x[4];
-  const uint4* src = reinterpret_cast<const uint4*>(A.q + (static_cast<long long>(i) * A.Hq + h * A.G + g) * kHeadDim);
+  const int head = kTwice ? g & 3 : g;
+  const uint2* src = reinterpret_cast<const uint2*>(A.q + (static_cast<long long>(i) * A.Hq + h * A.G + head) * kHeadDim);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) x[k] = g < A.G ? src[8 * (k >> 1) + 2 * c + (k & 1)] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    qa[4 * k] = x[k].x;
-    qa[4 * k + 1] = x[k].y;
-    qa[4 * k + 2] = x[k].z;
-    qa[4 * k + 3] = x[k].w;
+  for (int j = 0; j < 8; ++j) {
+    const uint2 x = head < A.G ? src[4 * j + c] : make_uint2(0, 0);
+    qa[2 * j] = x.x;
+    qa[2 * j + 1] = x.y;
   }
   if (!kBf16) return A.qscale;
   // bf16: times the power of two that takes the largest finite magnitude to [2^14, 2^15)
@@ -200,268 +248,428 @@ __device__ __forceinline__ float load_q8(const Decode8Args& A, int i, int h, int
   return A.qscale * __int_as_float((127 - k2) << 23);
 }
 
-template <bool kBf16, bool kE4M3>
+// 2^d for d <= 0 (0 below 2^-126).
+__device__ __forceinline__ float down2(int d) { return d < -126 ? 0.f : __int_as_float((127 + d) << 23); }
+
+// A running join of records: maximum, sum and four outputs, as they are weighted
+// by the maximum.  Records weigh 2^(m - maximum); one of -infinity has no weight,
+// but its NaN, if it holds one, still counts.
+struct Join8 {
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  template <int N>
+  __device__ __forceinline__ void add(const float (&rm)[N], const float (&rl)[N], const float4 (&ro)[N]) {
+    float to = m;
+#pragma unroll
+    for (int k = 0; k < N; ++k) to = fmaxf(to, rm[k]);
+    const float f = m == to ? 1.f : fast_exp2(m - to);
+    l *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float w = rm[k] == to ? 1.f : fast_exp2(rm[k] - to);
+      l = fmaf(w, rl[k], l);
+      o.x = fmaf(w, ro[k].x, o.x);
+      o.y = fmaf(w, ro[k].y, o.y);
+      o.z = fmaf(w, ro[k].z, o.z);
+      o.w = fmaf(w, ro[k].w, o.w);
+    }
+    m = to;
+  }
+  __device__ __forceinline__ void store(const Decode8Args& A, int i, int h, int head, int dim) const {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    store_out4(A.out, (static_cast<long long>(i) * A.Hq + h * A.G + head) * kHeadDim + dim, o.x * inv, o.y * inv, o.z * inv,
+               o.w * inv, A.out_dtype);
+  }
+};
+
+// What follows the pieces of a segment that more than one warp of a CTA took part
+// in, noted by the warp of the first one: the last warp, and whether the CTA has the
+// whole segment (the result), or a part (a record, in the CTA's slot 0 or 1).
+struct Chain8 {
+  int i, h, last, kind;  // kind: 0 none, 1 result, 2 and 3 record in slot 0 and 1
+};
+
+// kTwice: at most 4 heads, whose columns are repeated.
+template <bool kBf16, bool kE4M3, bool kTwice>
 __global__ void __launch_bounds__(kWarps8 * 32, 1) decode8_kernel(const __grid_constant__ Decode8Args A) {
-  extern __shared__ __align__(16) uint8_t smem8[];
-  int* const pfx = reinterpret_cast<int*>(smem8 + kWarps8 * kStages8 * kPair8);
-  int* const lens = pfx + A.B + 1;
+  using Record = Record8<kTwice>;
+  extern __shared__ uint8_t smem_raw8[];
+  // (the 128-byte swizzle goes by the address)
+  uint8_t* const smem8 =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw8) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ __align__(8) unsigned long long s_full[kWarps8][kStages8];
+  __shared__ Chain8 s_chain[kWarps8][2];
+  __shared__ int s_abort;
+  // rings, the warps' first records, the prefix
+  Record* const firsts = reinterpret_cast<Record*>(smem8 + kWarps8 * kStages8 * kPair8);
+  int* const pfx = reinterpret_cast<int*>(firsts + kWarps8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  if (threadIdx.x == 0) s_abort = 0;
+  if (lane < kStages8) mbar_init(smem_addr(&s_full[warp][lane]), 1);
+  if (lane < 2) s_chain[warp][lane].kind = 0;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  if (threadIdx.x == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&A.tmap)) : "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  prefix8(A, pfx, lens, blockIdx.x == 0);
-  const long long per = Ranges8(A, pfx).per;
-  const int unit = warp * gridDim.x + blockIdx.x;
-  const long long total = static_cast<long long>(A.Hkv) * pfx[A.B];
-  const long long u0 = per * unit, u1 = min(u0 + per, total);
-  if (u0 >= u1) return;
-  const int n = static_cast<int>(u1 - u0);
+  // the tables and the exponents on their way into L2 while the lengths are read
+  {
+    const long long at = 128ll * (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x);
+    if (at < 4ll * A.B * A.max_blocks) prefetch_l2(reinterpret_cast<const uint8_t*>(A.tables) + at);
+    if (at < 2ll * A.num_blocks * A.Hkv) prefetch_l2(A.exps + at);
+  }
+  prefix8(A, pfx, blockIdx.x == 0);
+  // the CTA's units [U0, U1) and the warp's [u0, u1)
+  long long U0, U1, per;
+  if (A.whole) {
+    const int i = blockIdx.x / A.Hkv;
+    const Segment8 seg(A, pfx, i, blockIdx.x - i * A.Hkv);
+    U0 = seg.s0;
+    U1 = U0 + seg.cnt;
+    per = (seg.cnt + kWarps8 - 1) / kWarps8;
+    if (per < kMinUnits8) per = kMinUnits8;
+  } else {
+    per = per_warp8(A, pfx, gridDim.x);
+    U0 = per * kWarps8 * blockIdx.x;
+    U1 = min(U0 + per * kWarps8, static_cast<long long>(A.Hkv) * pfx[A.B]);
+  }
+  const long long u0 = U0 + per * warp, u1 = min(u0 + per, U1);
+  const int n = static_cast<int>(max(u1 - u0, 0ll));
 
-  // the lane's bytes of a tile, and its slots of the ring
-  const int k_off = g * kRow8 + c * 16, v_off = kTile8 + 2 * c * kRow8 + g * 16;
-  const uint32_t ring = smem_addr(smem8) + warp * (kStages8 * kPair8) + lane * 16;
-  Window8 now = window8(A, pfx, u0 + lane, u1), next = now;
-  auto issue = [&](int x) {  // unit x of the range; x and the windows are the same in all lanes
+  const uint32_t ring = smem_addr(smem8) + warp * (kStages8 * kPair8), bars = smem_addr(&s_full[warp][0]);
+  // ldmatrix: lane's row of the tile, and its chunk before ^ 2jj; values: dims 16g .. of tokens 2c and 2c + 1
+  const uint32_t k_off = ((lane & 7) + (lane & 8)) * kRow8 + (((lane >> 4) ^ (lane & 7)) << 4);
+  const uint32_t va_off = kTile8 + 2 * c * kRow8 + ((g ^ (2 * c)) << 4);
+  const uint32_t vb_off = kTile8 + (2 * c + 1) * kRow8 + ((g ^ (2 * c + 1)) << 4);
+  Window8 now = window8(A, pfx, u0 + lane, u0, u1), next = now;
+  uint32_t flying = 0;  // stages with a load on its way
+  // unit x of the range into its stage; x and the windows are the same in all lanes
+  auto issue = [&](int x, int stage) {
     const int tile = __shfl_sync(0xffffffffu, next.tile, x & 31);
     if (x < n && tile >= 0) {
-      const uint32_t to = ring + (x % kStages8) * kPair8;
-      const uint8_t* from = A.codes + static_cast<long long>(tile) * kPair8;
-      const uint8_t *k = from + k_off, *v = from + v_off;
-      cp_async16(to, k);
-      cp_async16(to + 512, k + 64);
-      cp_async16(to + 1024, k + 8 * kRow8);
-      cp_async16(to + 1536, k + 8 * kRow8 + 64);
-      cp_async16(to + 2048, v);
-      cp_async16(to + 2560, v + kRow8);
-      cp_async16(to + 3072, v + 8 * kRow8);
-      cp_async16(to + 3584, v + 9 * kRow8);
+      flying |= 1u << stage;
+      if (lane == 0) load_tile8(ring + stage * kPair8, &A.tmap, tile, bars + 8 * stage);
     }
-    cp_commit();
   };
 #pragma unroll
-  for (int x = 0; x < kStages8; ++x) issue(x);
+  for (int x = 0; x < kStages8; ++x) issue(x, x);
+
+  // the rows of empty sequences
+  for (int i = blockIdx.x; i < A.B; i += gridDim.x)
+    if (pfx[i] == pfx[i + 1])
+      for (int x = threadIdx.x; x < A.Hq * (kHeadDim / 4); x += blockDim.x)
+        store_out4(A.out, (static_cast<long long>(i) * A.Hq * (kHeadDim / 4) + x) * 4, 0.f, 0.f, 0.f, 0.f, A.out_dtype);
 
   uint32_t qa[16];
-  float o[32], m, l, fq = 0.f, mref = 0.f;
-  int ci = -1, ch = -1;  // segment of the piece in hand
+  float o[8][4], m[2], l[2], mref[2], fq[2];
+  int ci = -1, ch = -1, E = 0;  // the piece in hand
   auto flush = [&]() {
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    l *= 1.f / (1 << static_cast<int>(kUp8));
-    if (g >= A.G) return;
-    const int cnt = pfx[ci + 1] - pfx[ci];
-    const long long s0 = static_cast<long long>(A.Hkv) * pfx[ci] + static_cast<long long>(ch) * cnt;
-    if (s0 + 1 >= u0 && s0 + cnt <= u1) {  // the whole segment
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const long long at = (static_cast<long long>(ci) * A.Hq + ch * A.G + g) * kHeadDim + 32 * c;
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          store_out4(A.out, at + 16 * e + 4 * w, o[8 * w + e] * inv, o[8 * w + 2 + e] * inv, o[8 * w + 4 + e] * inv,
-                     o[8 * w + 6 + e] * inv, A.out_dtype);
-      return;
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
     }
-    float* rec = A.rec + (2ll * unit + (s0 > u0)) * kRec8;
+    if (kTwice) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+      for (int u = 0; u < 8; ++u)
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        reinterpret_cast<float4*>(rec)[(4 * e + w) * 32 + lane] =
-            make_float4(o[8 * w + e], o[8 * w + 2 + e], o[8 * w + 4 + e], o[8 * w + 6 + e]);
-    if (c == 0) {
-      rec[1024 + g] = m;
-      rec[1032 + g] = l;
+        for (int k = 0; k < 4; ++k) o[u][k] += __shfl_xor_sync(0xffffffffu, o[u][k], 2);
+    }
+    const Segment8 seg(A, pfx, ci, ch);
+    const long long rs = seg.s0 + 1, end = seg.s0 + seg.cnt;  // its tiles
+    const bool whole = rs >= u0 && end <= u1;                 // all of them are this piece
+    const int slot = seg.s0 > u0;
+    // (a second record is the last piece's: the ring is done with)
+    Record* const rec = slot ? reinterpret_cast<Record*>(smem8 + warp * (kStages8 * kPair8)) : firsts + warp;
+    const float unit_of_o = E ? scale_of(E) : 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int head = 2 * c + e;
+      if (kTwice && c >= 2) continue;
+      const float f = whole ? (l[e] == 0.f ? 0.f : 1.f / l[e]) : 1.f / (1 << static_cast<int>(kUp8));
+      const long long at = (static_cast<long long>(ci) * A.Hq + ch * A.G + head) * kHeadDim + 16 * g;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x = o[2 * k][e] * f * unit_of_o, y = o[2 * k][e + 2] * f * unit_of_o;
+        const float z = o[2 * k + 1][e] * f * unit_of_o, w = o[2 * k + 1][e + 2] * f * unit_of_o;
+        if (!whole)
+          rec->o[Record::place(4 * e + k, g, c)] = make_float4(x, y, z, w);
+        else if (head < A.G)
+          store_out4(A.out, at + 4 * k, x, y, z, w, A.out_dtype);
+      }
+      if (!whole && g == 0) {
+        rec->m[head] = m[e];
+        rec->l[head] = l[e] * (1.f / (1 << static_cast<int>(kUp8)));
+      }
+    }
+    if (!whole && lane == 0 && (rs >= u0 || warp == 0)) {
+      const long long last = (end - 1 - U0) / per;
+      s_chain[warp][slot] = {ci, ch, static_cast<int>(min(last, kWarps8 - 1ll)),
+                             rs >= U0 && end <= U1 ? 1 : 2 + (seg.s0 > U0)};
     }
   };
 
+  uint32_t parity = 0;  // bit s: phase of stage s
+  int stage = 0;
   for (int x = 0; x < n; ++x) {
     if ((x & 31) == 0) now = next;  // (the issues are in this window until the one below)
-    const int j = __shfl_sync(0xffffffffu, now.j, x & 31);
-    if (j >= 0) {
-      const int i = __shfl_sync(0xffffffffu, now.i, x & 31), h = __shfl_sync(0xffffffffu, now.h, x & 31);
-      if (i != ci || h != ch) {
-        if (ci >= 0) flush();
-        ci = i;
-        ch = h;
-        fq = load_q8<kBf16>(A, i, h, g, c, qa);
-        m = -INFINITY;
-        mref = 0.f;
-        l = 0.f;
+    const int what = __shfl_sync(0xffffffffu, now.what, x & 31);
+    if (what & kNew8) {
+      if (ci >= 0) flush();
+      const Place8 p = place8(A, pfx, u0 + x);
+      ci = p.i;
+      ch = p.h;
+      const float f = load_q8<kBf16, kTwice>(A, ci, ch, g, c, qa);
+      fq[0] = __shfl_sync(0xffffffffu, f, 8 * c);
+      fq[1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+      m[0] = m[1] = -INFINITY;
+      mref[0] = mref[1] = l[0] = l[1] = 0.f;
+      E = 0;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = 0.f;
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[u][k] = 0.f;
+    }
+    const int left = what & 31;
+    if (left) {
+      const bool here = wait_phase(bars + 8 * stage, parity >> stage & 1, &s_abort, A.wait_limit_ns, A.err, 8);
+      if (!__all_sync(0xffffffffu, here)) break;
+      parity ^= 1u << stage;
+      flying &= ~(1u << stage);
+      const uint32_t at = ring + stage * kPair8;
+      // scores of tokens g (s[0], s[1]) and g + 8 (s[2], s[3]), heads 2c and 2c + 1
+      float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        const uint4 k = ldmatrix4((at + k_off) ^ (jj << 5));
+        uint32_t a0, a1, a2, a3;
+        unpack_codes<kE4M3>(k.x, a0, a2);
+        unpack_codes<kE4M3>(k.y, a1, a3);
+        mma_f16(d0, a0, a1, a2, a3, qa[4 * jj], qa[4 * jj + 1]);
+        unpack_codes<kE4M3>(k.z, a0, a2);
+        unpack_codes<kE4M3>(k.w, a1, a3);
+        mma_f16(d1, a0, a1, a2, a3, qa[4 * jj + 2], qa[4 * jj + 3]);
       }
-      cp_wait<kStages8 - 1>();
-      if (__shfl_sync(0xffffffffu, now.tile, x & 31) >= 0) {
-        const uint32_t at = ring + (x % kStages8) * kPair8;
-        const int left = lens[i] - j * kBlock;  // tokens of the tile that count
-        // scores of tokens 2c, 2c + 1 (s[0], s[1]) and 8 + 2c, 9 + 2c (s[2], s[3])
-        float s[4];
-        const float ks = __shfl_sync(0xffffffffu, now.ks, x & 31) * fq;
+      const float ks = __shfl_sync(0xffffffffu, now.ks, x & 31);
+      float s[4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < 4; ++k) s[k] = (d0[k] + d1[k]) * (ks * fq[k & 1]);
+      if (left < kBlock) {
+        if (g >= left) s[0] = s[1] = -INFINITY;
+        if (g + 8 >= left) s[2] = s[3] = -INFINITY;
+      }
+      // running maxima and weights
+      const float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
+      if (__any_sync(0xffffffffu, t0 > m[0] + kMove8 || t1 > m[1] + kMove8)) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint4 v = lds16(at + 1024 * t + 512 * half);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int e = 0; e < 2; ++e) {
+          float most = e ? t1 : t0;
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 4));
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
+          const float to = fmaxf(m[e], most);
+          const float f = to == m[e] ? 1.f : fast_exp2(m[e] - to);
+          m[e] = to;
+          mref[e] = to == -INFINITY ? 0.f : to - kUp8;
+          l[e] *= f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t b0, b1;
-              unpack_codes<kE4M3>(w[k], b0, b1);
-              mma_f16(half ? d1 : d0, qa[8 * half + 2 * k], 0u, qa[8 * half + 2 * k + 1], 0u, b0, b1);
-            }
+          for (int u = 0; u < 8; ++u) {
+            o[u][e] *= f;
+            o[u][e + 2] *= f;
           }
-          s[2 * t] = (d0[0] + d1[0]) * ks;
-          s[2 * t + 1] = (d0[1] + d1[1]) * ks;
         }
-        if (left < kBlock) {
+      }
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (8 * (k >> 1) + 2 * c + (k & 1) >= left) s[k] = -INFINITY;
-        }
-        // running maximum and weights
-        float most = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-        if (__any_sync(0xffffffffu, most > m + kMove8)) {
-          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-          const float to = fmaxf(m, most);
-          const float f = to == m ? 1.f : fast_exp2(m - to);
-          m = to;
-          mref = to == -INFINITY ? 0.f : to - kUp8;
-          l *= f;
+      for (int k = 0; k < 4; ++k) s[k] = fast_exp2(s[k] - mref[k & 1]);
+      l[0] += s[0] + s[2];
+      l[1] += s[1] + s[3];
+      // V's scale
+      const int ev = what >> 8;
+      if (ev > E && ev != kNanExponent) {
+        const float f = down2(E - ev);
+        E = ev;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] *= f;
-        }
+        for (int u = 0; u < 8; ++u)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[k] = fast_exp2(s[k] - mref);
-        l += (s[0] + s[1]) + (s[2] + s[3]);
-        const uint32_t a0 = pack_hi<false>(s[0], s[1]), a1 = pack_lo<false>(s[0], s[1]);
-        const uint32_t a2 = pack_hi<false>(s[2], s[3]), a3 = pack_lo<false>(s[2], s[3]);
-        // values
-        const float vs = __shfl_sync(0xffffffffu, now.vs, x & 31);
-        uint4 v[4];
+          for (int k = 0; k < 4; ++k) o[u][k] *= f;
+      }
+      const bool near = ev >= E - kNear8;
+      if (ev != E) {
+        const float f = ev == kNanExponent ? __int_as_float(0x7fffffff) : (near ? down2(ev - E) : 1.f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = lds16(at + 2048 + 512 * k);
-        if (left < kBlock) {  // (a weight of zero times NaN is NaN)
+        for (int k = 0; k < 4; ++k) s[k] *= f;
+      }
+      uint32_t p0, p1, r0, r1;
+      if (kTwice) {
+        p0 = transposed8(c < 2 ? pack_hi<false>(s[0], s[1]) : pack_lo<false>(s[0], s[1]));
+        p1 = transposed8(c < 2 ? pack_hi<false>(s[2], s[3]) : pack_lo<false>(s[2], s[3]));
+      } else {
+        p0 = transposed8(pack_hi<false>(s[0], s[1]));
+        p1 = transposed8(pack_hi<false>(s[2], s[3]));
+        r0 = transposed8(pack_lo<false>(s[0], s[1]));
+        r1 = transposed8(pack_lo<false>(s[2], s[3]));
+      }
+      // values
+      uint4 v[4] = {lds16(at + va_off), lds16(at + vb_off), lds16(at + va_off + 8 * kRow8), lds16(at + vb_off + 8 * kRow8)};
+      if (left < kBlock) {  // (a weight of zero times NaN is NaN)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (8 * (k >> 1) + 2 * c + (k & 1) >= left) v[k] = make_uint4(0, 0, 0, 0);
-        }
+        for (int k = 0; k < 4; ++k)
+          if (8 * (k >> 1) + 2 * c + (k & 1) >= left) v[k] = make_uint4(0, 0, 0, 0);
+      }
+      auto values = [&](auto add) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const uint32_t t0 = w == 0 ? v[0].x : w == 1 ? v[0].y : w == 2 ? v[0].z : v[0].w;
-          const uint32_t t1 = w == 0 ? v[1].x : w == 1 ? v[1].y : w == 2 ? v[1].z : v[1].w;
-          const uint32_t t2 = w == 0 ? v[2].x : w == 1 ? v[2].y : w == 2 ? v[2].z : v[2].w;
-          const uint32_t t3 = w == 0 ? v[3].x : w == 1 ? v[3].y : w == 2 ? v[3].z : v[3].w;
+          const uint32_t a = w == 0 ? v[0].x : w == 1 ? v[0].y : w == 2 ? v[0].z : v[0].w;
+          const uint32_t b = w == 0 ? v[1].x : w == 1 ? v[1].y : w == 2 ? v[1].z : v[1].w;
+          const uint32_t y = w == 0 ? v[2].x : w == 1 ? v[2].y : w == 2 ? v[2].z : v[2].w;
+          const uint32_t z = w == 0 ? v[3].x : w == 1 ? v[3].y : w == 2 ? v[3].z : v[3].w;
           uint32_t lo[4], hi[4];  // dims 16g + 4w + 0 .. 3 of tokens 2c, 2c + 1 and 2c + 8, 2c + 9
-          unpack_codes<kE4M3>(__byte_perm(t0, t1, 0x5140), lo[0], lo[1]);
-          unpack_codes<kE4M3>(__byte_perm(t0, t1, 0x7362), lo[2], lo[3]);
-          unpack_codes<kE4M3>(__byte_perm(t2, t3, 0x5140), hi[0], hi[1]);
-          unpack_codes<kE4M3>(__byte_perm(t2, t3, 0x7362), hi[2], hi[3]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(d, a0, a1, a2, a3, lo[k], hi[k]);
-            o[8 * w + 2 * k] = fmaf(vs, d[0] + d[2], o[8 * w + 2 * k]);
-            o[8 * w + 2 * k + 1] = fmaf(vs, d[1] + d[3], o[8 * w + 2 * k + 1]);
-          }
+          unpack_codes<kE4M3>(__byte_perm(a, b, 0x5140), lo[0], lo[1]);
+          unpack_codes<kE4M3>(__byte_perm(a, b, 0x7362), lo[2], lo[3]);
+          unpack_codes<kE4M3>(__byte_perm(y, z, 0x5140), hi[0], hi[1]);
+          unpack_codes<kE4M3>(__byte_perm(y, z, 0x7362), hi[2], hi[3]);
+          add(2 * w, lo[0], lo[1], hi[0], hi[1]);
+          add(2 * w + 1, lo[2], lo[3], hi[2], hi[3]);
         }
+      };
+      if (near) {
+        values([&](int u, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+          mma_f16(o[u], a0, a1, a2, a3, p0, p1);
+          if (!kTwice) mma_f16(o[u], a0, a1, a2, a3, r0, r1);
+        });
+      } else {
+        const float f = down2(ev - E);
+        values([&](int u, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_f16(d, a0, a1, a2, a3, p0, p1);
+          if (!kTwice) mma_f16(d, a0, a1, a2, a3, r0, r1);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[u][k] = fmaf(f, d[k], o[u][k]);
+        });
       }
     }
     // the stage is free: the unit kStages8 on, from the window it is in
+    __syncwarp();
     const int y = x + kStages8;
-    if ((y & 31) == 0 && y < n) next = window8(A, pfx, u0 + y + lane, u1);
-    issue(y);
+    if ((y & 31) == 0 && y < n) next = window8(A, pfx, u0 + y + lane, u0, u1);
+    issue(y, stage);
+    stage = stage + 1 == kStages8 ? 0 : stage + 1;
+  }
+  if (s_abort) {  // a wait ran out: nothing is left on its way into shared memory, with a limit again
+    const long long t0 = global_ns();
+    for (int k = 0; k < kStages8; ++k)
+      while ((flying >> k & 1) && !mbar_try_wait(bars + 8 * k, parity >> k & 1) && global_ns() - t0 < A.wait_limit_ns) {
+      }
   }
   if (ci >= 0) flush();
-  cp_wait<0>();
-}
-
-// Joins the records of segments that were cut, and writes the zeros of empty
-// ones.  A CTA takes a segment at a time; warp k float4 number k of each lane.
-__global__ void __launch_bounds__(256) merge8_kernel(const __grid_constant__ Decode8Args A) {
-  extern __shared__ __align__(16) uint8_t smem8[];
-  int* const pfx = reinterpret_cast<int*>(smem8);
-  int* const lens = pfx + A.B + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  prefix8(A, pfx, lens, false);
-  const long long per = Ranges8(A, pfx).per;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long segments = static_cast<long long>(A.B) * A.Hkv;
-  for (long long s = blockIdx.x; s < segments; s += gridDim.x) {
-    const int i = static_cast<int>(s / A.Hkv), h = static_cast<int>(s - static_cast<long long>(i) * A.Hkv);
-    const int cnt = pfx[i + 1] - pfx[i];
-    const long long at = (static_cast<long long>(i) * A.Hq + h * A.G + g) * kHeadDim + 32 * c + 4 * warp;
-    if (cnt == 0) {
-      if (g < A.G) store_out4(A.out, at, 0.f, 0.f, 0.f, 0.f, A.out_dtype);
-      continue;
-    }
-    const long long s0 = static_cast<long long>(A.Hkv) * pfx[i] + static_cast<long long>(h) * cnt;
-    const long long c0 = (s0 + 1) / per, c1 = (s0 + cnt - 1) / per;
-    if (c0 == c1 || g >= A.G) continue;
-    const int count = static_cast<int>(c1 - c0 + 1);
-    const float* first = A.rec + (2 * c0 + (s0 > c0 * per)) * kRec8;  // the others: slot 0 of their warps
-    const float* rest = A.rec + 2 * c0 * kRec8;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kBatch = 8;
-    for (int k0 = 0; k0 < count; k0 += kBatch) {
-      float rm[kBatch], rl[kBatch];
-      float4 ro[kBatch];
+  __syncthreads();
+  // pieces of one segment, joined: a warp a float4 a lane of each
+  for (int t = warp; t < 2 * kWarps8 * Record::kParts; t += kWarps8) {
+    const int first = t / Record::kParts >> 1, slot = t / Record::kParts & 1, f = t % Record::kParts * 32 + lane;
+    const Chain8 chain = s_chain[first][slot];
+    if (!chain.kind) continue;
+    const int head = Record::head(f);
+    Join8 join;
+    for (int w0 = first; w0 <= chain.last; w0 += 4) {
+      float rm[4], rl[4];
+      float4 ro[4];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        rm[k] = -INFINITY;
-        rl[k] = 0.f;
-        ro[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k0 + k < count) {
-          const float* r = k0 + k == 0 ? first : rest + 2ll * (k0 + k) * kRec8;
-          rm[k] = __ldcg(r + 1024 + g);
-          rl[k] = __ldcg(r + 1032 + g);
-          ro[k] = __ldcg(reinterpret_cast<const float4*>(r) + warp * 32 + lane);
-        }
+      for (int k = 0; k < 4; ++k) {
+        const int w = w0 + k;
+        const Record* rec = slot && w == first ? reinterpret_cast<const Record*>(smem8 + w * (kStages8 * kPair8)) : firsts + w;
+        const bool in = w <= chain.last;
+        rm[k] = in ? rec->m[head] : -INFINITY;
+        rl[k] = in ? rec->l[head] : 0.f;
+        ro[k] = in ? rec->o[f] : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      float to = m;
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) to = fmaxf(to, rm[k]);
-      const float f = m == to ? 1.f : fast_exp2(m - to);
-      l *= f;
-      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const float w = rm[k] == to ? 1.f : fast_exp2(rm[k] - to);
-        l = fmaf(w, rl[k], l);
-        o.x = fmaf(w, ro[k].x, o.x);
-        o.y = fmaf(w, ro[k].y, o.y);
-        o.z = fmaf(w, ro[k].z, o.z);
-        o.w = fmaf(w, ro[k].w, o.w);
-      }
-      m = to;
+      join.add(rm, rl, ro);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    store_out4(A.out, at, o.x * inv, o.y * inv, o.z * inv, o.w * inv, A.out_dtype);
+    if (chain.kind == 1) {
+      if (head < A.G) join.store(A, chain.i, chain.h, head, Record::dim(f));
+    } else {
+      Record* rec = static_cast<Record*>(A.rec) + 2 * blockIdx.x + (chain.kind - 2);
+      rec->o[f] = join.o;
+      if (Record::dim(f) == 0) {
+        rec->m[head] = join.m;
+        rec->l[head] = join.l;
+      }
+    }
   }
 }
 
-static size_t decode8_records(const pa_pool8* p) {
-  return 2 * static_cast<size_t>(sm_count(p->device)) * kWarps8 * kRec8 * sizeof(float);
+// Joins the records of the segments that CTAs' ranges cut: CTA b has the one that
+// goes on behind range b and starts in it, if there is one.
+template <bool kTwice>
+__global__ void __launch_bounds__(32 * Record8<kTwice>::kParts) merge8_kernel(const __grid_constant__ Decode8Args A) {
+  using Record = Record8<kTwice>;
+  extern __shared__ uint8_t smem_raw8[];
+  int* const pfx = reinterpret_cast<int*>(smem_raw8);
+  prefix8(A, pfx, false);
+  const long long per = per_warp8(A, pfx, gridDim.x + 1) * kWarps8, total = static_cast<long long>(A.Hkv) * pfx[A.B];
+  const long long next = per * (blockIdx.x + 1ll);  // the range behind
+  int count = 0, i = 0, h = 0;
+  bool second = false;
+  if (next < total) {
+    const Place8 p = place8(A, pfx, next);
+    i = p.i;
+    h = p.h;
+    const Segment8 seg(A, pfx, i, h);
+    if (p.j > 0 && (seg.s0 + 1) / per == blockIdx.x) {
+      count = static_cast<int>((seg.s0 + seg.cnt - 1) / per - blockIdx.x + 1);
+      second = seg.s0 > per * blockIdx.x;
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!count) return;
+  const int f = threadIdx.x, head = Record::head(f);
+  const Record* rec = static_cast<const Record*>(A.rec) + 2ll * blockIdx.x;
+  Join8 join;
+  constexpr int kBatch = 8;
+  for (int k0 = 0; k0 < count; k0 += kBatch) {
+    float rm[kBatch], rl[kBatch];
+    float4 ro[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      rm[k] = -INFINITY;
+      rl[k] = 0.f;
+      ro[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + k < count) {  // (behind the first, a segment's record is slot 0)
+        const Record* r = rec + 2 * (k0 + k) + (k0 + k == 0 && second);
+        rm[k] = __ldcg(&r->m[head]);
+        rl[k] = __ldcg(&r->l[head]);
+        ro[k] = __ldcg(&r->o[f]);
+      }
+    }
+    join.add(rm, rl, ro);
+  }
+  if (head < A.G) join.store(A, i, h, head, Record::dim(f));
 }
 
-template <bool kBf16, bool kE4M3>
+// Two records a CTA of the balanced split.
+static size_t decode8_records(const pa_pool8* p) {
+  return 2 * static_cast<size_t>(sm_count(p->device)) * Record8<false>::kBytes;
+}
+
+template <bool kBf16, bool kE4M3, bool kTwice>
 static int launch_decode8(Decode8Args& A, int device, cudaStream_t st) {
   const int sms = sm_count(device);
-  const size_t lists = sizeof(int) * (2 * static_cast<size_t>(A.B) + 1);
-  const size_t smem = static_cast<size_t>(kWarps8) * kStages8 * kPair8 + lists;
-  constexpr int kMaxSmem = kWarps8 * kStages8 * kPair8 + sizeof(int) * (2 * kSeqs8 + 1);
-  static_assert(kMaxSmem <= 232448, "shared memory of an SM");
+  const size_t list = sizeof(int) * (static_cast<size_t>(A.B) + 1);
+  static_assert(sizeof(Record8<kTwice>) == Record8<kTwice>::kBytes && sizeof(Record8<kTwice>) <= kStages8 * kPair8, "a record");
+  constexpr int kFixed = kWarps8 * (kStages8 * kPair8 + Record8<kTwice>::kBytes) + 1024;  // with room to align it
+  constexpr int kMaxSmem = kFixed + sizeof(int) * (kSeqs8 + 1);
+  static_assert(kMaxSmem + 1024 <= 232448, "shared memory of an SM, with the static part");
   // once a device, for the largest batch
   static std::atomic<uint64_t> allowed{0};
   const uint64_t bit = device < 64 ? 1ull << device : 0;
   if (!(allowed.load(std::memory_order_relaxed) & bit) || !bit) {
-    if (cudaFuncSetAttribute(decode8_kernel<kBf16, kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) !=
+    if (cudaFuncSetAttribute(decode8_kernel<kBf16, kE4M3, kTwice>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) !=
         cudaSuccess)
       return PA_ERR_CUDA;
     allowed.fetch_or(bit, std::memory_order_relaxed);
   }
+  const long long segments = static_cast<long long>(A.B) * A.Hkv;
+  A.whole = segments <= sms && A.max_blocks <= kWholeBlocks8;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -469,16 +677,20 @@ static int launch_decode8(Decode8Args& A, int device, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = st;
-  cfg.gridDim = dim3(sms);
+  cfg.gridDim = dim3(A.whole ? static_cast<unsigned>(segments) : sms);
   cfg.blockDim = dim3(kWarps8 * 32);
-  cfg.dynamicSmemBytes = smem;
-  if (cudaLaunchKernelEx(&cfg, decode8_kernel<kBf16, kE4M3>, A) != cudaSuccess) return PA_ERR_CUDA;
-  const long long segments = static_cast<long long>(A.B) * A.Hkv;
-  cfg.gridDim = dim3(static_cast<unsigned>(segments < 8ll * sms ? segments : 8ll * sms));
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = lists;
-  if (cudaLaunchKernelEx(&cfg, merge8_kernel, A) != cudaSuccess) return PA_ERR_CUDA;
-  return PA_OK;
+  cfg.dynamicSmemBytes = kFixed + list;
+  if (cudaLaunchKernelEx(&cfg, decode8_kernel<kBf16, kE4M3, kTwice>, A) != cudaSuccess) return PA_ERR_CUDA;
+  if (A.whole || sms == 1) return PA_OK;
+  cfg.gridDim = dim3(sms - 1);
+  cfg.blockDim = dim3(32 * Record8<kTwice>::kParts);
+  cfg.dynamicSmemBytes = list;
+  return cudaLaunchKernelEx(&cfg, merge8_kernel<kTwice>, A) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+template <bool kBf16, bool kE4M3>
+static int launch_g8(Decode8Args& A, int device, cudaStream_t st) {
+  return A.G <= 4 ? launch_decode8<kBf16, kE4M3, true>(A, device, st) : launch_decode8<kBf16, kE4M3, false>(A, device, st);
 }
 
 }  // namespace pa
@@ -510,13 +722,13 @@ extern "C" int pa_decode8(pa_pool8_t p, const void* q, int q_dtype, const int32_
   if (!workspace || workspace_bytes < decode8_records(p) || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return PA_ERR_INVALID;
   Decode8Args A{};
-  A.codes = p->codes;
+  A.tmap = p->tmap;
   A.exps = p->exps;
   A.q = static_cast<const uint16_t*>(q);
   A.tables = block_tables;
   A.seq_lens = seq_lens;
   A.out = out;
-  A.rec = static_cast<float*>(workspace);
+  A.rec = workspace;
   A.err = p->err;
   A.num_blocks = p->num_blocks;
   A.max_blocks = max_blocks_per_seq;
@@ -526,10 +738,9 @@ extern "C" int pa_decode8(pa_pool8_t p, const void* q, int q_dtype, const int32_
   A.G = n_q_heads / p->n_kv_heads;
   A.out_dtype = out_dtype;
   A.qscale = scale * kLog2e8;
-  A.units = sm_count(p->device) * kWarps8;
+  A.wait_limit_ns = wait_limit_ns();
   cudaStream_t st = as_stream(stream);
   const bool e4m3 = p->dtype == PA_E4M3;
-  if (q_dtype == PA_BF16)
-    return e4m3 ? launch_decode8<true, true>(A, p->device, st) : launch_decode8<true, false>(A, p->device, st);
-  return e4m3 ? launch_decode8<false, true>(A, p->device, st) : launch_decode8<false, false>(A, p->device, st);
+  if (q_dtype == PA_BF16) return e4m3 ? launch_g8<true, true>(A, p->device, st) : launch_g8<true, false>(A, p->device, st);
+  return e4m3 ? launch_g8<false, true>(A, p->device, st) : launch_g8<false, false>(A, p->device, st);
 }

@@ -30,6 +30,7 @@ struct pa_pool {
 // (block, head)'s K and V, which a decode reads together, are 4 KiB on end, and
 // exponent bytes [num_blocks][n_kv_heads][K|V].
 struct pa_pool8 {
+  CUtensorMap tmap;   // a (block, head)'s 32 rows of codes as one box, 128-byte swizzle
   int num_blocks;
   int n_kv_heads;
   int dtype;          // PA_E4M3 | PA_INT8
@@ -78,6 +79,9 @@ inline bool on_pool_device(const Pool* p) {
   int cur = -1;
   return cudaGetDevice(&cur) == cudaSuccess && cur == p->device;
 }
+
+// The map of an 8-bit pool: {128 bytes, 32 rows, tiles}, boxes {128, 32, 1}.
+bool encode_pool8_map(CUtensorMap* map, void* codes, long long tiles);
 
 // pa_check and pa_check8: synchronises the stream, reads and clears an error word.
 int check_error_word(long long* err, void* stream, int64_t* detail);

@@ -48,6 +48,17 @@ static bool encode_pool_map(CUtensorMap* map, void* base, long long rows, size_t
   return r == CUDA_SUCCESS;
 }
 
+bool encode_pool8_map(CUtensorMap* map, void* codes, long long tiles) {
+  auto fn = encode_tiled();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {kHeadDim, 2 * kBlock, static_cast<cuuint64_t>(tiles)};
+  cuuint64_t strides[2] = {kHeadDim, 2 * kBlock * kHeadDim};
+  cuuint32_t box[3] = {kHeadDim, 2 * kBlock, 1}, elem[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int sm_count(int device) {
   static std::mutex mu;
   static std::vector<int> cache;

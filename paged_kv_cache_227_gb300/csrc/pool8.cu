@@ -210,7 +210,8 @@ int pa_pool8_create(int num_blocks, int block_size, int n_kv_heads, int d_head, 
       cudaMalloc(&p->err, 2 * sizeof(long long)) != cudaSuccess)
     status = PA_ERR_OOM;
   else if (cudaMemset(p->codes, 0, tiles * kPair8) != cudaSuccess || cudaMemset(p->exps, 0, tiles * 2) != cudaSuccess ||
-           cudaMemset(p->err, 0, 2 * sizeof(long long)) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
+           cudaMemset(p->err, 0, 2 * sizeof(long long)) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess ||
+           !encode_pool8_map(&p->tmap, p->codes, static_cast<long long>(tiles)))
     status = PA_ERR_CUDA;
   if (status != PA_OK) {
     cudaFree(p->codes);
