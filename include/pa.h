@@ -149,7 +149,7 @@ int pa_cache_append(pa_pool_t pool, const void* k_new, const void* v_new,
  * Pointers are 16-byte aligned and strides multiples of 8 elements that hold
  * a token's heads (else INVALID).  rot_dim is a multiple of 16 up to 128, 1 <=
  * n_axes <= PA_MAX_ROPE_AXES, n_q_heads <= PA_MAX_ROPE_HEADS, and the rows
- * fit one launch (2^31 CTAs of 16 rows; else UNSUPPORTED).  Tokens that name
+ * fit one launch (2^31 CTAs of 16 rows, with norms 2^30 of them; else UNSUPPORTED).  Tokens that name
  * one slot race, as for pa_cache_append.  Arithmetic is fp32, rounded once to the pool's type.
  * n_tok == 0 is a no-op. */
 enum { PA_MAX_ROPE_AXES = 4, PA_MAX_ROPE_HEADS = 65536 };

@@ -8,22 +8,26 @@
 // the block's scale grows, the codes of its other rows move to it.
 //
 // Bound: memory (512 B read and 256 B written a K or V row; 512 B a query row),
-// and latency for the tokens of a decode step.  A warp takes 16 consecutive rows
-// of one kv head's K or V, in registers as they were loaded (16 bits), so a
-// run that fills a block is one pass, and so are 16 tokens of 16 sequences:
-// the runs' largest magnitudes come from one segmented reduction over the rows.
-// K rows are normed and turned twice, for the magnitudes and for the codes:
-// kept in 32 bits between, they would take 64 registers a thread.  The tokens'
-// angles are computed once for a CTA's four heads.  Query rows go by
-// (token, chunk of rows) as in the 16-bit append, in the same launch.
+// and latency for the tokens of a decode step.  Two warps take 16 consecutive rows
+// of one kv head's K or V, in registers, so a run that fills a block is one pass, and
+// so are 16 tokens of 16 sequences: the rows' largest magnitudes meet in shared
+// memory, and each run's comes from one segmented reduction over the 16.  A CTA
+// has 16 rows of four (kv head, K|V), whose angles are computed once.  Query rows
+// go as in the 16-bit appends, in the same launch, with the same bits.
+//
+// Measured: 7,900 tokens of 32 / 8 / 8 heads in 24 chunks (183 MB) 42.5 us, 0.63 of
+// the copy rate; one token of 64 sequences 5.4 us: three memory latencies (slots,
+// rows and scales, codes) and the reduction between them.
 #include "codes8.cuh"
+#include "device_utils.cuh"
 #include "rope_rows.cuh"
 
 namespace pa {
 
-constexpr int kTok8 = 16;           // rows of a warp
-constexpr int kTasks8 = kRopeThreads / 32;  // (kv head, K|V) of a CTA
-constexpr int kAngleRows = 2 * kTok8 - 1;   // a run that starts in the window ends at most 15 rows behind it
+constexpr int kTok8 = 16;                 // rows of a task
+constexpr int kThreads8 = 256;
+constexpr int kTasks8 = kThreads8 / 64;   // (kv head, K|V) of a CTA
+constexpr int kAngleRows = 2 * kTok8 - 1; // a run that starts in the window ends at most 15 rows behind it
 
 struct Append8Args {
   RopeArgs R;          // rows = query rows; k_pool and v_pool unused
@@ -33,17 +37,25 @@ struct Append8Args {
   unsigned kv_ctas;
 };
 
+// The larger magnitude, NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
+  return d;
+}
+
 // Largest k <= r whose row starts a run (bit k of cont clear).
 __device__ __forceinline__ int leader_of(uint32_t cont, int r) { return 31 - __clz(~cont & ((2u << r) - 1)); }
 
 template <bool kBf16, bool kE4M3>
-__device__ __forceinline__ void write_window(const Append8Args& A, float2 (*s_cs)[kMaxPairs]) {
+__device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_angles) {
+  __shared__ uint32_t s_top[2][kTasks8][kTok8];
   const RopeArgs& R = A.R;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, mine8 = threadIdx.x >> 6, half = threadIdx.x >> 5 & 1;
   const int group = blockIdx.x % A.groups;
   const long long base = static_cast<long long>(blockIdx.x / A.groups) * kTok8;
-  const int task = group * kTasks8 + (threadIdx.x >> 5);  // K of each head, then V of each head
-  const bool is_v = task >= R.Hkv;
+  const int task = group * kTasks8 + mine8;  // K of each head, then V of each head
+  const bool active = task < 2 * R.Hkv, is_v = task >= R.Hkv;
   const int h = is_v ? task - R.Hkv : task;
   const int j = lane & 7, sub = lane >> 3;
   const bool turn = !is_v && j < R.half_vecs;
@@ -55,7 +67,8 @@ __device__ __forceinline__ void write_window(const Append8Args& A, float2 (*s_cs
   const long long row = base - 1 + lane;
   const long long slot = row >= 0 && row < R.n_tok ? R.slots[row] : -1;
   const bool good = slot >= 0 && slot < R.num_slots;
-  if (slot >= R.num_slots && lane >= 1 && lane <= kTok8 && task == 0) record_error(R.err, PA_ERR_DEVICE_CHECK, slot);
+  if (slot >= R.num_slots && lane >= 1 && lane <= kTok8 && task == 0 && half == 0)
+    record_error(R.err, PA_ERR_DEVICE_CHECK, slot);
   const long long before = __shfl_up_sync(0xffffffffu, slot, 1);
   // bit i: row base + i is written; it goes on with the run of the row before it
   const uint32_t goodm = __ballot_sync(0xffffffffu, good) >> 1;
@@ -63,21 +76,12 @@ __device__ __forceinline__ void write_window(const Append8Args& A, float2 (*s_cs
       __ballot_sync(0xffffffffu, lane > 0 && good && before >= 0 && slot == before + 1 && (slot & (kBlock - 1)) != 0) >> 1;
   uint32_t todo = goodm & ~contm & 0xffffu;  // first rows of the runs that start in the window
 
-  // angles of the window's rows and of the run that leaves it
-  if (R.half_vecs && group * kTasks8 < R.Hkv) {
-    const int end = kTok8 + __ffs(~(contm >> kTok8)) - 1;  // (bit 31 of contm is clear)
-    const int pairs = 8 * R.half_vecs;
-    for (int x = threadIdx.x; x < end * kMaxPairs; x += kRopeThreads) {
-      const int r = x / kMaxPairs, f = x % kMaxPairs;
-      if (f < pairs && base + r < R.n_tok) s_cs[r][f] = cos_sin(R, base + r, f);
-    }
-    __syncthreads();
-  }
-  if (task >= 2 * R.Hkv) return;
-
   const uint16_t* from = is_v ? R.v : R.k;
   const long long stride = is_v ? R.v_stride : R.k_stride;
-  const uint16_t* weight = is_v ? nullptr : R.k_weight;
+  const uint16_t* weight = is_v || !active ? nullptr : R.k_weight;
+  bool angles = R.half_vecs && group * kTasks8 < R.Hkv;  // still to be computed
+  int pass = 0;
+  // (every warp of the CTA goes through the same passes)
   while (todo) {
     const int f = __ffs(todo) - 1;
     // rows f .. f + 15 (bit and row numbers from f on); runs that start among
@@ -87,19 +91,16 @@ __device__ __forceinline__ void write_window(const Append8Args& A, float2 (*s_cs
     if (f + kTok8 < 32 && ((contm >> (f + kTok8)) & 1)) lead &= (1u << leader_of(cont, kTok8 - 1)) - 1;
     todo &= ~((lead | 1u) << f);  // (a run has at most 16 rows: the first one is never cut)
     const uint32_t part = (goodm >> f) & 0xffffu;
-    uint32_t mine = 0;  // rows of the runs taken
+    // this lane's rows: 8 half + sub and 4 behind it
+    bool mine[2];
+    uint4 x[2][2];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int r = 4 * p + sub;
-      if (((part >> r) & 1) && ((lead >> leader_of(cont, r)) & 1)) mine |= 1u << p;
-    }
-
-    uint4 x[4][2];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    for (int p = 0; p < 2; ++p) {
+      const int r = 8 * half + 4 * p + sub;
+      mine[p] = active && ((part >> r) & 1) && ((lead >> leader_of(cont, r)) & 1);
       x[p][0] = x[p][1] = make_uint4(0, 0, 0, 0);
-      if (mine >> p & 1) {
-        const uint4* src = reinterpret_cast<const uint4*>(from + (base + f + 4 * p + sub) * stride + h * kHeadDim);
+      if (mine[p]) {
+        const uint4* src = reinterpret_cast<const uint4*>(from + (base + f + r) * stride + h * kHeadDim);
         x[p][0] = src[v0];
         x[p][1] = src[v1];
       }
@@ -108,49 +109,48 @@ __device__ __forceinline__ void write_window(const Append8Args& A, float2 (*s_cs
     const int l = lane & 15;
     const long long my_slot = __shfl_sync(0xffffffffu, slot, min(f + l + 1, 31));
     const int first = leader_of(cont, l);
-    const bool taken = ((part >> l) & 1) && ((lead >> first) & 1);
+    const bool taken = active && ((part >> l) & 1) && ((lead >> first) & 1);
     const long long tile = ((my_slot >> 4) * R.Hkv + h) * 2 + is_v;
     const int off = static_cast<int>(my_slot & (kBlock - 1)), off0 = off - (l - first);
     const int was = taken ? A.exps[tile] : 0;
 
-    float rr[4];
-    uint32_t top[4];
-    auto values = [&](int p, float a[8], float b[8]) {
-      unpack8f<kBf16>(x[p][0], a);
-      unpack8f<kBf16>(x[p][1], b);
-      if (is_v) return;
-      if (weight)
-        scale_row<kBf16>(a, b, rr[p], __ldg(reinterpret_cast<const uint4*>(weight) + v0),
-                         __ldg(reinterpret_cast<const uint4*>(weight) + v1));
-      // (a row that is not taken has no angles)
-      if (turn && (mine >> p & 1))
-        turn_row(a, b, R.interleaved != 0, [&](int k) { return s_cs[f + 4 * p + sub][8 * j + k]; });
-    };
+    if (angles) {  // of the window's rows and of the run that leaves it, once, with the first rows on their way
+      const int end = kTok8 + __ffs(~(contm >> kTok8)) - 1;  // (bit 31 of contm is clear)
+      fill_angles<kThreads8>(R, s_angles, base, static_cast<int>(min(static_cast<long long>(end), R.n_tok - base)));
+      __syncthreads();
+      angles = false;
+    }
+    RowPart y[2];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      float a[8], b[8];
+    for (int p = 0; p < 2; ++p) {
+      const int r = 8 * half + 4 * p + sub;
+      y[p].unpack<kBf16>(x[p][0], x[p][1]);
       if (weight) {
-        unpack8f<kBf16>(x[p][0], a);
-        unpack8f<kBf16>(x[p][1], b);
-        rr[p] = inverse_rms(a, b, R.eps);
+        const float rr = y[p].inverse_rms(R.eps);
+        RowPart w;
+        w.unpack<kBf16>(__ldg(reinterpret_cast<const uint4*>(weight) + v0), __ldg(reinterpret_cast<const uint4*>(weight) + v1));
+        y[p].times(w);
+        y[p].times(rr);
       }
-      values(p, a, b);
-      // magnitudes compare as their bits, infinities and NaN above all others
-      uint32_t t = 0;
+      // (a row that is not taken has no angles)
+      if (turn && mine[p]) y[p].turn(R.interleaved, s_angles[f + r], j);
+      float m = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        t = max(t, max(__float_as_uint(a[k]) & 0x7fffffffu, __float_as_uint(b[k]) & 0x7fffffffu));
+      for (int k = 0; k < 4; ++k) {
+        m = max_abs(max_abs(m, y[p].a[k].x), y[p].a[k].y);
+        m = max_abs(max_abs(m, y[p].b[k].x), y[p].b[k].y);
+      }
+      // magnitudes compare as their bits, infinities and NaN above all others
+      uint32_t t = __float_as_uint(m) & 0x7fffffffu;
       t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
       t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
-      top[p] = max(t, __shfl_xor_sync(0xffffffffu, t, 4));
+      t = max(t, __shfl_xor_sync(0xffffffffu, t, 4));
+      if (j == 0) s_top[pass & 1][mine8][r] = mine[p] ? t : 0;
     }
-    // row l's magnitude to lane l, and the run's to each of its rows
-    uint32_t most = 0;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const uint32_t t = __shfl_sync(0xffffffffu, top[p], 8 * (l & 3));
-      if (l >> 2 == p) most = t;
-    }
+    __syncthreads();  // (the next pass writes the other half of s_top)
+    // the run's magnitude to each of its rows
+    uint32_t most = s_top[pass & 1][mine8][l];
+    ++pass;
 #pragma unroll
     for (int d = 1; d < kTok8; d <<= 1) {
       const uint32_t t = __shfl_up_sync(0xffffffffu, most, d, 16);
@@ -163,20 +163,19 @@ __device__ __forceinline__ void write_window(const Append8Args& A, float2 (*s_cs
     if (off0 > 0 && was > e) e = was;
 
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int r = 4 * p + sub;
+    for (int p = 0; p < 2; ++p) {
+      const int r = 8 * half + 4 * p + sub;
       const int er = __shfl_sync(0xffffffffu, e, r);
       const long long tr = __shfl_sync(0xffffffffu, tile, r);
       const int at = __shfl_sync(0xffffffffu, off, r);
-      if (!(mine >> p & 1)) continue;
-      const float inv = inverse_scale(er);
-      float a[8], b[8];
-      values(p, a, b);
+      if (!mine[p]) continue;
+      y[p].times(inverse_scale(er));
       uint8_t* dst = A.codes + tr * kTile8 + at * kRow8;
-      const uint2 c0 = make_uint2(pack_codes<kE4M3>(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv),
-                                  pack_codes<kE4M3>(a[4] * inv, a[5] * inv, a[6] * inv, a[7] * inv));
-      const uint2 c1 = make_uint2(pack_codes<kE4M3>(b[0] * inv, b[1] * inv, b[2] * inv, b[3] * inv),
-                                  pack_codes<kE4M3>(b[4] * inv, b[5] * inv, b[6] * inv, b[7] * inv));
+      const float2 *a = y[p].a, *b = y[p].b;
+      const uint2 c0 = make_uint2(pack_codes<kE4M3>(a[0].x, a[0].y, a[1].x, a[1].y),
+                                  pack_codes<kE4M3>(a[2].x, a[2].y, a[3].x, a[3].y));
+      const uint2 c1 = make_uint2(pack_codes<kE4M3>(b[0].x, b[0].y, b[1].x, b[1].y),
+                                  pack_codes<kE4M3>(b[2].x, b[2].y, b[3].x, b[3].y));
       if (halves) {
         *reinterpret_cast<uint2*>(dst + 8 * v0) = c0;
         *reinterpret_cast<uint2*>(dst + 8 * v1) = c1;
@@ -185,9 +184,9 @@ __device__ __forceinline__ void write_window(const Append8Args& A, float2 (*s_cs
       }
     }
     const bool heads_run = taken && l == first && lane < kTok8;
-    if (heads_run) A.exps[tile] = static_cast<uint8_t>(e);
+    if (heads_run && half == 0) A.exps[tile] = static_cast<uint8_t>(e);
 
-    // blocks whose scale grew: the codes of their other rows
+    // blocks whose scale grew: the codes of their other rows, half of the tile a warp
     uint32_t grown = __ballot_sync(0xffffffffu, heads_run && off0 > 0 && e > was && e != kNanExponent);
     while (grown) {
       const int r = __ffs(grown) - 1;
@@ -197,17 +196,17 @@ __device__ __forceinline__ void write_window(const Append8Args& A, float2 (*s_cs
       const int d = __shfl_sync(0xffffffffu, e - was, r);
       const float ratio = d > 126 ? 0.f : __int_as_float((127 - d) << 23);
       uint4* tile_codes = reinterpret_cast<uint4*>(A.codes + tr * kTile8);
-      uint4 c[4];
+      uint4 c[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // vector 32 i + lane: row 4 i + lane / 8
-        const int rw = 4 * i + sub;
-        c[i] = rw < o0 || rw > o1 ? tile_codes[32 * i + lane] : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 2; ++i) {  // vector 32 (2 half + i) + lane: row 4 (2 half + i) + lane / 8
+        const int n = 2 * half + i, rw = 4 * n + sub;
+        if (rw < o0 || rw > o1) c[i] = tile_codes[32 * n + lane];
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int rw = 4 * i + sub;
+      for (int i = 0; i < 2; ++i) {
+        const int n = 2 * half + i, rw = 4 * n + sub;
         if (rw < o0 || rw > o1)
-          tile_codes[32 * i + lane] =
+          tile_codes[32 * n + lane] =
               make_uint4(shrink_codes<kE4M3>(c[i].x, ratio), shrink_codes<kE4M3>(c[i].y, ratio),
                          shrink_codes<kE4M3>(c[i].z, ratio), shrink_codes<kE4M3>(c[i].w, ratio));
       }
@@ -217,14 +216,23 @@ __device__ __forceinline__ void write_window(const Append8Args& A, float2 (*s_cs
 
 // CTAs below kv_ctas: K and V rows; the others: query rows (U row quads a warp).
 template <bool kBf16, bool kE4M3, int U, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads) append8_kernel(const __grid_constant__ Append8Args A) {
-  __shared__ float2 s_cs[kAngleRows][kMaxPairs];
+__global__ void __launch_bounds__(kThreads8, U > 1 ? 3 : 2) append8_kernel(const __grid_constant__ Append8Args A) {
+  constexpr int kWarps = kThreads8 / 32;
+  constexpr int kRows = kNorm && U > 1 ? kWarps * 64 * U : 0;  // vectors of query rows that wait
+  // angles of a window, or the query rows' and the rows
+  constexpr int kQueries = kWarps * sizeof(Angles) + 16 * kRows, kKeys = kAngleRows * sizeof(Angles);
+  __shared__ __align__(16) uint8_t s_space[kQueries > kKeys ? kQueries : kKeys];
+  Angles* const s_angles = reinterpret_cast<Angles*>(s_space);
   if (blockIdx.x < A.kv_ctas) {
-    write_window<kBf16, kE4M3>(A, s_cs);
-  } else {
-    const int wib = threadIdx.x >> 5;
-    turn_rows<kBf16, U, kNorm>(A.R, static_cast<long long>(blockIdx.x - A.kv_ctas) * (kRopeThreads / 32) + wib, s_cs[wib]);
+    write_window<kBf16, kE4M3>(A, s_angles);
+    return;
   }
+  const int wib = threadIdx.x >> 5;
+  const unsigned w = (blockIdx.x - A.kv_ctas) * kWarps + wib;
+  if (kNorm)
+    norm_rows<kBf16, U>(A.R, w, s_angles + wib, smem_addr(s_space) + kWarps * sizeof(Angles) + wib * 1024 * U);
+  else
+    turn_rows<kBf16, U>(A.R, w, reinterpret_cast<float2*>(s_angles + wib));
 }
 
 template <int U, bool kNorm>
@@ -233,16 +241,16 @@ static int launch_append8(Append8Args& A, bool bf16, bool e4m3, cudaStream_t st)
   A.R.chunks = (R.rows + 4 * U - 1) / (4 * U);
   A.groups = (2 * R.Hkv + kTasks8 - 1) / kTasks8;
   const long long kv = (R.n_tok + kTok8 - 1) / kTok8 * A.groups;
-  const long long grid = kv + (R.n_tok * A.R.chunks + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  if (grid > 0x7fffffffll) return PA_ERR_UNSUPPORTED;
+  const long long q = (R.n_tok * A.R.chunks + kThreads8 / 32 - 1) / (kThreads8 / 32);
+  if (kv > 0x3fffffffll || q > 0x1fffffffll) return PA_ERR_UNSUPPORTED;  // (warps of query rows are counted in 32 bits)
   A.kv_ctas = static_cast<unsigned>(kv);
-  const unsigned n = static_cast<unsigned>(grid);
+  const unsigned n = static_cast<unsigned>(kv + q);
   if (bf16)
-    e4m3 ? append8_kernel<true, true, U, kNorm><<<n, kRopeThreads, 0, st>>>(A)
-         : append8_kernel<true, false, U, kNorm><<<n, kRopeThreads, 0, st>>>(A);
+    e4m3 ? append8_kernel<true, true, U, kNorm><<<n, kThreads8, 0, st>>>(A)
+         : append8_kernel<true, false, U, kNorm><<<n, kThreads8, 0, st>>>(A);
   else
-    e4m3 ? append8_kernel<false, true, U, kNorm><<<n, kRopeThreads, 0, st>>>(A)
-         : append8_kernel<false, false, U, kNorm><<<n, kRopeThreads, 0, st>>>(A);
+    e4m3 ? append8_kernel<false, true, U, kNorm><<<n, kThreads8, 0, st>>>(A)
+         : append8_kernel<false, false, U, kNorm><<<n, kThreads8, 0, st>>>(A);
   return cuda_status(cudaGetLastError());
 }
 
@@ -255,10 +263,13 @@ static int launch8(pa_pool8_t p, Append8Args& A, bool bf16, void* stream) {
   A.R.rows = A.R.Hq;
   const bool e4m3 = p->dtype == PA_E4M3;
   cudaStream_t st = as_stream(stream);
-  // (query rows a warp: as in the 16-bit append)
   const long long quads = A.R.n_tok * ((A.R.rows + 3) / 4);
-  const bool few = quads <= 32ll * sm_count(p->device);
-  if (A.R.q_weight) return few ? launch_append8<1, true>(A, bf16, e4m3, st) : launch_append8<3, true>(A, bf16, e4m3, st);
+  // query rows a warp with norms, 4 or 16.  us, captured calls: 32 query heads, 480
+  // tokens (the switch is at 760) 6.6 and 7.3, 960 9.6 and 8.4, 3,840 39.0 and
+  // 24.0; 12 heads (2,027) 1,920 tokens 6.9 and 7.9, 4,000 13.0 and 11.5
+  const bool few = quads <= 40ll * sm_count(p->device);
+  if (A.R.q_weight || A.R.k_weight)
+    return few ? launch_append8<1, true>(A, bf16, e4m3, st) : launch_append8<4, true>(A, bf16, e4m3, st);
   return few ? launch_append8<1, false>(A, bf16, e4m3, st) : launch_append8<3, false>(A, bf16, e4m3, st);
 }
 

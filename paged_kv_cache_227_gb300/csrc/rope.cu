@@ -16,26 +16,40 @@
 // computed by the lanes of a warp together (two each) and shared by all of
 // the warp's rows through shared memory.  Measured: 8,192 tokens of 48 heads
 // (201 MB) 32.8 us, 6.1 TB/s, 0.90 of this GPU's copy rate; 64 tokens 2.3 us.
+// With norms 36.4 us, 0.82 of the copy rate, and 2.7 us: half of the issue slots go
+// to the norms' arithmetic, and its registers leave room for fewer warps.
+#include "device_utils.cuh"
 #include "rope_rows.cuh"
 
 namespace pa {
 
-template <bool kBf16, int U, bool kNorm>
+
+template <bool kBf16, int U>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeArgs A) {
   __shared__ float2 s_cs[kRopeThreads / 32][kMaxPairs];
   const int wib = threadIdx.x >> 5;
-  turn_rows<kBf16, U, kNorm>(A, static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + wib, s_cs[wib]);
+  turn_rows<kBf16, U>(A, static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + wib, s_cs[wib]);
+}
+
+template <bool kBf16, int U>
+__global__ void __launch_bounds__(kRopeThreads, 7) norm_append_kernel(const __grid_constant__ RopeArgs A) {
+  constexpr int kWarps = kRopeThreads / 32;
+  __shared__ Angles s_angles[kWarps];
+  __shared__ uint4 s_rows[kWarps][U > 1 ? 64 * U : 1];
+  const int wib = threadIdx.x >> 5;
+  norm_rows<kBf16, U>(A, blockIdx.x * kWarps + wib, s_angles + wib, smem_addr(s_rows[wib]));
 }
 
 template <int U, bool kNorm>
 static int launch_rope(RopeArgs& A, bool bf16, cudaStream_t st) {
   A.chunks = (A.rows + 4 * U - 1) / (4 * U);
   const long long grid = (A.n_tok * A.chunks + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  if (grid > 0x7fffffffll) return PA_ERR_UNSUPPORTED;
-  if (bf16)
-    rope_append_kernel<true, U, kNorm><<<static_cast<unsigned>(grid), kRopeThreads, 0, st>>>(A);
+  if (grid > (kNorm ? 0x3fffffffll : 0x7fffffffll)) return PA_ERR_UNSUPPORTED;  // (norms count warps in 32 bits)
+  const unsigned n = static_cast<unsigned>(grid);
+  if constexpr (kNorm)
+    bf16 ? norm_append_kernel<true, U><<<n, kRopeThreads, 0, st>>>(A) : norm_append_kernel<false, U><<<n, kRopeThreads, 0, st>>>(A);
   else
-    rope_append_kernel<false, U, kNorm><<<static_cast<unsigned>(grid), kRopeThreads, 0, st>>>(A);
+    bf16 ? rope_append_kernel<true, U><<<n, kRopeThreads, 0, st>>>(A) : rope_append_kernel<false, U><<<n, kRopeThreads, 0, st>>>(A);
   return cuda_status(cudaGetLastError());
 }
 
@@ -112,8 +126,15 @@ static int rope_append(pa_pool_t p, const void* q, int64_t q_stride, int n_q_hea
   // and 4.00; 120 rows a token (162) 64 tokens 2.83 and 2.67, 128 3.39 and 3.11
   const long long quads = A.n_tok * ((A.rows + 3) / 4);
   const bool few = quads <= 32ll * sm_count(p->device), bf16 = p->dtype == PA_BF16;
+  const bool norm = q_weight || k_weight;
   cudaStream_t st = as_stream(stream);
-  if (q_weight || k_weight) return few ? launch_rope<1, true>(A, bf16, st) : launch_rope<3, true>(A, bf16, st);
+  // with norms: 4 rows a warp, or 16 that wait in shared memory; those pay only for
+  // tokens of many rows.  us with 4 and with 16, captured calls: 48 rows a token
+  // (the switch is at 405 tokens) 200 tokens 2.96 and 3.84, 400 4.25 and 4.15, 800
+  // 6.30 and 5.06, 4,000 27.1 and 21.5; 16 rows a token 1,531 tokens 4.73 and 5.92,
+  // 6,000 15.1 and 16.5
+  const bool few_norm = few || A.rows < 32;
+  if (norm) return few_norm ? launch_rope<1, true>(A, bf16, st) : launch_rope<4, true>(A, bf16, st);
   return few ? launch_rope<1, false>(A, bf16, st) : launch_rope<3, false>(A, bf16, st);
 }
 

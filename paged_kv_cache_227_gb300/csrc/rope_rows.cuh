@@ -29,7 +29,7 @@ struct RopeArgs {
   long long n_tok, num_slots;
   int Hq, Hkv, half_vecs;    // half_vecs = rot / 16: lanes of a row that turn
   int interleaved;
-  int rows;                  // rows of a token that turn_rows takes: Hq + 2 Hkv, or the Hq query rows alone
+  int rows;                  // rows of a token: Hq + 2 Hkv, or the Hq query rows alone
   int chunks;                // warps a token's rows are cut into
   float eps;
   long long* err;
@@ -54,15 +54,6 @@ __device__ __forceinline__ float turns(int p, float f) {
   float r = (u - rintf(u)) + (w - rintf(w));
   r += (eu + ew) + (a + b) * g_lo;
   return r - rintf(r);
-}
-
-// cos and sin of pair f of token t.
-__device__ __forceinline__ float2 cos_sin(const RopeArgs& A, long long t, int f) {
-  const uint32_t word = f < 32 ? (f < 16 ? A.axis[0] : A.axis[1]) : (f < 48 ? A.axis[2] : A.axis[3]);
-  const int p = A.positions[((word >> (2 * (f & 15))) & 3) * A.n_tok + t];
-  float c, s;
-  sincospif(2.f * turns(p, A.inv_freq[f]), &s, &c);
-  return make_float2(c, s);
 }
 
 template <bool kBf16>
@@ -95,57 +86,121 @@ __device__ __forceinline__ uint4 pack8f(const float f[8]) {
                     pack2<kBf16>(f[6], f[7]));
 }
 
-// 1 / rms of a row of 128 whose 8 lanes (an aligned octet) hold 16 elements
-// each; every lane of the warp takes part.  The sum of squares is fp32: 128
-// terms of one sign, off by at most 2^-20 of itself.
-__device__ __forceinline__ float inverse_rms(const float a[8], const float b[8], float eps) {
-  float s = 0.f, z = 0.f;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    s = fmaf(a[k], a[k], s);
-    z = fmaf(b[k], b[k], z);
+// Packed pairs of fp32: one instruction for two elements.
+__device__ __forceinline__ unsigned long long bits2(float2 a) { return *reinterpret_cast<unsigned long long*>(&a); }
+__device__ __forceinline__ float2 floats2(unsigned long long a) { return *reinterpret_cast<float2*>(&a); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+  return floats2(d);
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+  return floats2(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return floats2(d);
+}
+
+// Cosines and sines of a row's angles, in shared memory; pair f = 8j + e, of lane
+// j, is element e % 4 of vector 8 (e / 4) + j, so that the lanes of a row read 128
+// bytes on end.  The angle is reduced to at most half a turn first, where the
+// hardware's sine and cosine are off by at most 2^-21: below what 16 bits (or 8)
+// keep, and a third of sincospif's instructions.
+struct Angles {
+  float4 c[kMaxPairs / 4], s[kMaxPairs / 4], minus_s[kMaxPairs / 4];
+};
+
+// A lane's part of a row of 128: 8 lanes (an aligned octet) hold it, lane j the 8
+// elements from 8 v0 (a) and the 8 from 8 v1 (b).
+struct RowPart {
+  float2 a[4], b[4];
+  template <bool kBf16>
+  __device__ __forceinline__ void unpack(const uint4& x, const uint4& y) {
+    a[0] = unpack2<kBf16>(x.x), a[1] = unpack2<kBf16>(x.y), a[2] = unpack2<kBf16>(x.z), a[3] = unpack2<kBf16>(x.w);
+    b[0] = unpack2<kBf16>(y.x), b[1] = unpack2<kBf16>(y.y), b[2] = unpack2<kBf16>(y.z), b[3] = unpack2<kBf16>(y.w);
   }
-  s += z;
-  s += __shfl_xor_sync(0xffffffffu, s, 1);
-  s += __shfl_xor_sync(0xffffffffu, s, 2);
-  s += __shfl_xor_sync(0xffffffffu, s, 4);
-  return rsqrtf(fmaf(s, 1.f / kHeadDim, eps));
-}
-
-// x r w for a lane's 16 elements; w0 and w1 are the weights of its two vectors.
-template <bool kBf16>
-__device__ __forceinline__ void scale_row(float a[8], float b[8], float r, const uint4& w0, const uint4& w1) {
-  float w[8];
-  unpack8f<kBf16>(w0, w);
+  // 1 / rms of the row; every lane of the warp takes part.  128 terms of one sign
+  // in chains of 8: off by at most 2^-20 of itself.
+  __device__ __forceinline__ float inverse_rms(float eps) const {
+    float2 s = mul2(a[0], a[0]);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) a[k] = a[k] * r * w[k];
-  unpack8f<kBf16>(w1, w);
+    for (int k = 1; k < 4; ++k) s = fma2(a[k], a[k], s);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) b[k] = b[k] * r * w[k];
-}
-
-// Turns a lane's 8 pairs: (a[k], b[k]) in halves, adjacent elements of a and
-// then of b interleaved.  cs(k) is the pair's cos and sin.
-template <class CosSin>
-__device__ __forceinline__ void turn_row(float a[8], float b[8], bool interleaved, CosSin cs) {
-  if (interleaved) {
+    for (int k = 0; k < 4; ++k) s = fma2(b[k], b[k], s);
+    float t = s.x + s.y;
+    t += __shfl_xor_sync(0xffffffffu, t, 1);
+    t += __shfl_xor_sync(0xffffffffu, t, 2);
+    t += __shfl_xor_sync(0xffffffffu, t, 4);
+    return rsqrtf(fmaf(t, 1.f / kHeadDim, eps));
+  }
+  __device__ __forceinline__ void times(const RowPart& w) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float2 ca = cs(k), cb = cs(4 + k);
-      const float x = a[2 * k], y = a[2 * k + 1], u = b[2 * k], w = b[2 * k + 1];
-      a[2 * k] = x * ca.x - y * ca.y;
-      a[2 * k + 1] = y * ca.x + x * ca.y;
-      b[2 * k] = u * cb.x - w * cb.y;
-      b[2 * k + 1] = w * cb.x + u * cb.y;
+      a[k] = mul2(a[k], w.a[k]);
+      b[k] = mul2(b[k], w.b[k]);
     }
-  } else {
+  }
+  __device__ __forceinline__ void times(float r) {
+    const float2 rr = make_float2(r, r);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 c = cs(k);
-      const float x = a[k], y = b[k];
-      a[k] = x * c.x - y * c.y;
-      b[k] = y * c.x + x * c.y;
+    for (int k = 0; k < 4; ++k) {
+      a[k] = mul2(a[k], rr);
+      b[k] = mul2(b[k], rr);
     }
+  }
+  // Turns the lane's 8 pairs: elements k of a and b in halves, adjacent elements of
+  // a and then of b interleaved.
+  __device__ __forceinline__ void turn(bool interleaved, const Angles& t, int j) {
+    const float4 c0 = t.c[j], c1 = t.c[8 + j], s0 = t.s[j], s1 = t.s[8 + j];
+    const float2 cc[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
+    const float2 ss[4] = {{s0.x, s0.y}, {s0.z, s0.w}, {s1.x, s1.y}, {s1.z, s1.w}};
+    if (!interleaved) {
+      const float4 m0 = t.minus_s[j], m1 = t.minus_s[8 + j];
+      const float2 mm[4] = {{m0.x, m0.y}, {m0.z, m0.w}, {m1.x, m1.y}, {m1.z, m1.w}};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = fma2(b[k], mm[k], mul2(a[k], cc[k]));
+        b[k] = fma2(a[k], ss[k], mul2(b[k], cc[k]));
+        a[k] = x;
+      }
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // pair k of the lane: element pair k of a, or k - 4 of b
+      const float2 x = a[k], y = b[k];
+      const float cx = k & 1 ? cc[k >> 1].y : cc[k >> 1].x, sx = k & 1 ? ss[k >> 1].y : ss[k >> 1].x;
+      const float cy = k & 1 ? cc[2 + (k >> 1)].y : cc[2 + (k >> 1)].x, sy = k & 1 ? ss[2 + (k >> 1)].y : ss[2 + (k >> 1)].x;
+      a[k] = make_float2(x.x * cx - x.y * sx, x.y * cx + x.x * sx);
+      b[k] = make_float2(y.x * cy - y.y * sy, y.y * cy + y.x * sy);
+    }
+  }
+};
+template <bool kBf16>
+__device__ __forceinline__ uint4 pack_part(const float2 (&x)[4]) {
+  return make_uint4(pack2<kBf16>(x[0].x, x[0].y), pack2<kBf16>(x[1].x, x[1].y), pack2<kBf16>(x[2].x, x[2].y),
+                    pack2<kBf16>(x[3].x, x[3].y));
+}
+
+// kThreads threads (a CTA's, or a warp's) take rows t0 .. t0 + rows - 1.
+template <int kThreads>
+__device__ __forceinline__ void fill_angles(const RopeArgs& A, Angles* to, long long t0, int rows) {
+  const int pairs = 8 * A.half_vecs, thread = threadIdx.x % kThreads;
+#pragma unroll 4
+  for (int x = thread; x < rows * kMaxPairs; x += kThreads) {
+    const int r = x / kMaxPairs, f = x % kMaxPairs;
+    if (f >= pairs) continue;
+    const uint32_t word = f < 32 ? (f < 16 ? A.axis[0] : A.axis[1]) : (f < 48 ? A.axis[2] : A.axis[3]);
+    const int p = A.positions[((word >> (2 * (f & 15))) & 3) * A.n_tok + t0 + r];
+    const float a = 6.283185307f * turns(p, A.inv_freq[f]);
+    const int at = 4 * (8 * (f >> 2 & 1) + (f >> 3)) + (f & 3);
+    const float sine = __sinf(a);
+    reinterpret_cast<float*>(to[r].c)[at] = __cosf(a);
+    reinterpret_cast<float*>(to[r].s)[at] = sine;
+    reinterpret_cast<float*>(to[r].minus_s)[at] = -sine;
   }
 }
 
@@ -155,7 +210,7 @@ __device__ __forceinline__ void turn_row(float a[8], float b[8], bool interleave
 // interleaved) or copies vectors 2j and 2j + 1.  U row quads of a warp are
 // loaded before the first is turned.  Products and sums are fp32; one rounding
 // to 16 bits.  s_cs: the warp's kMaxPairs entries of shared memory.
-template <bool kBf16, int U, bool kNorm>
+template <bool kBf16, int U>
 __device__ __forceinline__ void turn_rows(const RopeArgs& A, long long w, float2* s_cs) {
   const int lane = threadIdx.x & 31;
   const long long t = w / A.chunks;
@@ -175,7 +230,6 @@ __device__ __forceinline__ void turn_rows(const RopeArgs& A, long long w, float2
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int r = r0 + 4 * u;
-    if (kNorm) x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);  // (all lanes take part in the rows' sums)
     if (r >= rows) continue;
     const int h = r < A.Hq ? r : (r < A.Hq + A.Hkv ? r - A.Hq : r - A.Hq - A.Hkv);
     const uint16_t* base = r < A.Hq ? A.q + t * A.q_stride
@@ -189,7 +243,13 @@ __device__ __forceinline__ void turn_rows(const RopeArgs& A, long long w, float2
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int f = lane + 32 * e;
-    if (f < 8 * A.half_vecs) s_cs[f] = cos_sin(A, t, f);
+    if (f < 8 * A.half_vecs) {
+      const uint32_t word = lane < 16 ? A.axis[2 * e] : A.axis[2 * e + 1];
+      const int p = A.positions[((word >> (2 * (lane & 15))) & 3) * A.n_tok + t];
+      float c, s;
+      sincospif(2.f * turns(p, A.inv_freq[f]), &s, &c);
+      s_cs[f] = make_float2(c, s);
+    }
   }
   __syncwarp();
   float2 cs[8];
@@ -204,41 +264,161 @@ __device__ __forceinline__ void turn_rows(const RopeArgs& A, long long w, float2
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int r = r0 + 4 * u;
-    const bool takes_part = r < rows && (r < A.Hq || to_cache);
+    if (r >= rows || (r >= A.Hq && !to_cache)) continue;
     uint16_t* to = r < A.Hq ? A.q_out + t * A.q_out_stride + r * kHeadDim
                             : (r < A.Hq + A.Hkv ? A.k_pool + (row + (r - A.Hq) * kBlock) * kHeadDim
                                                 : A.v_pool + (row + (r - A.Hq - A.Hkv) * kBlock) * kHeadDim);
     uint4* dst = reinterpret_cast<uint4*>(to);
-    if (kNorm) {
-      float a[8], b[8];
-      unpack8f<kBf16>(x[u][0], a);
-      unpack8f<kBf16>(x[u][1], b);
-      const float rr = inverse_rms(a, b, A.eps);
-      if (!takes_part) continue;
-      if (r < A.Hq + A.Hkv) {
-        const uint16_t* weight = r < A.Hq ? A.q_weight : A.k_weight;
-        if (weight)
-          scale_row<kBf16>(a, b, rr, __ldg(reinterpret_cast<const uint4*>(weight) + v0),
-                           __ldg(reinterpret_cast<const uint4*>(weight) + v1));
-        if (turn) turn_row(a, b, A.interleaved != 0, [&](int k) { return cs[k]; });
-        x[u][0] = pack8f<kBf16>(a);
-        x[u][1] = pack8f<kBf16>(b);
-      }
-      dst[v0] = x[u][0];
-      dst[v1] = x[u][1];
-      continue;
-    }
-    if (!takes_part) continue;
+    uint32_t a[4] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w};
+    uint32_t b[4] = {x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
     if (turn && r < A.Hq + A.Hkv) {
-      float a[8], b[8];
-      unpack8f<kBf16>(x[u][0], a);
-      unpack8f<kBf16>(x[u][1], b);
-      turn_row(a, b, A.interleaved != 0, [&](int k) { return cs[k]; });
-      x[u][0] = pack8f<kBf16>(a);
-      x[u][1] = pack8f<kBf16>(b);
+      if (A.interleaved) {  // word k of vector e holds pair 8j + 4e + k
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 xa = unpack2<kBf16>(a[k]), xb = unpack2<kBf16>(b[k]);
+          const float2 ca = cs[k], cb = cs[4 + k];
+          a[k] = pack2<kBf16>(xa.x * ca.x - xa.y * ca.y, xa.y * ca.x + xa.x * ca.y);
+          b[k] = pack2<kBf16>(xb.x * cb.x - xb.y * cb.y, xb.y * cb.x + xb.x * cb.y);
+        }
+      } else {  // word k of both vectors holds pairs 8j + 2k, + 1
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 xa = unpack2<kBf16>(a[k]), xb = unpack2<kBf16>(b[k]);
+          const float2 c0 = cs[2 * k], c1 = cs[2 * k + 1];
+          a[k] = pack2<kBf16>(xa.x * c0.x - xb.x * c0.y, xa.y * c1.x - xb.y * c1.y);
+          b[k] = pack2<kBf16>(xb.x * c0.x + xa.x * c0.y, xb.y * c1.x + xa.y * c1.y);
+        }
+      }
     }
-    dst[v0] = x[u][0];
-    dst[v1] = x[u][1];
+    dst[v0] = make_uint4(a[0], a[1], a[2], a[3]);
+    dst[v1] = make_uint4(b[0], b[1], b[2], b[3]);
+  }
+}
+
+// turn_rows with norms.  The weight comes before the rotation (it belongs to a dim),
+// 1 / rms, one number a row, behind it.  Four rows (a quad) go together; quads of query
+// rows alone, nearly all of them, take a path whose branches are the warp's, not the
+// rows' (the others spend a third of their instructions on those).
+// What bounds it is the bytes that a resident warp has on their way (its rows) times
+// the warps that its registers leave room for.  So with U > 1 the rows wait in shared
+// memory: a lane copies the 32 bytes of each row that it will read (cp.async), needs
+// no barrier for its own bytes, and no registers for rows that it has not come to.
+// s_rows: 1 KiB a quad; with U = 1 not used.
+__device__ __forceinline__ void copy16_async(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+// Waits until at most n of the lane's groups are on their way (n < 8).
+__device__ __forceinline__ void wait_async(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+  }
+}
+
+template <bool kBf16, int U>
+__device__ __forceinline__ void norm_rows(const RopeArgs& A, unsigned w, Angles* s_angles, uint32_t s_rows) {
+  static_assert(U <= 8, "wait_async");
+  const int lane = threadIdx.x & 31;
+  const unsigned token = w / static_cast<unsigned>(A.chunks);
+  if (token >= A.n_tok) return;
+  const int r0 = static_cast<int>(w - token * A.chunks) * 4 * U, kv = A.Hq + A.Hkv;  // the first row
+  const long long t = token;
+  const int j = lane & 7, sub = lane >> 3;
+  const bool turn = j < A.half_vecs;
+  const int v0 = turn && !A.interleaved ? j : 2 * j;
+  const int v1 = turn && !A.interleaved ? j + A.half_vecs : 2 * j + 1;
+  const uint4* const q = reinterpret_cast<const uint4*>(A.q + t * A.q_stride) + (r0 + sub) * (kHeadDim / 8);
+  const uint32_t mine = s_rows + 16 * lane;
+  uint4 only[2];  // U = 1
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int r = r0 + 4 * u + sub;
+    const uint4* from = q + 4 * u * (kHeadDim / 8);
+    if (r0 + 4 * u + 4 > A.Hq && r >= A.Hq)
+      from = reinterpret_cast<const uint4*>(r < kv ? A.k + t * A.k_stride + (r - A.Hq) * kHeadDim
+                                                   : A.v + t * A.v_stride + (r - kv) * kHeadDim);
+    if (U == 1) {
+      only[0] = only[1] = make_uint4(0, 0, 0, 0);
+      if (r < A.rows) only[0] = from[v0], only[1] = from[v1];
+    } else {
+      if (r < A.rows) {
+        copy16_async(mine + 1024 * u, from + v0);
+        copy16_async(mine + 1024 * u + 512, from + v1);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  }
+  fill_angles<32>(A, s_angles, t, 1);
+  __syncwarp();
+  // (an octet whose row is past the end sums what it finds; nothing of it leaves the octet)
+  auto row = [&](int u, uint4 (&x)[2]) {
+    if (U == 1) {
+      x[0] = only[0], x[1] = only[1];
+    } else {
+      wait_async(U - 1 - u);
+      x[0] = shared16(mine + 1024 * u), x[1] = shared16(mine + 1024 * u + 512);
+    }
+  };
+  auto norm_and_turn = [&](RowPart& y, const uint4* weight, float rr) {
+    if (weight) {
+      RowPart wt;
+      wt.unpack<kBf16>(__ldg(weight + v0), __ldg(weight + v1));
+      y.times(wt);
+    }
+    if (turn) y.turn(A.interleaved, *s_angles, j);
+    if (weight) y.times(rr);
+  };
+  uint4* const q_out = reinterpret_cast<uint4*>(A.q_out + t * A.q_out_stride) + (r0 + sub) * (kHeadDim / 8);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (r0 + 4 * u + 4 > A.Hq) break;
+    uint4 x[2];
+    row(u, x);
+    RowPart y;
+    y.unpack<kBf16>(x[0], x[1]);
+    const float rr = y.inverse_rms(A.eps);
+    norm_and_turn(y, reinterpret_cast<const uint4*>(A.q_weight), rr);
+    q_out[4 * u * (kHeadDim / 8) + v0] = pack_part<kBf16>(y.a);
+    q_out[4 * u * (kHeadDim / 8) + v1] = pack_part<kBf16>(y.b);
+  }
+  if (r0 + 4 * U <= A.Hq) return;
+  // quads that hold K or V rows
+  const long long slot = A.slots[t];
+  const bool to_cache = slot >= 0 && slot < A.num_slots;
+  if (slot >= A.num_slots && lane == 0 && r0 < kv) record_error(A.err, PA_ERR_DEVICE_CHECK, slot);
+  const long long at = (slot >> 4) * A.Hkv * kBlock + (slot & 15);  // row of kv head 0
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int r = r0 + 4 * u + sub;
+    if (r0 + 4 * u + 4 <= A.Hq) continue;
+    if (r0 + 4 * u >= A.rows) break;
+    uint4 x[2];
+    row(u, x);
+    RowPart y;
+    y.unpack<kBf16>(x[0], x[1]);
+    const float rr = y.inverse_rms(A.eps);
+    if (r >= A.rows || (r >= A.Hq && !to_cache)) continue;
+    uint4* dst = reinterpret_cast<uint4*>(
+        r < A.Hq ? A.q_out + t * A.q_out_stride + r * kHeadDim
+                 : (r < kv ? A.k_pool + (at + (r - A.Hq) * kBlock) * kHeadDim : A.v_pool + (at + (r - kv) * kBlock) * kHeadDim));
+    if (r < kv) {
+      norm_and_turn(y, reinterpret_cast<const uint4*>(r < A.Hq ? A.q_weight : A.k_weight), rr);
+      x[0] = pack_part<kBf16>(y.a);
+      x[1] = pack_part<kBf16>(y.b);
+    }
+    dst[v0] = x[0];
+    dst[v1] = x[1];
   }
 }
 
