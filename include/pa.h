@@ -462,8 +462,8 @@ int pa_norm_rope_append8(pa_pool8_t pool, int dtype, const void* q, int64_t q_st
  * over the values that the codes stand for.  q [num_seqs][n_q_heads][128] of
  * q_dtype PA_FP16 or PA_BF16; block_tables, seq_lens, out as for pa_decode.  A
  * head's query elements below 2^-28 of its largest may lose bits (bf16); weights
- * are carried to 2^-22 of themselves or 2^-35 of the row's largest, sums in
- * fp32.  Codes and exponents past a sequence's end may be anything.  A block id
+ * are carried to 2^-22 of themselves or 2^-31 of the row's largest, sums in
+ * fp32 (where V's scales lie 2^100 apart, the smallest blocks' share may vanish).  Codes and exponents past a sequence's end may be anything.  A block id
  * out of range counts as not attended (reported by pa_check8).  n_q_heads /
  * n_kv_heads <= 8, num_seqs <= 4096, max_blocks_per_seq <= PA_MAX_WALKED_BLOCKS,
  * (max_blocks_per_seq + 1) times num_seqs or n_kv_heads below 2^31 - 1 and times

@@ -234,13 +234,19 @@ class Pool8:
         self.k_scale, self.v_scale = scale[:, :, 0], scale[:, :, 1]
 
     @property
-    def handle(self):
-        return self._h.ptr
+    def handle(self):  # (a pa_pool8_t is no pa_pool_t: the calls of the one read past the other)
+        raise TypeError("this call takes a Pool, got a Pool8")
 
     def close(self):
         if self._h.ptr:
             self.k = self.v = self.k_scale = self.v_scale = None
             self._h.destroy()
+
+
+def _handle8(pool):
+    if not isinstance(pool, Pool8):
+        raise TypeError(f"this call takes a Pool8, got {type(pool).__name__}")
+    return pool._h.ptr
 
 
 def pa_pool_bytes(num_blocks, n_kv_heads, dtype, block_size=BLOCK_SIZE, d_head=HEAD_DIM):
@@ -536,7 +542,7 @@ def pa_norm_rope_append8(pool, q, k_new, v_new, q_weight, k_weight, positions, i
     are consecutive, in the order of their slots."""
     dtype = _row_dtype(q, "q")
     rows, turn, to = _rope_at(pool, dtype, q, k_new, v_new, positions, inv_freq, axis_of_pair, slot_mapping, q_out)
-    _check(lib.pa_norm_rope_append8(pool.handle, _DTYPE_CODE[dtype], *rows, _norm_at(pool, dtype, q_weight, "q_weight"),
+    _check(lib.pa_norm_rope_append8(_handle8(pool), _DTYPE_CODE[dtype], *rows, _norm_at(pool, dtype, q_weight, "q_weight"),
                                     _norm_at(pool, dtype, k_weight, "k_weight"), float(eps), *turn,
                                     1 if interleaved else 0, *to, _raw_stream(pool, stream)), "pa_norm_rope_append8")
 
@@ -550,13 +556,13 @@ def pa_cache_append8(pool, k_new, v_new, slot_mapping, stream=None):
     n = slot_mapping.numel()
     if k_new.shape != (n, pool.n_kv_heads, HEAD_DIM) or v_new.shape != k_new.shape:
         raise ValueError("k_new/v_new must be [n_tok][n_kv_heads][128]")
-    _check(lib.pa_cache_append8(pool.handle, _DTYPE_CODE[dtype], ka, va, sa, n, _raw_stream(pool, stream)),
+    _check(lib.pa_cache_append8(_handle8(pool), _DTYPE_CODE[dtype], ka, va, sa, n, _raw_stream(pool, stream)),
            "pa_cache_append8")
 
 
 def decode8_workspace_for(pool, q, block_tables, stream=None):
     """Workspace of pa_decode8 for these sizes."""
-    n = lib.pa_decode8_workspace_bytes(pool.handle, q.shape[0], q.shape[1], block_tables.shape[1])
+    n = lib.pa_decode8_workspace_bytes(_handle8(pool), q.shape[0], q.shape[1], block_tables.shape[1])
     return _workspace(n, "pa_decode8_workspace_bytes", pool.device, stream)
 
 
@@ -567,7 +573,7 @@ def pa_decode8(pool, q, block_tables, seq_lens, scale, out, workspace=None, stre
     qa, ta, la, oa, code, B, Hq, W = _decode_at(pool, q, block_tables, seq_lens, out, dtype)
     if workspace is None:
         workspace = decode8_workspace_for(pool, q, block_tables, stream)
-    _check(lib.pa_decode8(pool.handle, qa, _DTYPE_CODE[dtype], ta, W, la, B, Hq, float(scale), oa, code,
+    _check(lib.pa_decode8(_handle8(pool), qa, _DTYPE_CODE[dtype], ta, W, la, B, Hq, float(scale), oa, code,
                           _at(pool, workspace, "workspace", torch.uint8), workspace.numel(), _raw_stream(pool, stream)),
            "pa_decode8")
 
@@ -587,7 +593,7 @@ def _both_pools(pool, pool8):
 def pa_copy_blocks8(pool, src, dst, stream=None):
     """pa_copy_blocks for a Pool8."""
     sa = _block_ids(pool, src, "src")
-    _check(lib.pa_copy_blocks8(pool.handle, sa, _block_ids(pool, dst, "dst", src.numel()), src.numel(),
+    _check(lib.pa_copy_blocks8(_handle8(pool), sa, _block_ids(pool, dst, "dst", src.numel()), src.numel(),
                                _raw_stream(pool, stream)), "pa_copy_blocks8")
 
 
@@ -598,7 +604,7 @@ def pa_quantize_blocks(pool, src, pool8, dst, rows=None, stream=None):
     sa = _block_ids(pool8, src, "src")
     da = _block_ids(pool8, dst, "dst", src.numel())
     ra = None if rows is None else _block_ids(pool8, rows, "rows", src.numel())
-    _check(lib.pa_quantize_blocks(pool.handle, sa, pool8.handle, da, ra, src.numel(), _raw_stream(pool8, stream)),
+    _check(lib.pa_quantize_blocks(pool.handle, sa, _handle8(pool8), da, ra, src.numel(), _raw_stream(pool8, stream)),
            "pa_quantize_blocks")
 
 
@@ -606,14 +612,14 @@ def pa_dequantize_blocks(pool8, src, pool, dst, stream=None):
     """Blocks src of a Pool8 into blocks dst of a Pool."""
     _both_pools(pool, pool8)
     sa = _block_ids(pool8, src, "src")
-    _check(lib.pa_dequantize_blocks(pool8.handle, sa, pool.handle, _block_ids(pool8, dst, "dst", src.numel()), src.numel(),
+    _check(lib.pa_dequantize_blocks(_handle8(pool8), sa, pool.handle, _block_ids(pool8, dst, "dst", src.numel()), src.numel(),
                                     _raw_stream(pool8, stream)), "pa_dequantize_blocks")
 
 
 def pa_check8(pool, stream=None):
     """pa_check for a Pool8."""
     detail = ctypes.c_int64()
-    code = lib.pa_check8(pool.handle, _stream(stream), ctypes.byref(detail))
+    code = lib.pa_check8(_handle8(pool), _stream(stream), ctypes.byref(detail))
     return code, detail.value
 
 

@@ -8,10 +8,18 @@
 // Bound: memory, 256 bytes a token and kv head, read once for all of the head's
 // G query heads (2 G flops a byte).  The tiles (16 tokens: 2 KiB of K, 2 KiB of
 // V on end) of all (sequence, kv head) segments, laid end to end, are cut into
-// equal ranges, one a warp, so that any length mix loads the GPU evenly; each
-// warp streams its range through a ring of its own in shared memory.  A segment
-// that a cut divides leaves a record a piece, which a second kernel joins by
-// log-sum-exp, in their order.
+// equal ranges, one a CTA and SM, so that any length mix loads the GPU evenly, and
+// those into equal ranges for the warps; each warp streams its own through a ring
+// in shared memory.  Where a cut divides a segment, the warps of a CTA leave
+// records in shared memory and join them there; at most one segment goes on from
+// one CTA to the next, and a second kernel joins those, by log-sum-exp, always in
+// the order of their tiles.  Few or short segments get a CTA each instead.
+//
+// Measured (captured calls): batch 64 of chats (108 MB) 29.5 us, 0.54 of the copy
+// rate, of which 3 us are lengths, tables and first tiles, 17 the stream, and 6 the
+// joins and what the SMs' ends lie apart; 16 multi-head sequences (276 MB) 52 us, 0.78;
+// four documents of 8 to 32 thousand tokens (161 MB) 35 us, 0.67; four short
+// requests 7.7 us.
 //
 // A tile is one TMA box, 32 rows of 128 bytes in the 128-byte swizzle, so that the
 // operand loads below meet no bank conflict.  Per tile, with mma.sync m16n8k16 (16
@@ -38,15 +46,21 @@
 
 namespace pa {
 
-#ifndef W8
-#define W8 12
-#define S8 3
-#endif
-constexpr int kWarps8 = W8;    // warps of a CTA, one CTA an SM
-constexpr int kStages8 = S8;   // tiles in flight of a warp
+// One CTA an SM, 12 warps with 3 tiles (4 KiB) in flight each: with 4 tiles, or with 8
+// warps of 6, the captured calls measured the same within 1 us, and the room goes to
+// the warps' records; 16 warps leave 128 registers and spill.
+constexpr int kWarps8 = 12;
+constexpr int kStages8 = 3;
+static_assert(2 * kWarps8 <= 32, "a lane a chain of pieces");
 constexpr int kSeqs8 = 4096;   // sequences of a call (their prefix lives in shared memory)
-constexpr int kMinUnits8 = 2;  // smallest range of a warp
-constexpr int kWholeBlocks8 = 8 * kWarps8;  // widest table of the plan with a CTA a segment
+constexpr int kMinUnits8 = 8;  // smallest range of a CTA (8, 16, 24: four short requests 7.7, 8.5, 9.1 us)
+// Widest tables of the plan with a CTA a segment, which needs no second kernel but
+// waits for its longest segment: for few segments, and for at least kManyWhole8 (the
+// balanced split then leaves records in every CTA).  us a call with it and with the
+// balanced split: 8 segments of 300, 500, 800 tokens 6.7, 7.6, 9.2 and 7.4, 7.8, 8.6;
+// 72 of 500, 1,100, 1,500 tokens 8.1, 10.6, 12.4 and 10.2, 11.8, 12.8; 128 of 1,500
+// tokens 14.8 and 18.0.
+constexpr int kFewBlocks8 = 32, kManyBlocks8 = 96, kManyWhole8 = 64;
 constexpr float kLog2e8 = 1.4426950408889634f;
 // The running maximum moves when a score passes it by 2^4; weights are carried
 // at 2^11 times their size, below 2^15, so that the low half's smallest step
@@ -54,7 +68,7 @@ constexpr float kLog2e8 = 1.4426950408889634f;
 constexpr float kMove8 = 4.f, kUp8 = 11.f;
 constexpr int kNear8 = 4;
 
-// Record of a piece: O as float4 number k * kLanes + r, then the heads' maxima (log2
+// Record of a piece: O, divided by its sums, as float4 number k * kLanes + r, then the heads' maxima (log2
 // units) and sums.  Lane (g, c) of a warp has k = 4e + q: head 2c + e, dims 16g + 4q
 // .. + 3; with up to 4 heads only c < 2 do (kLanes = 16).
 template <bool kTwice>
@@ -112,10 +126,9 @@ struct Segment8 {
       : s0(static_cast<long long>(A.Hkv) * pfx[i] + static_cast<long long>(h) * (pfx[i + 1] - pfx[i])),
         cnt(pfx[i + 1] - pfx[i]) {}
 };
-// Units of a warp in the balanced split over `ctas` CTAs.
-__device__ __forceinline__ long long per_warp8(const Decode8Args& A, const int* pfx, int ctas) {
-  const long long warps = static_cast<long long>(ctas) * kWarps8;
-  const long long per = (static_cast<long long>(A.Hkv) * pfx[A.B] + warps - 1) / warps;
+// Units of a CTA in the balanced split over `ctas` CTAs.
+__device__ __forceinline__ long long per_cta8(const Decode8Args& A, const int* pfx, int ctas) {
+  const long long per = (static_cast<long long>(A.Hkv) * pfx[A.B] + ctas - 1) / ctas;
   return per < kMinUnits8 ? kMinUnits8 : per;
 }
 
@@ -251,9 +264,10 @@ __device__ __forceinline__ float load_q8(const Decode8Args& A, int i, int h, int
 // 2^d for d <= 0 (0 below 2^-126).
 __device__ __forceinline__ float down2(int d) { return d < -126 ? 0.f : __int_as_float((127 + d) << 23); }
 
-// A running join of records: maximum, sum and four outputs, as they are weighted
-// by the maximum.  Records weigh 2^(m - maximum); one of -infinity has no weight,
-// but its NaN, if it holds one, still counts.
+// A running join of records: maximum, sum of weights and four outputs.  Records
+// weigh 2^(m - maximum) l; one of -infinity has no weight, but its NaN, if it holds
+// one, still counts.  Outputs are means throughout, here and in the records, so that
+// the sum of many large values does not leave fp32 where their mean does not.
 struct Join8 {
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -262,24 +276,28 @@ struct Join8 {
     float to = m;
 #pragma unroll
     for (int k = 0; k < N; ++k) to = fmaxf(to, rm[k]);
-    const float f = m == to ? 1.f : fast_exp2(m - to);
-    l *= f;
+    const float had = l * (m == to ? 1.f : fast_exp2(m - to));
+    float w[N];
+    l = had;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      w[k] = rl[k] * (rm[k] == to ? 1.f : fast_exp2(rm[k] - to));
+      l += w[k];
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l, f = had * inv;
     o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const float w = rm[k] == to ? 1.f : fast_exp2(rm[k] - to);
-      l = fmaf(w, rl[k], l);
-      o.x = fmaf(w, ro[k].x, o.x);
-      o.y = fmaf(w, ro[k].y, o.y);
-      o.z = fmaf(w, ro[k].z, o.z);
-      o.w = fmaf(w, ro[k].w, o.w);
+      const float a = w[k] * inv;
+      o.x = fmaf(a, ro[k].x, o.x);
+      o.y = fmaf(a, ro[k].y, o.y);
+      o.z = fmaf(a, ro[k].z, o.z);
+      o.w = fmaf(a, ro[k].w, o.w);
     }
     m = to;
   }
   __device__ __forceinline__ void store(const Decode8Args& A, int i, int h, int head, int dim) const {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    store_out4(A.out, (static_cast<long long>(i) * A.Hq + h * A.G + head) * kHeadDim + dim, o.x * inv, o.y * inv, o.z * inv,
-               o.w * inv, A.out_dtype);
+    store_out4(A.out, (static_cast<long long>(i) * A.Hq + h * A.G + head) * kHeadDim + dim, o.x, o.y, o.z, o.w, A.out_dtype);
   }
 };
 
@@ -326,13 +344,12 @@ __global__ void __launch_bounds__(kWarps8 * 32, 1) decode8_kernel(const __grid_c
     const Segment8 seg(A, pfx, i, blockIdx.x - i * A.Hkv);
     U0 = seg.s0;
     U1 = U0 + seg.cnt;
-    per = (seg.cnt + kWarps8 - 1) / kWarps8;
-    if (per < kMinUnits8) per = kMinUnits8;
   } else {
-    per = per_warp8(A, pfx, gridDim.x);
-    U0 = per * kWarps8 * blockIdx.x;
-    U1 = min(U0 + per * kWarps8, static_cast<long long>(A.Hkv) * pfx[A.B]);
+    per = per_cta8(A, pfx, gridDim.x);
+    U0 = per * blockIdx.x;
+    U1 = min(U0 + per, static_cast<long long>(A.Hkv) * pfx[A.B]);
   }
+  per = max((U1 - U0 + kWarps8 - 1) / kWarps8, 1ll);
   const long long u0 = U0 + per * warp, u1 = min(u0 + per, U1);
   const int n = static_cast<int>(max(u1 - u0, 0ll));
 
@@ -382,12 +399,12 @@ __global__ void __launch_bounds__(kWarps8 * 32, 1) decode8_kernel(const __grid_c
     const int slot = seg.s0 > u0;
     // (a second record is the last piece's: the ring is done with)
     Record* const rec = slot ? reinterpret_cast<Record*>(smem8 + warp * (kStages8 * kPair8)) : firsts + warp;
-    const float unit_of_o = E ? scale_of(E) : 0.f;
+    const float unit_of_o = scale_of(E);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int head = 2 * c + e;
       if (kTwice && c >= 2) continue;
-      const float f = whole ? (l[e] == 0.f ? 0.f : 1.f / l[e]) : 1.f / (1 << static_cast<int>(kUp8));
+      const float f = l[e] == 0.f ? 0.f : 1.f / l[e];
       const long long at = (static_cast<long long>(ci) * A.Hq + ch * A.G + head) * kHeadDim + 16 * g;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -400,12 +417,11 @@ __global__ void __launch_bounds__(kWarps8 * 32, 1) decode8_kernel(const __grid_c
       }
       if (!whole && g == 0) {
         rec->m[head] = m[e];
-        rec->l[head] = l[e] * (1.f / (1 << static_cast<int>(kUp8)));
+        rec->l[head] = l[e];
       }
     }
     if (!whole && lane == 0 && (rs >= u0 || warp == 0)) {
-      const long long last = (end - 1 - U0) / per;
-      s_chain[warp][slot] = {ci, ch, static_cast<int>(min(last, kWarps8 - 1ll)),
+      s_chain[warp][slot] = {ci, ch, static_cast<int>((min(end, U1) - 1 - U0) / per),
                              rs >= U0 && end <= U1 ? 1 : 2 + (seg.s0 > U0)};
     }
   };
@@ -565,34 +581,42 @@ __global__ void __launch_bounds__(kWarps8 * 32, 1) decode8_kernel(const __grid_c
   if (ci >= 0) flush();
   __syncthreads();
   // pieces of one segment, joined: a warp a float4 a lane of each
-  for (int t = warp; t < 2 * kWarps8 * Record::kParts; t += kWarps8) {
-    const int first = t / Record::kParts >> 1, slot = t / Record::kParts & 1, f = t % Record::kParts * 32 + lane;
-    const Chain8 chain = s_chain[first][slot];
-    if (!chain.kind) continue;
-    const int head = Record::head(f);
-    Join8 join;
-    for (int w0 = first; w0 <= chain.last; w0 += 4) {
-      float rm[4], rl[4];
-      float4 ro[4];
+  const Chain8* const chains = &s_chain[0][0];
+  uint32_t found = __ballot_sync(0xffffffffu, lane < 2 * kWarps8 && chains[lane < 2 * kWarps8 ? lane : 0].kind != 0);
+  for (int t = warp, seen = 0; found; found &= found - 1, seen += Record::kParts) {
+    const int number = __ffs(found) - 1, first = number >> 1;
+    for (; t < seen + Record::kParts; t += kWarps8) {
+      const Chain8 chain = chains[number];
+      const int f = (t - seen) * 32 + lane, head = Record::head(f);
+      const Record* second = reinterpret_cast<const Record*>(smem8 + first * (kStages8 * kPair8));
+      constexpr int kBatch = 4;
+      Join8 join;
+      for (int w = first; w <= chain.last; w += kBatch) {
+        float rm[kBatch], rl[kBatch];
+        float4 ro[kBatch];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int w = w0 + k;
-        const Record* rec = slot && w == first ? reinterpret_cast<const Record*>(smem8 + w * (kStages8 * kPair8)) : firsts + w;
-        const bool in = w <= chain.last;
-        rm[k] = in ? rec->m[head] : -INFINITY;
-        rl[k] = in ? rec->l[head] : 0.f;
-        ro[k] = in ? rec->o[f] : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < kBatch; ++k) {
+          rm[k] = -INFINITY;
+          rl[k] = 0.f;
+          ro[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (w + k <= chain.last) {
+            const Record* rec = w + k == first && (number & 1) ? second : firsts + w + k;
+            rm[k] = rec->m[head];
+            rl[k] = rec->l[head];
+            ro[k] = rec->o[f];
+          }
+        }
+        join.add(rm, rl, ro);
       }
-      join.add(rm, rl, ro);
-    }
-    if (chain.kind == 1) {
-      if (head < A.G) join.store(A, chain.i, chain.h, head, Record::dim(f));
-    } else {
-      Record* rec = static_cast<Record*>(A.rec) + 2 * blockIdx.x + (chain.kind - 2);
-      rec->o[f] = join.o;
-      if (Record::dim(f) == 0) {
-        rec->m[head] = join.m;
-        rec->l[head] = join.l;
+      if (chain.kind == 1) {
+        if (head < A.G) join.store(A, chain.i, chain.h, head, Record::dim(f));
+      } else {
+        Record* rec = static_cast<Record*>(A.rec) + 2 * blockIdx.x + (chain.kind - 2);
+        rec->o[f] = join.o;
+        if (Record::dim(f) == 0) {
+          rec->m[head] = join.m;
+          rec->l[head] = join.l;
+        }
       }
     }
   }
@@ -606,7 +630,7 @@ __global__ void __launch_bounds__(32 * Record8<kTwice>::kParts) merge8_kernel(co
   extern __shared__ uint8_t smem_raw8[];
   int* const pfx = reinterpret_cast<int*>(smem_raw8);
   prefix8(A, pfx, false);
-  const long long per = per_warp8(A, pfx, gridDim.x + 1) * kWarps8, total = static_cast<long long>(A.Hkv) * pfx[A.B];
+  const long long per = per_cta8(A, pfx, gridDim.x + 1), total = static_cast<long long>(A.Hkv) * pfx[A.B];
   const long long next = per * (blockIdx.x + 1ll);  // the range behind
   int count = 0, i = 0, h = 0;
   bool second = false;
@@ -669,7 +693,7 @@ static int launch_decode8(Decode8Args& A, int device, cudaStream_t st) {
     allowed.fetch_or(bit, std::memory_order_relaxed);
   }
   const long long segments = static_cast<long long>(A.B) * A.Hkv;
-  A.whole = segments <= sms && A.max_blocks <= kWholeBlocks8;
+  A.whole = segments <= sms && A.max_blocks <= (segments >= kManyWhole8 ? kManyBlocks8 : kFewBlocks8);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

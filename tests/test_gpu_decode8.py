@@ -153,6 +153,21 @@ def test_scales_that_differ_widely(pa, lens, kind):
     c.check(c.call())
 
 
+@pytest.mark.parametrize("e", [0, 1, 40, 247])
+@pytest.mark.parametrize("L", [9, 3000])
+def test_values_at_the_ends_of_the_exponents(pa, e, L):
+    """All of V at one exponent: the outputs scale with it (2^-127 to 2^120; fp32 output, below its largest number)."""
+    c = Case(pa, [L], 4, 1, "int8", seed=e)
+    c.ev[:] = 127
+    c.refill()
+    want = c.call().double()
+    c.ev[:] = e
+    c.refill()
+    # (subnormal outputs are rounded to 2^-149)
+    got, size = c.call().double(), 2.0 ** (e - 127)
+    assert (got - want * size).abs().max() <= 2.0 ** -22 * (want * size).abs().max() + 2.0 ** -148
+
+
 def test_tokens_that_one_outweighs_keep_their_values(pa):
     """4,096 tokens behind one that outweighs each by 2^26: their sum is 2^-14 of the weight."""
     c = Case(pa, [4097], 4, 1, "int8", torch.float16)
@@ -330,6 +345,23 @@ def test_refusals(pa):
     assert L.pa_decode8(c.pool.handle, *args[:3], 1 << 27, args[4], 2, 8, 0.1, *tail) == pa.PA_ERR_UNSUPPORTED
     assert L.pa_decode8_workspace_bytes(c.pool.handle, 4097, 8, 1) == 0
     assert (out == 0).all()
+
+
+def test_pools_of_the_other_kind_are_refused(pa):
+    p16, p8 = pa.Pool(2, 2, torch.bfloat16), pa.Pool8(2, 2, torch.int8)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    q, out = (torch.zeros(1, 4, D, dtype=torch.bfloat16, device="cuda") for _ in "qo")
+    rows, slots = torch.zeros(1, 2, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    for call in (lambda: pa.pa_decode8(p16, q, i32(0)[None], i32(1), SCALE, out), lambda: pa.pa_cache_append8(p16, rows, rows, slots),
+                 lambda: pa.pa_copy_blocks8(p16, i32(0), i32(1)), lambda: pa.pa_check8(p16)):
+        with pytest.raises(TypeError, match="takes a Pool8"):
+            call()
+    q8, rows8 = q.to(torch.int8), rows.to(torch.int8)
+    for call in (lambda: pa.pa_decode(p8, q8, i32(0)[None], i32(1), SCALE, out), lambda: pa.pa_copy_blocks(p8, i32(0), i32(1)),
+                 lambda: pa.pa_cache_append(p8, rows8, rows8, slots), lambda: pa.pa_check(p8),
+                 lambda: pa.pa_decode_split(p8, q8, i32(0)[None], i32(1), SCALE, out)):
+        with pytest.raises(TypeError, match="takes a Pool, got a Pool8"):
+            call()
 
 
 def test_the_pool_lives_as_long_as_its_views(pa):

@@ -48,6 +48,18 @@ def test_row_types_are_refused():
         pa.pa_quantize_blocks(fake_pool(BF), torch.zeros(1, dtype=I32), p8, torch.zeros(1, dtype=I32))
 
 
+def test_a_pool_of_the_other_kind_is_refused():
+    """A pa_pool8_t is no pa_pool_t: neither call may reach the library with the other's handle."""
+    p8 = pa.Pool8.__new__(pa.Pool8)
+    with pytest.raises(TypeError, match="takes a Pool, got a Pool8"):
+        p8.handle
+    with pytest.raises(TypeError, match="takes a Pool, got a Pool8"):
+        pa.pa_check(p8, types.SimpleNamespace(cuda_stream=0))
+    for call in (pa.pa_check8, lambda p, s: pa.decode8_workspace_for(p, torch.zeros(1, 4, 128), torch.zeros(1, 1), s)):
+        with pytest.raises(TypeError, match="takes a Pool8"):
+            call(fake_pool(BF), types.SimpleNamespace(cuda_stream=0))
+
+
 def test_null_pools_and_bad_sizes_are_refused():
     L, bad, none = pa.lib, pa.PA_ERR_INVALID, None
     turn = (none, 1, none, none, 128, 0, none, 1, none, 0, none)
