@@ -237,6 +237,10 @@ class Pool8:
     def handle(self):  # (a pa_pool8_t is no pa_pool_t: the calls of the one read past the other)
         raise TypeError("this call takes a Pool, got a Pool8")
 
+    @property
+    def handle8(self):
+        return self._h.ptr
+
     def close(self):
         if self._h.ptr:
             self.k = self.v = self.k_scale = self.v_scale = None
@@ -246,7 +250,7 @@ class Pool8:
 def _handle8(pool):
     if not isinstance(pool, Pool8):
         raise TypeError(f"this call takes a Pool8, got {type(pool).__name__}")
-    return pool._h.ptr
+    return pool.handle8
 
 
 def pa_pool_bytes(num_blocks, n_kv_heads, dtype, block_size=BLOCK_SIZE, d_head=HEAD_DIM):

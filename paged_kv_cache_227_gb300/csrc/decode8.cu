@@ -15,11 +15,11 @@
 // one CTA to the next, and a second kernel joins those, by log-sum-exp, always in
 // the order of their tiles.  Few or short segments get a CTA each instead.
 //
-// Measured (captured calls): batch 64 of chats (108 MB) 29.5 us, 0.54 of the copy
+// Measured (captured calls): batch 64 of chats (108 MB) 29.6 us, 0.54 of the copy
 // rate, of which 3 us are lengths, tables and first tiles, 17 the stream, and 6 the
 // joins and what the SMs' ends lie apart; 16 multi-head sequences (276 MB) 52 us, 0.78;
 // four documents of 8 to 32 thousand tokens (161 MB) 35 us, 0.67; four short
-// requests 7.7 us.
+// requests 8.1 us.
 //
 // A tile is one TMA box, 32 rows of 128 bytes in the 128-byte swizzle, so that the
 // operand loads below meet no bank conflict.  Per tile, with mma.sync m16n8k16 (16
@@ -53,7 +53,7 @@ constexpr int kWarps8 = 12;
 constexpr int kStages8 = 3;
 static_assert(2 * kWarps8 <= 32, "a lane a chain of pieces");
 constexpr int kSeqs8 = 4096;   // sequences of a call (their prefix lives in shared memory)
-constexpr int kMinUnits8 = 8;  // smallest range of a CTA (8, 16, 24: four short requests 7.7, 8.5, 9.1 us)
+constexpr int kMinUnits8 = 8;  // smallest range of a CTA (8, 16, 24: four short requests, 7.7, 8.5, 9.1 us)
 // Widest tables of the plan with a CTA a segment, which needs no second kernel but
 // waits for its longest segment: for few segments, and for at least kManyWhole8 (the
 // balanced split then leaves records in every CTA).  us a call with it and with the

@@ -286,7 +286,7 @@ def test_writes_stay_inside(pa):
     c = Case(pa, [16 * n for n in range(1, 40)] + [3000], 8, 2, "int8")
     B = len(c.lens)
     tables, lens = cuda(c.tables), cuda(np.asarray(c.lens, np.int32))
-    n = pa.lib.pa_decode8_workspace_bytes(c.pool.handle, B, 8, tables.shape[1])
+    n = pa.lib.pa_decode8_workspace_bytes(c.pool.handle8, B, 8, tables.shape[1])
     ws = torch.full((n + 512,), 0xAB, dtype=torch.uint8, device="cuda")
     out = torch.full((B + 2, 8, D), 7.0, device="cuda")
     pa.pa_decode8(c.pool, c.q, tables, lens, SCALE, out[1:-1], workspace=ws[256:256 + n])
@@ -339,11 +339,11 @@ def test_refusals(pa):
     L, none = pa.lib, None
     args = (c.q.data_ptr(), pa.PA_BF16, t.data_ptr(), t.shape[1], lens.data_ptr())
     tail = (out.data_ptr(), pa.PA_FP32, ws.data_ptr(), ws.numel(), none)
-    assert L.pa_decode8(c.pool.handle, *args, 4097, 8, 0.1, *tail) == pa.PA_ERR_UNSUPPORTED
-    assert L.pa_decode8(c.pool.handle, *args, 2, 7, 0.1, *tail) == pa.PA_ERR_INVALID
-    assert L.pa_decode8(c.pool.handle, args[0], pa.PA_FP32, *args[2:], 2, 8, 0.1, *tail) == pa.PA_ERR_INVALID
-    assert L.pa_decode8(c.pool.handle, *args[:3], 1 << 27, args[4], 2, 8, 0.1, *tail) == pa.PA_ERR_UNSUPPORTED
-    assert L.pa_decode8_workspace_bytes(c.pool.handle, 4097, 8, 1) == 0
+    assert L.pa_decode8(c.pool.handle8, *args, 4097, 8, 0.1, *tail) == pa.PA_ERR_UNSUPPORTED
+    assert L.pa_decode8(c.pool.handle8, *args, 2, 7, 0.1, *tail) == pa.PA_ERR_INVALID
+    assert L.pa_decode8(c.pool.handle8, args[0], pa.PA_FP32, *args[2:], 2, 8, 0.1, *tail) == pa.PA_ERR_INVALID
+    assert L.pa_decode8(c.pool.handle8, *args[:3], 1 << 27, args[4], 2, 8, 0.1, *tail) == pa.PA_ERR_UNSUPPORTED
+    assert L.pa_decode8_workspace_bytes(c.pool.handle8, 4097, 8, 1) == 0
     assert (out == 0).all()
 
 
