@@ -144,6 +144,10 @@ CASES = [  # pieces, Hq, Hkv, dtype, kind, rot, axes, interleaved, fused, norms
     ([(3, 4)] * 9, 8, 8, torch.bfloat16, "int8", 96, 1, False, True, "k"),
     ([(0, 33), (31, 2)], 5, 5, torch.float16, "e4m3", 16, 3, False, False, "q"),
     ([(8, 700)], 10, 2, torch.bfloat16, "e4m3", 128, 1, True, True, ""),
+    # query rows that wait in shared memory
+    ([(8, 300), (0, 290), (77, 220)], 30, 3, torch.float16, "int8", 64, 1, True, False, "qk"),
+    ([(5, 400), (300, 380)], 32, 2, torch.bfloat16, "e4m3", 128, 1, False, True, "q"),
+    ([(1, 900)], 28, 1, torch.float16, "e4m3", 96, 1, False, True, "k"),
 ]
 
 

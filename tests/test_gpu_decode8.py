@@ -97,6 +97,41 @@ def test_batches(pa, B):
     ok8(pa, c.pool)
 
 
+@pytest.mark.parametrize("Hq,Hkv,B", [(6, 1, 3), (4, 2, 9), (8, 4, 15), (8, 4, 16), (12, 2, 40), (4, 2, 80)])
+@pytest.mark.parametrize("width", [31, 32, 33, 95, 96, 97, 5000])
+def test_tables_of_every_width(pa, Hq, Hkv, B, width):
+    """The table's width and the number of segments choose the plan, not the result: both sides of each limit
+    (32 and 96 blocks, 64 segments, the SMs), also with lengths far below the width."""
+    rng = np.random.default_rng(width * B)
+    top = min(width, 97) * BS
+    lens = rng.integers(0, top + 1, B)
+    lens[:3] = top, 0, top - 15
+    c = Case(pa, lens.tolist(), Hq, Hkv, "e4m3" if B % 2 else "int8", seed=B, width=width)
+    c.check(c.call())
+    ok8(pa, c.pool)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (6, 1)])
+@pytest.mark.parametrize("lens", [[3000, 77, 500], [20] * 40, [9000]])
+def test_any_blocks_out_of_range(pa, Hq, Hkv, lens):
+    """A third of the table's entries name no block, first and last ones among them: softmax over what is left."""
+    c = Case(pa, lens, Hq, Hkv, "int8", seed=4)
+    k, v = values8(c.k, c.ek, c.kind), values8(c.v, c.ev, c.kind)
+    q, want, bound = to64(c.q), np.zeros((len(lens), Hq, D)), 0.0
+    for i, L in enumerate(lens):
+        keep = np.ones(L, bool)
+        kr, vr = cache_rows(k, c.tables[i], L), cache_rows(v, c.tables[i], L)
+        for j in range(-(-L // BS)):
+            if c.rng.random() < 0.3 or (i == 0 and j in (0, (L - 1) // BS)):
+                c.tables[i, j] = int(c.rng.choice([-1, -(1 << 31), c.pool.num_blocks, (1 << 31) - 1]))
+                keep[j * BS:(j + 1) * BS] = False
+        want[i] = attend64(q[i], kr[:, keep], vr[:, keep], SCALE)[0]
+        a = np.einsum("hgd,htd->hgt", np.abs(q[i]).reshape(Hkv, -1, D), np.abs(kr)).max() * SCALE
+        bound = max(bound, 2 * (2.0 ** -19 + 2 * a * 2.0 ** -20) * np.abs(vr).max())
+    assert np.abs(to64(c.call()) - want).max() <= bound
+    assert pa.pa_check8(c.pool)[0] == pa.PA_ERR_DEVICE_CHECK
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_what_is_behind_the_end_does_not_count(pa, kind):
     """NaN codes, NaN exponents and table entries that name no block, behind the sequences' ends."""

@@ -72,6 +72,11 @@ CASES = [  # n, Hq, Hkv, dtype, rot, axes, interleaved, fused, norms
     (33, 12, 2, torch.float16, 64, 2, True, False, "k"),
     (129, 7, 1, torch.bfloat16, 96, 1, False, True, "qk"),
     (1531, 5, 1, torch.float16, 128, 4, False, False, "qk"),
+    # rows that wait in shared memory: query rows alone in a quad and not, a last quad with one row
+    (420, 32, 8, torch.bfloat16, 128, 2, False, True, "qk"),
+    (620, 30, 3, torch.float16, 64, 1, True, False, "qk"),
+    (560, 27, 7, torch.bfloat16, 96, 1, False, True, "q"),
+    (700, 40, 40, torch.float16, 128, 1, True, True, "k"),
 ]
 
 
@@ -98,6 +103,23 @@ def test_against_the_definition(pa, n, Hq, Hkv, dtype, rot, n_axes, interleaved,
     assert np.array_equal(vrows[slots[at]], to64(t.v)[at]), "v moves bit for bit"
     rest = np.setdiff1d(np.arange(nb * BS), slots[at])
     assert np.array_equal(rows[rest], to64(k0).transpose(0, 2, 1, 3).reshape(-1, Hkv, D)[rest])
+    pool.close()
+
+
+@pytest.mark.parametrize("far", [1 << 24, 1 << 31])
+@pytest.mark.parametrize("n", [70, 700])
+def test_far_positions(pa, n, far):
+    """The angle in turns is off by 2^-23 up to 2^24 and by 2^-19.5 for any 32-bit position (tests of the
+    rotary append): 2^-18 and 2^-16 of |x| + |y| with the norm's share, before the rounding."""
+    rng = np.random.default_rng(far % 1000 + n)
+    dtype = torch.float16
+    t = Tokens(rng, n, 32, 2, dtype, 128, 2, False)
+    t.pos = rng.integers(-far, far, (2, n), dtype=np.int64).astype(np.int32)
+    pool, w = pa.Pool(-(-n // BS), 2, dtype), weight(rng, dtype)
+    pa.pa_norm_rope_append(pool, *t.args(w, w, np.arange(n)))
+    ref, normed = t.want(t.q, w)
+    slack = (2.0 ** -18 if far <= 1 << 24 else 2.0 ** -16) * pair_size(normed, 128, False)
+    assert (np.abs(to64(t.q_out) - ref) <= half_step(dtype) * (np.abs(ref) + slack) + slack + 2.0 ** -25).all()
     pool.close()
 
 
