@@ -15,11 +15,11 @@
 // one CTA to the next, and a second kernel joins those, by log-sum-exp, always in
 // the order of their tiles.  Few or short segments get a CTA each instead.
 //
-// Measured (captured calls): batch 64 of chats (108 MB) 29.6 us, 0.54 of the copy
-// rate, of which 3 us are lengths, tables and first tiles, 17 the stream, and 6 the
-// joins and what the SMs' ends lie apart; 16 multi-head sequences (276 MB) 52 us, 0.78;
-// four documents of 8 to 32 thousand tokens (161 MB) 35 us, 0.67; four short
-// requests 8.1 us.
+// Measured (captured calls, three inputs in turn): batch 64 of chats (108 MB) 26.4 us,
+// 0.61 of the copy rate (a call alone from a cold L2, with its launch, 35 us): 3 us
+// are lengths, tables and first tiles, 17 the stream, 6 the joins and what the SMs'
+// ends lie apart; 16 multi-head sequences (276 MB) 49 us, 0.83; four documents of 8 to
+// 32 thousand tokens (161 MB) 33 us, 0.72; four short requests 7.7-8.1 us.
 //
 // A tile is one TMA box, 32 rows of 128 bytes in the 128-byte swizzle, so that the
 // operand loads below meet no bank conflict.  Per tile, with mma.sync m16n8k16 (16
@@ -46,9 +46,10 @@
 
 namespace pa {
 
-// One CTA an SM, 12 warps with 3 tiles (4 KiB) in flight each: with 4 tiles, or with 8
-// warps of 6, the captured calls measured the same within 1 us, and the room goes to
-// the warps' records; 16 warps leave 128 registers and spill.
+// One CTA an SM, 12 warps with 3 tiles (4 KiB) in flight each.  us for 64 chats, 16
+// multi-head sequences and four documents: 29.2, 52.2, 35.1; 10 warps of 4 tiles 30.5,
+// 56.4, 37.9; 8 of 5 31.9, 57.9, 39.5; 11 of 3 30.0, 52.6, 35.9; 13 of 3 (fewer
+// registers, spills) 31.9, 55.2, 38.0.
 constexpr int kWarps8 = 12;
 constexpr int kStages8 = 3;
 static_assert(2 * kWarps8 <= 32, "a lane a chain of pieces");
@@ -68,9 +69,9 @@ constexpr float kLog2e8 = 1.4426950408889634f;
 constexpr float kMove8 = 4.f, kUp8 = 11.f;
 constexpr int kNear8 = 4;
 
-// Record of a piece: O, divided by its sums, as float4 number k * kLanes + r, then the heads' maxima (log2
-// units) and sums.  Lane (g, c) of a warp has k = 4e + q: head 2c + e, dims 16g + 4q
-// .. + 3; with up to 4 heads only c < 2 do (kLanes = 16).
+// Record of a piece: O, divided by its sums, as float4 number k * kLanes + r, then the
+// heads' maxima (log2 units) and sums.  Lane (g, c) of a warp has k = 4e + q: head 2c +
+// e, dims 16g + 4q .. + 3; with up to 4 heads only c < 2 do (kLanes = 16).
 template <bool kTwice>
 struct Record8 {
   static constexpr int kLanes = kTwice ? 16 : 32;
@@ -189,13 +190,19 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The K and V tile number `tile` of the pool into shared memory.
+// The K and V tile number `tile` of the pool into shared memory.  Tiles are read once,
+// so they leave L2 first and push out neither records nor tables nor what the
+// caller's next kernels read (captured calls over three inputs in turn: 29.2 -> 26.6
+// us for 64 chats; from a cold L2 the same time with and without).
 __device__ __forceinline__ void load_tile8(uint32_t to, const CUtensorMap* map, int tile, uint32_t bar) {
   const int z = 0;
+  uint64_t policy;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
   mbar_arrive_expect_tx(bar, kPair8);
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3}], [%4];" ::"r"(to),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(z), "r"(tile), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %2, %3}],"
+      " [%4], %5;" ::"r"(to),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(z), "r"(tile), "r"(bar), "l"(policy)
       : "memory");
 }
 
