@@ -153,7 +153,7 @@ def _exponent(amax, kind):
 
 def _power(e):
     """2^(e - 127) in 64 bits, NaN for 255."""
-    p = torch.where(e > 0, e.int() << 23, 1 << 22).to(torch.int32).view(torch.float32).double()
+    p = torch.ldexp(torch.ones((), dtype=torch.float64, device=e.device), e.int() - 127)
     return torch.where(e == 255, torch.full_like(p, torch.nan), p)
 
 
