@@ -440,10 +440,12 @@ int pa_check8(pa_pool8_t pool, void* stream, int64_t* detail);
  *    what they stood for is lost);
  *  - any other run keeps the block's scale if that holds its rows too; if not, the
  *    scale grows and the codes of the block's other rows are rounded to it.
- * The rows of one block have to be one run of the call: a block that two runs
- * name, or a slot named twice, ends up with the codes and the scale of either
- * (no other block is touched).  Slots out of range are skipped and reported by
- * pa_check8. */
+ * The rows of one block have to be one run of the call.  Where two runs name a
+ * block (rows in the order of the tokens, not of the sequences, or a slot twice), at
+ * most one of them is written for each kv head, K and V apart, and not always the same
+ * one; the others are skipped and reported by pa_check8 (PA_ERR_DEVICE_CHECK, with the
+ * first slot of one), and rows of earlier calls are kept.  Slots out of range are
+ * skipped and reported too.  Two calls in flight at once must not name the same block. */
 int pa_cache_append8(pa_pool8_t pool, int dtype, const void* k_new, const void* v_new, const int64_t* slot_mapping,
                      int n_tok, void* stream);
 

@@ -5,7 +5,8 @@
 // other inside one block.  For every kv head, K and V apart, a run's rows get
 // one power-of-two scale, the smallest that holds their largest magnitude, and,
 // unless the run starts its block, no smaller one than the block has; where
-// the block's scale grows, the codes of its other rows move to it.
+// the block's scale grows, the codes of its other rows move to it.  Of two runs in
+// one block one is skipped and reported.
 //
 // Bound: memory (512 B read and 256 B written a K or V row; 512 B a query row),
 // and latency for the tokens of a decode step.  Two warps take 16 consecutive rows
@@ -26,13 +27,14 @@ namespace pa {
 
 constexpr int kTok8 = 16;                 // rows of a task
 constexpr int kThreads8 = 256;
-constexpr int kTasks8 = kThreads8 / 64;   // (kv head, K|V) of a CTA
+static_assert(kTasks8 == kThreads8 / 64, "(kv head, K|V) of a CTA");
 constexpr int kAngleRows = 2 * kTok8 - 1; // a run that starts in the window ends at most 15 rows behind it
 
 struct Append8Args {
   RopeArgs R;          // rows = query rows; k_pool and v_pool unused
   uint8_t* codes;
   uint8_t* exps;
+  uint32_t* claims;
   int groups;          // CTAs that share a window's K and V rows
   unsigned kv_ctas;
 };
@@ -47,9 +49,22 @@ __device__ __forceinline__ float max_abs(float a, float b) {
 // Largest k <= r whose row starts a run (bit k of cont clear).
 __device__ __forceinline__ int leader_of(uint32_t cont, int r) { return 31 - __clz(~cont & ((2u << r) - 1)); }
 
+// Two runs of a call in one block would each move the block's rows to a scale of its
+// own.  So the run that starts in row r leaves r + 1 in the claim of the block and the
+// CTA's four tiles, and of two the later one to come finds the other's there.  Claims
+// are not cleared: what an earlier call left counts only where the row that it names has,
+// in this call, a slot of the same block and is none of the run's own.  One warp asks for all
+// four, before its rows are loaded (64 tokens 5.2 -> 5.4 us, 7,900 42.0 -> 42.4; behind
+// the loads 5.6 and 42.7; a claim a tile 5.5 and 43.6).
+__device__ __forceinline__ bool another_run(const RopeArgs& R, uint32_t claim, long long row, int behind, long long slot) {
+  const long long r = static_cast<long long>(claim) - 1;
+  if (r < 0 || r >= R.n_tok || (r >= row && r <= row + behind)) return false;
+  return R.slots[r] >> 4 == slot >> 4;
+}
+
 template <bool kBf16, bool kE4M3>
 __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_angles) {
-  __shared__ uint32_t s_top[2][kTasks8][kTok8];
+  __shared__ uint32_t s_top[2][kTasks8][kTok8], s_clash[2];
   const RopeArgs& R = A.R;
   const int lane = threadIdx.x & 31, mine8 = threadIdx.x >> 6, half = threadIdx.x >> 5 & 1;
   const int group = blockIdx.x % A.groups;
@@ -80,6 +95,7 @@ __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_ang
   const long long stride = is_v ? R.v_stride : R.k_stride;
   const uint16_t* weight = is_v || !active ? nullptr : R.k_weight;
   bool angles = R.half_vecs && group * kTasks8 < R.Hkv;  // still to be computed
+  const bool claims = threadIdx.x < 32;  // (the first task of a CTA is an active one)
   int pass = 0;
   // (every warp of the CTA goes through the same passes)
   while (todo) {
@@ -91,6 +107,19 @@ __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_ang
     if (f + kTok8 < 32 && ((contm >> (f + kTok8)) & 1)) lead &= (1u << leader_of(cont, kTok8 - 1)) - 1;
     todo &= ~((lead | 1u) << f);  // (a run has at most 16 rows: the first one is never cut)
     const uint32_t part = (goodm >> f) & 0xffffu;
+    // row f + l in lane l < 16: its tile, its place in the run and the tile's scale
+    const int l = lane & 15;
+    const long long my_slot = __shfl_sync(0xffffffffu, slot, min(f + l + 1, 31));
+    const int first = leader_of(cont, l);
+    const bool taken = active && ((part >> l) & 1) && ((lead >> first) & 1);
+    const long long tile = ((my_slot >> 4) * R.Hkv + h) * 2 + is_v;
+    const int off = static_cast<int>(my_slot & (kBlock - 1)), off0 = off - (l - first);
+    const int was = taken ? A.exps[tile] : 0;
+    const uint32_t next = (~cont & 0xffffu) >> 1 >> l;  // bit i: row l + 1 + i starts a run
+    const int last = next ? l + __ffs(next) - 1 : kTok8 - 1;
+    const bool heads_run = taken && l == first && lane < kTok8;
+    const uint32_t claim =
+        claims && heads_run ? atomicExch(A.claims + (my_slot >> 4) * A.groups + group, static_cast<uint32_t>(base + f + l + 1)) : 0;
     // this lane's rows: 8 half + sub and 4 behind it
     bool mine[2];
     uint4 x[2][2];
@@ -105,15 +134,6 @@ __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_ang
         x[p][1] = src[v1];
       }
     }
-    // row f + l in lane l < 16: its tile, its place in the run and the tile's scale
-    const int l = lane & 15;
-    const long long my_slot = __shfl_sync(0xffffffffu, slot, min(f + l + 1, 31));
-    const int first = leader_of(cont, l);
-    const bool taken = active && ((part >> l) & 1) && ((lead >> first) & 1);
-    const long long tile = ((my_slot >> 4) * R.Hkv + h) * 2 + is_v;
-    const int off = static_cast<int>(my_slot & (kBlock - 1)), off0 = off - (l - first);
-    const int was = taken ? A.exps[tile] : 0;
-
     if (angles) {  // of the window's rows and of the run that leaves it, once, with the first rows on their way
       const int end = kTok8 + __ffs(~(contm >> kTok8)) - 1;  // (bit 31 of contm is clear)
       fill_angles<kThreads8>(R, s_angles, base, static_cast<int>(min(static_cast<long long>(end), R.n_tok - base)));
@@ -147,7 +167,14 @@ __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_ang
       t = max(t, __shfl_xor_sync(0xffffffffu, t, 4));
       if (j == 0) s_top[pass & 1][mine8][r] = mine[p] ? t : 0;
     }
+    if (claims) {
+      const bool clash = heads_run && another_run(R, claim, base + f + l, last - l, my_slot);
+      if (clash) record_error(R.err, PA_ERR_DEVICE_CHECK, my_slot);
+      const uint32_t all = __ballot_sync(0xffffffffu, clash);
+      if (lane == 0) s_clash[pass & 1] = all;
+    }
     __syncthreads();  // (the next pass writes the other half of s_top)
+    const uint32_t clashes = s_clash[pass & 1];
     // the run's magnitude to each of its rows
     uint32_t most = s_top[pass & 1][mine8][l];
     ++pass;
@@ -156,8 +183,6 @@ __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_ang
       const uint32_t t = __shfl_up_sync(0xffffffffu, most, d, 16);
       if (l - d >= first) most = max(most, t);
     }
-    const uint32_t next = (~cont & 0xffffu) >> 1 >> l;  // bit i: row l + 1 + i starts a run
-    const int last = next ? l + __ffs(next) - 1 : kTok8 - 1;
     most = __shfl_sync(0xffffffffu, most, last, 16);
     int e = exponent_for<kE4M3>(most);
     if (off0 > 0 && was > e) e = was;
@@ -168,7 +193,7 @@ __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_ang
       const int er = __shfl_sync(0xffffffffu, e, r);
       const long long tr = __shfl_sync(0xffffffffu, tile, r);
       const int at = __shfl_sync(0xffffffffu, off, r);
-      if (!mine[p]) continue;
+      if (!mine[p] || (clashes >> leader_of(cont, r) & 1)) continue;
       y[p].times(inverse_scale(er));
       uint8_t* dst = A.codes + tr * kTile8 + at * kRow8;
       const float2 *a = y[p].a, *b = y[p].b;
@@ -183,11 +208,11 @@ __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_ang
         *reinterpret_cast<uint4*>(dst + 8 * v0) = make_uint4(c0.x, c0.y, c1.x, c1.y);
       }
     }
-    const bool heads_run = taken && l == first && lane < kTok8;
-    if (heads_run && half == 0) A.exps[tile] = static_cast<uint8_t>(e);
+    const bool writes = heads_run && !(clashes >> l & 1);
+    if (writes && half == 0) A.exps[tile] = static_cast<uint8_t>(e);
 
     // blocks whose scale grew: the codes of their other rows, half of the tile a warp
-    uint32_t grown = __ballot_sync(0xffffffffu, heads_run && off0 > 0 && e > was && e != kNanExponent);
+    uint32_t grown = __ballot_sync(0xffffffffu, writes && off0 > 0 && e > was && e != kNanExponent);
     while (grown) {
       const int r = __ffs(grown) - 1;
       grown &= grown - 1;
@@ -239,7 +264,7 @@ template <int U, bool kNorm>
 static int launch_append8(Append8Args& A, bool bf16, bool e4m3, cudaStream_t st) {
   const RopeArgs& R = A.R;
   A.R.chunks = (R.rows + 4 * U - 1) / (4 * U);
-  A.groups = (2 * R.Hkv + kTasks8 - 1) / kTasks8;
+  A.groups = claim_groups(R.Hkv);
   const long long kv = (R.n_tok + kTok8 - 1) / kTok8 * A.groups;
   const long long q = (R.n_tok * A.R.chunks + kThreads8 / 32 - 1) / (kThreads8 / 32);
   if (kv > 0x3fffffffll || q > 0x1fffffffll) return PA_ERR_UNSUPPORTED;  // (warps of query rows are counted in 32 bits)
@@ -258,6 +283,7 @@ static int launch_append8(Append8Args& A, bool bf16, bool e4m3, cudaStream_t st)
 static int launch8(pa_pool8_t p, Append8Args& A, bool bf16, void* stream) {
   A.codes = p->codes;
   A.exps = p->exps;
+  A.claims = p->claims;
   A.R.num_slots = static_cast<long long>(p->num_blocks) * kBlock;
   A.R.err = p->err;
   A.R.rows = A.R.Hq;

@@ -21,6 +21,8 @@ constexpr int kRow8 = kHeadDim;               // bytes of a row of codes
 constexpr int kTile8 = kBlock * kRow8;        // of a tile: 2 KiB
 constexpr int kPair8 = 2 * kTile8;            // K tile, then V tile of a (block, kv head)
 constexpr int kNanExponent = 255;
+constexpr int kTasks8 = 4;                    // tiles of a block that a CTA of the cache write has, with one claim
+constexpr int claim_groups(int n_kv_heads) { return (2 * n_kv_heads + kTasks8 - 1) / kTasks8; }
 
 // Biased exponent of the smallest power of two 2^x >= 2^-126 whose largest code
 // (448 or 127) holds a magnitude, given as its bits; 255 if it is not finite.

@@ -28,7 +28,9 @@ struct pa_pool {
 
 // One 8-bit pool: codes [num_blocks][n_kv_heads][K|V][16][128], so that a
 // (block, head)'s K and V, which a decode reads together, are 4 KiB on end, and
-// exponent bytes [num_blocks][n_kv_heads][K|V].
+// exponent bytes [num_blocks][n_kv_heads][K|V].  claims [num_blocks][groups of
+// tiles] name the row whose run wrote them last, so that two runs of one call in one
+// block show (the cache write).
 struct pa_pool8 {
   CUtensorMap tmap;   // a (block, head)'s 32 rows of codes as one box, 128-byte swizzle
   int num_blocks;
@@ -37,6 +39,7 @@ struct pa_pool8 {
   int device;
   uint8_t* codes;     // device
   uint8_t* exps;      // device
+  uint32_t* claims;   // device
   long long* err;     // device: [0] = status code, [1] = detail
 };
 

@@ -205,17 +205,20 @@ int pa_pool8_create(int num_blocks, int block_size, int n_kv_heads, int d_head, 
   p->dtype = dtype;
   if (cudaGetDevice(&p->device) != cudaSuccess) { delete p; return PA_ERR_CUDA; }
   const size_t tiles = static_cast<size_t>(num_blocks) * n_kv_heads;
+  const size_t claims = static_cast<size_t>(num_blocks) * claim_groups(n_kv_heads) * sizeof(uint32_t);
   int status = PA_OK;
   if (cudaMalloc(&p->codes, tiles * kPair8) != cudaSuccess || cudaMalloc(&p->exps, tiles * 2) != cudaSuccess ||
-      cudaMalloc(&p->err, 2 * sizeof(long long)) != cudaSuccess)
+      cudaMalloc(&p->claims, claims) != cudaSuccess || cudaMalloc(&p->err, 2 * sizeof(long long)) != cudaSuccess)
     status = PA_ERR_OOM;
   else if (cudaMemset(p->codes, 0, tiles * kPair8) != cudaSuccess || cudaMemset(p->exps, 0, tiles * 2) != cudaSuccess ||
+           cudaMemset(p->claims, 0, claims) != cudaSuccess ||
            cudaMemset(p->err, 0, 2 * sizeof(long long)) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess ||
            !encode_pool8_map(&p->tmap, p->codes, static_cast<long long>(tiles)))
     status = PA_ERR_CUDA;
   if (status != PA_OK) {
     cudaFree(p->codes);
     cudaFree(p->exps);
+    cudaFree(p->claims);
     cudaFree(p->err);
     cudaGetLastError();
     delete p;
@@ -233,6 +236,7 @@ int pa_pool8_destroy(pa_pool8_t p) {
   cudaDeviceSynchronize();
   cudaFree(p->codes);
   cudaFree(p->exps);
+  cudaFree(p->claims);
   cudaFree(p->err);
   cudaSetDevice(prev);
   delete p;
