@@ -472,7 +472,8 @@ int pa_norm_rope_append8(pa_pool8_t pool, int dtype, const void* q, int64_t q_st
  * both below 2^41 (else UNSUPPORTED); a finite scale (else INVALID).  workspace:
  * device, >= pa_decode8_workspace_bytes(...), 256-byte aligned, caller-owned; its
  * contents on entry do not matter, and calls that share one must not overlap on
- * the GPU.  The result does not depend on timing. */
+ * the GPU.  The result does not depend on timing; where a wait runs out
+ * (PA_ERR_TIMEOUT from pa_check8) the rows that it concerns are NaN. */
 size_t pa_decode8_workspace_bytes(pa_pool8_t pool, int num_seqs, int n_q_heads, int max_blocks_per_seq);
 int pa_decode8(pa_pool8_t pool, const void* q, int q_dtype, const int32_t* block_tables, int max_blocks_per_seq,
                const int32_t* seq_lens, int num_seqs, int n_q_heads, float scale, void* out, int out_dtype,
@@ -565,6 +566,16 @@ int pa_selftest_shared_timeout(pa_pool_t pool, const void* q, const int32_t* blo
                                const int32_t* members, int n_members, const int32_t* prefix_blocks,
                                int n_groups, void* out, int out_dtype, void* workspace,
                                size_t workspace_bytes, long long limit_ns, void* stream);
+
+/* The same for pa_decode8, with its arguments: some loads of CTA `cta` (-1: of every
+ * CTA; <= 65535, one that the call does not launch holds nothing) do not come.  As
+ * after any wait of pa_decode8 that ran out, which pa_check8 reports, `out` is NaN in
+ * the rows of each (sequence, kv head) that such a CTA has a part of; the other rows
+ * are right. */
+int pa_selftest_decode8_timeout(pa_pool8_t pool, const void* q, int q_dtype, const int32_t* block_tables,
+                                int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs, int n_q_heads,
+                                float scale, void* out, int out_dtype, void* workspace, size_t workspace_bytes,
+                                int cta, long long limit_ns, void* stream);
 
 /* Synchronises `stream`, reads and clears the pool's device error word.
  * Returns PA_OK, PA_ERR_DEVICE_CHECK or PA_ERR_TIMEOUT; *detail (may be NULL)

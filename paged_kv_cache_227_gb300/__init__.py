@@ -61,6 +61,8 @@ def _load():
                                        i32, vp, i64, vp]),
         "pa_decode8_workspace_bytes": (sz, [vp, i32, i32, i32]),
         "pa_decode8": (i32, [vp, vp, i32, vp, i32, vp, i32, i32, f32, vp, i32, vp, sz, vp]),
+        "pa_selftest_decode8_timeout": (i32, [vp, vp, i32, vp, i32, vp, i32, i32, f32, vp, i32, vp, sz, i32,
+                                              ctypes.c_longlong, vp]),
         "pa_copy_blocks8": (i32, [vp, vp, vp, i32, vp]),
         "pa_quantize_blocks": (i32, [vp, vp, vp, vp, vp, i32, vp]),
         "pa_dequantize_blocks": (i32, [vp, vp, vp, vp, i32, vp]),
@@ -570,16 +572,29 @@ def decode8_workspace_for(pool, q, block_tables, stream=None):
     return _workspace(n, "pa_decode8_workspace_bytes", pool.device, stream)
 
 
-def pa_decode8(pool, q, block_tables, seq_lens, scale, out, workspace=None, stream=None):
-    """Decode attention over a Pool8: q [B][Hq][128] fp16 or bf16, out [B][Hq][128]
-    of fp16, bf16 or fp32, tables and lengths as for pa_decode."""
+def _decode8_args(pool, q, block_tables, seq_lens, scale, out, workspace, stream):
+    """Checks of pa_decode8; the C call's arguments up to the stream."""
     dtype = _row_dtype(q, "q")
     qa, ta, la, oa, code, B, Hq, W = _decode_at(pool, q, block_tables, seq_lens, out, dtype)
     if workspace is None:
         workspace = decode8_workspace_for(pool, q, block_tables, stream)
-    _check(lib.pa_decode8(_handle8(pool), qa, _DTYPE_CODE[dtype], ta, W, la, B, Hq, float(scale), oa, code,
-                          _at(pool, workspace, "workspace", torch.uint8), workspace.numel(), _raw_stream(pool, stream)),
-           "pa_decode8")
+    return (_handle8(pool), qa, _DTYPE_CODE[dtype], ta, W, la, B, Hq, float(scale), oa, code,
+            _at(pool, workspace, "workspace", torch.uint8), workspace.numel()), workspace
+
+
+def pa_decode8(pool, q, block_tables, seq_lens, scale, out, workspace=None, stream=None):
+    """Decode attention over a Pool8: q [B][Hq][128] fp16 or bf16, out [B][Hq][128]
+    of fp16, bf16 or fp32, tables and lengths as for pa_decode."""
+    args, _own = _decode8_args(pool, q, block_tables, seq_lens, scale, out, workspace, stream)
+    _check(lib.pa_decode8(*args, _raw_stream(pool, stream)), "pa_decode8")
+
+
+def pa_selftest_decode8_timeout(pool, q, block_tables, seq_lens, scale, out, limit_ns, cta=-1, workspace=None, stream=None):
+    """pa_decode8 some of whose loads do not come, in one CTA or (-1) all: their
+    waits give up after limit_ns and PA_ERR_TIMEOUT is recorded (read it with
+    pa_check8).  Returns the launch status."""
+    args, _own = _decode8_args(pool, q, block_tables, seq_lens, scale, out, workspace, stream)
+    return lib.pa_selftest_decode8_timeout(*args, int(cta), int(limit_ns), _raw_stream(pool, stream))
 
 
 def _block_ids(pool, t, name, n=None):

@@ -100,6 +100,7 @@ struct Decode8Args {
   int out_dtype;
   int whole;                  // a CTA a segment, instead of equal ranges
   float qscale;               // scale * log2(e)
+  int hold;                   // self-test: loads of CTA hold - 1 (-1: of all CTAs) do not come, 0: none is held
   long long wait_limit_ns;
 };
 
@@ -230,6 +231,8 @@ __device__ __forceinline__ Window8 window8(const Decode8Args& A, const int* pfx,
   } else {
     record_error(A.err, PA_ERR_DEVICE_CHECK, blk);
   }
+  // (the first two units of a window: one of them is a tile, and loads behind them are on their way)
+  if (A.hold && (A.hold < 0 || A.hold == static_cast<int>(blockIdx.x) + 1) && (threadIdx.x & 31) < 2) w.tile = -1;
   return w;
 }
 
@@ -314,6 +317,32 @@ struct Join8 {
 struct Chain8 {
   int i, h, last, kind;  // kind: 0 none, 1 result, 2 and 3 record in slot 0 and 1
 };
+
+// What a CTA leaves whose wait ran out: NaN in the rows of each segment that it has
+// tiles of, and in its two records, so that a segment which goes on in another CTA gets
+// NaN from the second kernel too.
+template <bool kTwice>
+__device__ __noinline__ void give_up8(const Decode8Args& A, const int* pfx, long long U0, long long U1) {
+  using Record = Record8<kTwice>;
+  const float nan = __int_as_float(0x7fffffff);
+  for (long long u = U0; u < U1;) {
+    const Place8 p = place8(A, pfx, u);
+    const Segment8 seg(A, pfx, p.i, p.h);
+    if (seg.s0 + 1 < U1)  // (not where only its start is here)
+      for (int x = threadIdx.x; x < A.G * (kHeadDim / 4); x += blockDim.x)
+        store_out4(A.out, (static_cast<long long>(p.i) * A.Hq + p.h * A.G) * kHeadDim + 4 * x, nan, nan, nan, nan, A.out_dtype);
+    u = seg.s0 + seg.cnt;
+  }
+  if (A.whole) return;
+  for (int k = 0; k < 2; ++k) {
+    Record* rec = static_cast<Record*>(A.rec) + 2 * blockIdx.x + k;
+    for (int x = threadIdx.x; x < Record::kVecs; x += blockDim.x) rec->o[x] = make_float4(nan, nan, nan, nan);
+    if (threadIdx.x < 8) {
+      rec->m[threadIdx.x] = -INFINITY;
+      rec->l[threadIdx.x] = nan;
+    }
+  }
+}
 
 // kTwice: at most 4 heads, whose columns are repeated.
 template <bool kBf16, bool kE4M3, bool kTwice>
@@ -579,14 +608,19 @@ __global__ void __launch_bounds__(kWarps8 * 32, 1) decode8_kernel(const __grid_c
     issue(y, stage);
     stage = stage + 1 == kStages8 ? 0 : stage + 1;
   }
-  if (s_abort) {  // a wait ran out: nothing is left on its way into shared memory, with a limit again
+  if (flying) {  // a wait ran out: nothing is left on its way into shared memory, with a limit again
     const long long t0 = global_ns();
     for (int k = 0; k < kStages8; ++k)
-      while ((flying >> k & 1) && !mbar_try_wait(bars + 8 * k, parity >> k & 1) && global_ns() - t0 < A.wait_limit_ns) {
+      while ((flying >> k & 1) && !mbar_try_wait(bars + 8 * k, parity >> k & 1) && global_ns() - t0 < kDrainNs) {
       }
+  } else if (ci >= 0) {
+    flush();
   }
-  if (ci >= 0) flush();
   __syncthreads();
+  if (*static_cast<volatile int*>(&s_abort)) {
+    give_up8<kTwice>(A, pfx, U0, U1);
+    return;
+  }
   // pieces of one segment, joined: a warp a float4 a lane of each
   const Chain8* const chains = &s_chain[0][0];
   uint32_t found = __ballot_sync(0xffffffffu, lane < 2 * kWarps8 && chains[lane < 2 * kWarps8 ? lane : 0].kind != 0);
@@ -734,9 +768,9 @@ extern "C" size_t pa_decode8_workspace_bytes(pa_pool8_t p, int num_seqs, int n_q
   return decode8_records(p);
 }
 
-extern "C" int pa_decode8(pa_pool8_t p, const void* q, int q_dtype, const int32_t* block_tables, int max_blocks_per_seq,
-                          const int32_t* seq_lens, int num_seqs, int n_q_heads, float scale, void* out, int out_dtype,
-                          void* workspace, size_t workspace_bytes, void* stream) {
+static int decode8(pa_pool8_t p, const void* q, int q_dtype, const int32_t* block_tables, int max_blocks_per_seq,
+                   const int32_t* seq_lens, int num_seqs, int n_q_heads, float scale, void* out, int out_dtype,
+                   void* workspace, size_t workspace_bytes, void* stream, int hold, long long limit_ns) {
   if (!p || !q || !block_tables || !seq_lens || !out || num_seqs <= 0 || n_q_heads <= 0 || max_blocks_per_seq <= 0)
     return PA_ERR_INVALID;
   if ((q_dtype != PA_FP16 && q_dtype != PA_BF16) || (out_dtype != PA_FP16 && out_dtype != PA_BF16 && out_dtype != PA_FP32))
@@ -769,9 +803,26 @@ extern "C" int pa_decode8(pa_pool8_t p, const void* q, int q_dtype, const int32_
   A.G = n_q_heads / p->n_kv_heads;
   A.out_dtype = out_dtype;
   A.qscale = scale * kLog2e8;
-  A.wait_limit_ns = wait_limit_ns();
+  A.hold = hold;
+  A.wait_limit_ns = limit_ns;
   cudaStream_t st = as_stream(stream);
   const bool e4m3 = p->dtype == PA_E4M3;
   if (q_dtype == PA_BF16) return e4m3 ? launch_g8<true, true>(A, p->device, st) : launch_g8<true, false>(A, p->device, st);
   return e4m3 ? launch_g8<false, true>(A, p->device, st) : launch_g8<false, false>(A, p->device, st);
+}
+
+extern "C" int pa_decode8(pa_pool8_t p, const void* q, int q_dtype, const int32_t* block_tables, int max_blocks_per_seq,
+                          const int32_t* seq_lens, int num_seqs, int n_q_heads, float scale, void* out, int out_dtype,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return decode8(p, q, q_dtype, block_tables, max_blocks_per_seq, seq_lens, num_seqs, n_q_heads, scale, out, out_dtype,
+                 workspace, workspace_bytes, stream, 0, wait_limit_ns());
+}
+
+extern "C" int pa_selftest_decode8_timeout(pa_pool8_t p, const void* q, int q_dtype, const int32_t* block_tables,
+                                           int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs, int n_q_heads,
+                                           float scale, void* out, int out_dtype, void* workspace, size_t workspace_bytes,
+                                           int cta, long long limit_ns, void* stream) {
+  if (limit_ns <= 0 || limit_ns > 1000000000ll || cta < -1 || cta > 0xffff) return PA_ERR_INVALID;
+  return decode8(p, q, q_dtype, block_tables, max_blocks_per_seq, seq_lens, num_seqs, n_q_heads, scale, out, out_dtype,
+                 workspace, workspace_bytes, stream, cta < 0 ? -1 : cta + 1, limit_ns);
 }

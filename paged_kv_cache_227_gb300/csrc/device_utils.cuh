@@ -43,6 +43,7 @@ __device__ __forceinline__ float fast_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+constexpr long long kDrainNs = 2000000000ll;  // limit of the last waits of a CTA that gives up
 // Bounded wait on an mbarrier phase.  Returns false if the CTA is aborting or
 // the wait ran out (then it records PA_ERR_TIMEOUT and raises the abort flag).
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort_flag,

@@ -87,7 +87,6 @@ constexpr int kSoftWarps = 16;
 constexpr int kTeam = 256;             // threads of a team: two a row
 constexpr int kPrefixThreads = (kSoftWarps + 2) * 32;  // + producer warp, + MMA warp
 constexpr int kMasks = 4;              // chunk masks in flight
-constexpr long long kDrainNs = 2000000000ll;  // limit of the last waits of a CTA that gives up
 // Estimates, in ns, to divide the SMs by: a chunk of the product on its SM, a
 // CTA's start and records; a tile of 16 tokens of the decode on one SM, and its
 // start.  Measured on 64 chats of 2,048 + about 280 tokens, 16 multi-head
