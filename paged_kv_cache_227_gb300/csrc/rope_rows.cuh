@@ -107,9 +107,10 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 
 // Cosines and sines of a row's angles, in shared memory; pair f = 8j + e, of lane
 // j, is element e % 4 of vector 8 (e / 4) + j, so that the lanes of a row read 128
-// bytes on end.  The angle is reduced to at most half a turn first, where the
-// hardware's sine and cosine are off by at most 2^-21: below what 16 bits (or 8)
-// keep, and a third of sincospif's instructions.
+// bytes on end.  They are those of turn_rows, to the last bit: 2^-24 off, where the
+// hardware's approximations would be 2^-21 (us with those and now: 8,192 tokens 36.2
+// and 36.4, 64 tokens 2.62 and 2.71; into 8 bits 7,900 tokens 42.8 and 43.8, 64 tokens
+// 5.6 and 5.7).
 struct Angles {
   float4 c[kMaxPairs / 4], s[kMaxPairs / 4], minus_s[kMaxPairs / 4];
 };
@@ -195,10 +196,10 @@ __device__ __forceinline__ void fill_angles(const RopeArgs& A, Angles* to, long 
     if (f >= pairs) continue;
     const uint32_t word = f < 32 ? (f < 16 ? A.axis[0] : A.axis[1]) : (f < 48 ? A.axis[2] : A.axis[3]);
     const int p = A.positions[((word >> (2 * (f & 15))) & 3) * A.n_tok + t0 + r];
-    const float a = 6.283185307f * turns(p, A.inv_freq[f]);
+    float sine, cosine;
+    sincospif(2.f * turns(p, A.inv_freq[f]), &sine, &cosine);
     const int at = 4 * (8 * (f >> 2 & 1) + (f >> 3)) + (f & 3);
-    const float sine = __sinf(a);
-    reinterpret_cast<float*>(to[r].c)[at] = __cosf(a);
+    reinterpret_cast<float*>(to[r].c)[at] = cosine;
     reinterpret_cast<float*>(to[r].s)[at] = sine;
     reinterpret_cast<float*>(to[r].minus_s)[at] = -sine;
   }
