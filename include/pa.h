@@ -167,7 +167,8 @@ int pa_rope_append(pa_pool_t pool, const void* q, int64_t q_stride, int n_q_head
  *                  pa_rope_append).
  *   eps          : finite, >= 0 (else INVALID).
  * Everything else as for pa_rope_append; value rows are not normed.  fp32
- * throughout, rounded once. */
+ * throughout, rounded once, for rows of every size and every eps (a row of zeros with
+ * eps 0 is NaN, as the formula has it). */
 int pa_norm_rope_append(pa_pool_t pool, const void* q, int64_t q_stride, int n_q_heads, const void* k_new,
                         int64_t k_stride, const void* v_new, int64_t v_stride, const void* q_weight,
                         const void* k_weight, float eps, const int32_t* positions, int n_axes,

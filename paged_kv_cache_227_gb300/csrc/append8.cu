@@ -56,19 +56,22 @@ __device__ __forceinline__ int leader_of(uint32_t cont, int r) { return 31 - __c
 // in this call, a slot of the same block and is none of the run's own.  One warp asks for all
 // four, before its rows are loaded (64 tokens 5.2 -> 5.4 us, 7,900 42.0 -> 42.4; behind
 // the loads 5.6 and 42.7; a claim a tile 5.5 and 43.6).
-__device__ __forceinline__ bool another_run(const RopeArgs& R, uint32_t claim, long long row, int behind, long long slot) {
-  const long long r = static_cast<long long>(claim) - 1;
-  if (r < 0 || r >= R.n_tok || (r >= row && r <= row + behind)) return false;
+__device__ __forceinline__ bool another_run(const RopeArgs& R, uint32_t claim, uint32_t row, int behind, int slot) {
+  const uint32_t r = claim - 1;
+  if (r >= static_cast<uint32_t>(R.n_tok) || r - row <= static_cast<uint32_t>(behind)) return false;
   return R.slots[r] >> 4 == slot >> 4;
 }
 
-template <bool kBf16, bool kE4M3>
+// kTogether: rows of a lane whose norms are made side by side, 2 where latency counts and
+// registers are free, 1 where warps are many (us with 1 and 2: 64 tokens 5.97 and 5.68,
+// 7,900 tokens 43.7 and 44.9).
+template <bool kBf16, bool kE4M3, bool kNorm, int kTogether>
 __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_angles) {
   __shared__ uint32_t s_top[2][kTasks8][kTok8], s_clash[2];
   const RopeArgs& R = A.R;
   const int lane = threadIdx.x & 31, mine8 = threadIdx.x >> 6, half = threadIdx.x >> 5 & 1;
   const int group = blockIdx.x % A.groups;
-  const long long base = static_cast<long long>(blockIdx.x / A.groups) * kTok8;
+  const uint32_t base = blockIdx.x / A.groups * kTok8;
   const int task = group * kTasks8 + mine8;  // K of each head, then V of each head
   const bool active = task < 2 * R.Hkv, is_v = task >= R.Hkv;
   const int h = is_v ? task - R.Hkv : task;
@@ -78,13 +81,14 @@ __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_ang
   const bool halves = turn && !R.interleaved;
   const int v0 = halves ? j : 2 * j, v1 = halves ? j + R.half_vecs : 2 * j + 1;
 
-  // slots of rows base - 1 .. base + 30, one a lane
-  const long long row = base - 1 + lane;
-  const long long slot = row >= 0 && row < R.n_tok ? R.slots[row] : -1;
-  const bool good = slot >= 0 && slot < R.num_slots;
-  if (slot >= R.num_slots && lane >= 1 && lane <= kTok8 && task == 0 && half == 0)
-    record_error(R.err, PA_ERR_DEVICE_CHECK, slot);
-  const long long before = __shfl_up_sync(0xffffffffu, slot, 1);
+  // slots of rows base - 1 .. base + 30, one a lane (a pool has fewer than 2^31)
+  const uint32_t row = base - 1 + lane, n_tok = static_cast<uint32_t>(R.n_tok);
+  const long long named = row < n_tok ? R.slots[row] : -1;
+  const bool good = named >= 0 && named < R.num_slots;
+  if (named >= R.num_slots && lane >= 1 && lane <= kTok8 && task == 0 && half == 0)
+    record_error(R.err, PA_ERR_DEVICE_CHECK, named);
+  const int slot = good ? static_cast<int>(named) : -1;
+  const int before = __shfl_up_sync(0xffffffffu, slot, 1);
   // bit i: row base + i is written; it goes on with the run of the row before it
   const uint32_t goodm = __ballot_sync(0xffffffffu, good) >> 1;
   const uint32_t contm =
@@ -93,7 +97,7 @@ __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_ang
 
   const uint16_t* from = is_v ? R.v : R.k;
   const long long stride = is_v ? R.v_stride : R.k_stride;
-  const uint16_t* weight = is_v || !active ? nullptr : R.k_weight;
+  const uint16_t* weight = !kNorm || is_v || !active ? nullptr : R.k_weight;
   bool angles = R.half_vecs && group * kTasks8 < R.Hkv;  // still to be computed
   const bool claims = threadIdx.x < 32;  // (the first task of a CTA is an active one)
   int pass = 0;
@@ -109,17 +113,17 @@ __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_ang
     const uint32_t part = (goodm >> f) & 0xffffu;
     // row f + l in lane l < 16: its tile, its place in the run and the tile's scale
     const int l = lane & 15;
-    const long long my_slot = __shfl_sync(0xffffffffu, slot, min(f + l + 1, 31));
+    const int my_slot = __shfl_sync(0xffffffffu, slot, min(f + l + 1, 31));
     const int first = leader_of(cont, l);
     const bool taken = active && ((part >> l) & 1) && ((lead >> first) & 1);
-    const long long tile = ((my_slot >> 4) * R.Hkv + h) * 2 + is_v;
-    const int off = static_cast<int>(my_slot & (kBlock - 1)), off0 = off - (l - first);
+    const int tile = ((my_slot >> 4) * R.Hkv + h) * 2 + is_v;
+    const int off = my_slot & (kBlock - 1), off0 = off - (l - first);
     const int was = taken ? A.exps[tile] : 0;
     const uint32_t next = (~cont & 0xffffu) >> 1 >> l;  // bit i: row l + 1 + i starts a run
     const int last = next ? l + __ffs(next) - 1 : kTok8 - 1;
     const bool heads_run = taken && l == first && lane < kTok8;
     const uint32_t claim =
-        claims && heads_run ? atomicExch(A.claims + (my_slot >> 4) * A.groups + group, static_cast<uint32_t>(base + f + l + 1)) : 0;
+        claims && heads_run ? atomicExch(A.claims + (my_slot >> 4) * A.groups + group, base + f + l + 1) : 0;
     // this lane's rows: 8 half + sub and 4 behind it
     bool mine[2];
     uint4 x[2][2];
@@ -129,43 +133,65 @@ __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_ang
       mine[p] = active && ((part >> r) & 1) && ((lead >> leader_of(cont, r)) & 1);
       x[p][0] = x[p][1] = make_uint4(0, 0, 0, 0);
       if (mine[p]) {
-        const uint4* src = reinterpret_cast<const uint4*>(from + (base + f + r) * stride + h * kHeadDim);
+        const uint4* src = reinterpret_cast<const uint4*>(from + static_cast<long long>(base + f + r) * stride + h * kHeadDim);
         x[p][0] = src[v0];
         x[p][1] = src[v1];
       }
     }
     if (angles) {  // of the window's rows and of the run that leaves it, once, with the first rows on their way
       const int end = kTok8 + __ffs(~(contm >> kTok8)) - 1;  // (bit 31 of contm is clear)
-      fill_angles<kThreads8>(R, s_angles, base, static_cast<int>(min(static_cast<long long>(end), R.n_tok - base)));
+      fill_angles<kThreads8>(R, s_angles, base, static_cast<int>(min(static_cast<uint32_t>(end), n_tok - base)));
       __syncthreads();
       angles = false;
     }
     RowPart y[2];
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int r = 8 * half + 4 * p + sub;
-      y[p].unpack<kBf16>(x[p][0], x[p][1]);
-      if (weight) {
-        const float rr = y[p].inverse_rms(R.eps);
-        RowPart w;
-        w.unpack<kBf16>(__ldg(reinterpret_cast<const uint4*>(weight) + v0), __ldg(reinterpret_cast<const uint4*>(weight) + v1));
-        y[p].times(w);
-        y[p].times(rr);
-      }
-      // (a row that is not taken has no angles)
-      if (turn && mine[p]) y[p].turn(R.interleaved, s_angles[f + r], j);
-      float m = 0.f;
+    for (int p0 = 0; p0 < 2; p0 += kTogether) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        m = max_abs(max_abs(m, y[p].a[k].x), y[p].a[k].y);
-        m = max_abs(max_abs(m, y[p].b[k].x), y[p].b[k].y);
+      for (int p = p0; p < p0 + kTogether; ++p) y[p].unpack<kBf16>(x[p][0], x[p][1]);
+      if (weight) {
+        const uint4* const at = reinterpret_cast<const uint4*>(weight);
+        uint4 w0, w1;
+        if (kTogether == 2) w0 = __ldg(at + v0), w1 = __ldg(at + v1);  // (early, where registers are free)
+        float mean[2];
+        bool any_far = false;
+#pragma unroll
+        for (int p = p0; p < p0 + kTogether; ++p) any_far |= RowPart::far(mean[p] = y[p].mean_square(R.eps));
+        if (any_far) {
+#pragma unroll
+          for (int p = p0; p < p0 + kTogether; ++p) {
+            const FarRow there = far_row(y[p], R.eps);
+            y[p] = there.y;
+            mean[p] = there.mean;
+          }
+        }
+        if (kTogether == 1) w0 = __ldg(at + v0), w1 = __ldg(at + v1);
+        RowPart w;
+        w.unpack<kBf16>(w0, w1);
+#pragma unroll
+        for (int p = p0; p < p0 + kTogether; ++p) {
+          y[p].times(rsqrtf(mean[p]));
+          y[p].times(w);
+        }
       }
-      // magnitudes compare as their bits, infinities and NaN above all others
-      uint32_t t = __float_as_uint(m) & 0x7fffffffu;
-      t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
-      t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
-      t = max(t, __shfl_xor_sync(0xffffffffu, t, 4));
-      if (j == 0) s_top[pass & 1][mine8][r] = mine[p] ? t : 0;
+#pragma unroll
+      for (int p = p0; p < p0 + kTogether; ++p) {
+        const int r = 8 * half + 4 * p + sub;
+        // (a row that is not taken has no angles)
+        if (turn && mine[p]) y[p].turn(R.interleaved, s_angles[f + r], j);
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          m = max_abs(max_abs(m, y[p].a[k].x), y[p].a[k].y);
+          m = max_abs(max_abs(m, y[p].b[k].x), y[p].b[k].y);
+        }
+        // magnitudes compare as their bits, infinities and NaN above all others
+        uint32_t t = __float_as_uint(m) & 0x7fffffffu;
+        t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
+        t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
+        t = max(t, __shfl_xor_sync(0xffffffffu, t, 4));
+        if (j == 0) s_top[pass & 1][mine8][r] = mine[p] ? t : 0;
+      }
     }
     if (claims) {
       const bool clash = heads_run && another_run(R, claim, base + f + l, last - l, my_slot);
@@ -191,11 +217,11 @@ __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_ang
     for (int p = 0; p < 2; ++p) {
       const int r = 8 * half + 4 * p + sub;
       const int er = __shfl_sync(0xffffffffu, e, r);
-      const long long tr = __shfl_sync(0xffffffffu, tile, r);
+      const int tr = __shfl_sync(0xffffffffu, tile, r);
       const int at = __shfl_sync(0xffffffffu, off, r);
       if (!mine[p] || (clashes >> leader_of(cont, r) & 1)) continue;
       y[p].times(inverse_scale(er));
-      uint8_t* dst = A.codes + tr * kTile8 + at * kRow8;
+      uint8_t* dst = A.codes + static_cast<long long>(tr) * kTile8 + at * kRow8;
       const float2 *a = y[p].a, *b = y[p].b;
       const uint2 c0 = make_uint2(pack_codes<kE4M3>(a[0].x, a[0].y, a[1].x, a[1].y),
                                   pack_codes<kE4M3>(a[2].x, a[2].y, a[3].x, a[3].y));
@@ -216,11 +242,11 @@ __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_ang
     while (grown) {
       const int r = __ffs(grown) - 1;
       grown &= grown - 1;
-      const long long tr = __shfl_sync(0xffffffffu, tile, r);
+      const int tr = __shfl_sync(0xffffffffu, tile, r);
       const int o0 = __shfl_sync(0xffffffffu, off0, r), o1 = o0 + __shfl_sync(0xffffffffu, last, r) - r;
       const int d = __shfl_sync(0xffffffffu, e - was, r);
       const float ratio = d > 126 ? 0.f : __int_as_float((127 - d) << 23);
-      uint4* tile_codes = reinterpret_cast<uint4*>(A.codes + tr * kTile8);
+      uint4* tile_codes = reinterpret_cast<uint4*>(A.codes + static_cast<long long>(tr) * kTile8);
       uint4 c[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {  // vector 32 (2 half + i) + lane: row 4 (2 half + i) + lane / 8
@@ -249,7 +275,7 @@ __global__ void __launch_bounds__(kThreads8, U > 1 ? 3 : 2) append8_kernel(const
   __shared__ __align__(16) uint8_t s_space[kQueries > kKeys ? kQueries : kKeys];
   Angles* const s_angles = reinterpret_cast<Angles*>(s_space);
   if (blockIdx.x < A.kv_ctas) {
-    write_window<kBf16, kE4M3>(A, s_angles);
+    write_window<kBf16, kE4M3, kNorm, U == 1 ? 2 : 1>(A, s_angles);
     return;
   }
   const int wib = threadIdx.x >> 5;

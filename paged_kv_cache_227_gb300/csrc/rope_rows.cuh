@@ -124,19 +124,43 @@ struct RowPart {
     a[0] = unpack2<kBf16>(x.x), a[1] = unpack2<kBf16>(x.y), a[2] = unpack2<kBf16>(x.z), a[3] = unpack2<kBf16>(x.w);
     b[0] = unpack2<kBf16>(y.x), b[1] = unpack2<kBf16>(y.y), b[2] = unpack2<kBf16>(y.z), b[3] = unpack2<kBf16>(y.w);
   }
-  // 1 / rms of the row; every lane of the warp takes part.  128 terms of one sign
-  // in chains of 8: off by at most 2^-20 of itself.
-  __device__ __forceinline__ float inverse_rms(float eps) const {
+  __device__ static __forceinline__ unsigned octet() { return 0xffu << (threadIdx.x & 24); }
+  // mean(x^2) + eps of the row, for the lanes of `who` (whole rows).  128 terms of one
+  // sign in chains of 8: off by at most 2^-19 of itself.
+  __device__ __forceinline__ float mean_square(float eps, unsigned who = 0xffffffffu) const {
     float2 s = mul2(a[0], a[0]);
 #pragma unroll
     for (int k = 1; k < 4; ++k) s = fma2(a[k], a[k], s);
 #pragma unroll
     for (int k = 0; k < 4; ++k) s = fma2(b[k], b[k], s);
     float t = s.x + s.y;
-    t += __shfl_xor_sync(0xffffffffu, t, 1);
-    t += __shfl_xor_sync(0xffffffffu, t, 2);
-    t += __shfl_xor_sync(0xffffffffu, t, 4);
-    return rsqrtf(fmaf(t, 1.f / kHeadDim, eps));
+    t += __shfl_xor_sync(who, t, 1);
+    t += __shfl_xor_sync(who, t, 2);
+    t += __shfl_xor_sync(who, t, 4);
+    return fmaf(t, 1.f / kHeadDim, eps);
+  }
+  // Where the mean leaves the range in which squares count in full (those below 2^-149
+  // are lost: together less than 2^-42 of 2^-100), and its root and the row's products
+  // stay in theirs.  Bits of a sum that is not negative compare as numbers.
+  __device__ static __forceinline__ bool far(float mean) {
+    return __float_as_uint(mean) - 0x0d800000u >= 0x7f800000u - 0x0d800000u;  // not in [2^-100, infinity)
+  }
+  // Multiplies the row by the power of two that takes the larger one of its largest
+  // magnitude and sqrt(eps) to about 1 (none if it is not finite), which leaves
+  // x / sqrt(mean(x^2) + eps) as it is with what is returned for eps.
+  __device__ __forceinline__ float to_unit_size(float eps) {
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      m = fmaxf(fmaxf(m, fabsf(a[k].x)), fabsf(a[k].y));
+      m = fmaxf(fmaxf(m, fabsf(b[k].x)), fabsf(b[k].y));
+    }
+    const int e = static_cast<int>(__reduce_max_sync(octet(), __float_as_uint(m)) >> 23);  // exponents of both, biased
+    int up = 127 - e;
+    if (eps > 0.f) up = min(up, (127 - static_cast<int>(__float_as_uint(eps) >> 23)) >> 1);
+    const float r = e == 255 ? 1.f : __int_as_float((127 + max(up, -126)) << 23);
+    times(r);
+    return eps * r * r;
   }
   __device__ __forceinline__ void times(const RowPart& w) {
 #pragma unroll
@@ -180,6 +204,17 @@ struct RowPart {
     }
   }
 };
+// A row whose mean is far, and its mean, as to_unit_size leaves them; not inlined, which
+// costs the latency of a decode step less (2.76 -> 2.70 us).
+struct FarRow {
+  RowPart y;
+  float mean;
+};
+static __device__ __noinline__ FarRow far_row(RowPart y, float eps) {
+  eps = y.to_unit_size(eps);
+  const float mean = y.mean_square(eps, RowPart::octet());
+  return {y, mean};
+}
 template <bool kBf16>
 __device__ __forceinline__ uint4 pack_part(const float2 (&x)[4]) {
   return make_uint4(pack2<kBf16>(x[0].x, x[0].y), pack2<kBf16>(x[1].x, x[1].y), pack2<kBf16>(x[2].x, x[2].y),
@@ -296,8 +331,8 @@ __device__ __forceinline__ void turn_rows(const RopeArgs& A, long long w, float2
   }
 }
 
-// turn_rows with norms.  The weight comes before the rotation (it belongs to a dim),
-// 1 / rms, one number a row, behind it.  Four rows (a quad) go together; quads of query
+// turn_rows with norms.  1 / rms comes first: the product with it is in the range of 32
+// bits for rows of every size.  Four rows (a quad) go together; quads of query
 // rows alone, nearly all of them, take a path whose branches are the warp's, not the
 // rows' (the others spend a third of their instructions on those).
 // What bounds it is the bytes that a resident warp has on their way (its rows) times
@@ -375,12 +410,13 @@ __device__ __forceinline__ void norm_rows(const RopeArgs& A, unsigned w, Angles*
     if (weight) {
       RowPart wt;
       wt.unpack<kBf16>(__ldg(weight + v0), __ldg(weight + v1));
+      y.times(rr);
       y.times(wt);
     }
     if (turn) y.turn(A.interleaved, *s_angles, j);
-    if (weight) y.times(rr);
   };
   uint4* const q_out = reinterpret_cast<uint4*>(A.q_out + t * A.q_out_stride) + (r0 + sub) * (kHeadDim / 8);
+  bool far = false;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (r0 + 4 * u + 4 > A.Hq) break;
@@ -388,38 +424,67 @@ __device__ __forceinline__ void norm_rows(const RopeArgs& A, unsigned w, Angles*
     row(u, x);
     RowPart y;
     y.unpack<kBf16>(x[0], x[1]);
-    const float rr = y.inverse_rms(A.eps);
-    norm_and_turn(y, reinterpret_cast<const uint4*>(A.q_weight), rr);
+    const float mean = y.mean_square(A.eps);
+    far |= RowPart::far(mean);
+    norm_and_turn(y, reinterpret_cast<const uint4*>(A.q_weight), rsqrtf(mean));
     q_out[4 * u * (kHeadDim / 8) + v0] = pack_part<kBf16>(y.a);
     q_out[4 * u * (kHeadDim / 8) + v1] = pack_part<kBf16>(y.b);
   }
-  if (r0 + 4 * U <= A.Hq) return;
   // quads that hold K or V rows
-  const long long slot = A.slots[t];
-  const bool to_cache = slot >= 0 && slot < A.num_slots;
-  if (slot >= A.num_slots && lane == 0 && r0 < kv) record_error(A.err, PA_ERR_DEVICE_CHECK, slot);
-  const long long at = (slot >> 4) * A.Hkv * kBlock + (slot & 15);  // row of kv head 0
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int r = r0 + 4 * u + sub;
-    if (r0 + 4 * u + 4 <= A.Hq) continue;
-    if (r0 + 4 * u >= A.rows) break;
-    uint4 x[2];
-    row(u, x);
+  long long at = 0;  // row of kv head 0
+  bool to_cache = false;
+  // row r, given as x, to its place; `again`: as to_unit_size leaves it, if it is far
+  auto any_row = [&](int r, uint4 (&x)[2], bool again) {
     RowPart y;
     y.unpack<kBf16>(x[0], x[1]);
-    const float rr = y.inverse_rms(A.eps);
-    if (r >= A.rows || (r >= A.Hq && !to_cache)) continue;
+    const uint16_t* const weight = r < A.Hq ? A.q_weight : (r < kv ? A.k_weight : nullptr);
+    float mean = y.mean_square(A.eps);
+    if (again) {
+      if (!weight || !RowPart::far(mean)) return;
+      if (U > 1) {
+        mean = y.mean_square(y.to_unit_size(A.eps), RowPart::octet());
+      } else {
+        const FarRow there = far_row(y, A.eps);
+        y = there.y;
+        mean = there.mean;
+      }
+    } else {
+      far |= weight && RowPart::far(mean);
+    }
+    if (r >= A.rows || (r >= A.Hq && !to_cache)) return;
     uint4* dst = reinterpret_cast<uint4*>(
         r < A.Hq ? A.q_out + t * A.q_out_stride + r * kHeadDim
                  : (r < kv ? A.k_pool + (at + (r - A.Hq) * kBlock) * kHeadDim : A.v_pool + (at + (r - kv) * kBlock) * kHeadDim));
     if (r < kv) {
-      norm_and_turn(y, reinterpret_cast<const uint4*>(r < A.Hq ? A.q_weight : A.k_weight), rr);
+      norm_and_turn(y, reinterpret_cast<const uint4*>(weight), rsqrtf(mean));
       x[0] = pack_part<kBf16>(y.a);
       x[1] = pack_part<kBf16>(y.b);
     }
     dst[v0] = x[0];
     dst[v1] = x[1];
+  };
+  if (r0 + 4 * U > A.Hq) {
+    const long long slot = A.slots[t];
+    to_cache = slot >= 0 && slot < A.num_slots;
+    if (slot >= A.num_slots && lane == 0 && r0 < kv) record_error(A.err, PA_ERR_DEVICE_CHECK, slot);
+    at = (slot >> 4) * A.Hkv * kBlock + (slot & 15);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (r0 + 4 * u + 4 <= A.Hq) continue;
+      if (r0 + 4 * u >= A.rows) break;
+      uint4 x[2];
+      row(u, x);
+      any_row(r0 + 4 * u + sub, x, false);
+    }
+  }
+  // rows whose squares left 32 bits, once more, apart from the loops above, whose registers
+  // they would take (36.5 -> 39.3 us there); they are still here, also where q_out is q
+  if (!__any_sync(0xffffffffu, far)) return;
+#pragma unroll 1
+  for (int u = 0; u < U && r0 + 4 * u < A.rows; ++u) {
+    uint4 x[2] = {only[0], only[1]};
+    if (U > 1) x[0] = shared16(mine + 1024 * u), x[1] = shared16(mine + 1024 * u + 512);
+    any_row(r0 + 4 * u + sub, x, true);
   }
 }
 
