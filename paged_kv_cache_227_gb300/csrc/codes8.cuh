@@ -36,9 +36,9 @@ __device__ __forceinline__ int exponent_for(uint32_t amax_bits) {
   return x < 1 ? 1 : x;
 }
 
-// 2^(127 - e), exact for what exponent_for gives; 0 for NaN (no code stands for it).
+// 2^(127 - e), exact; 0 for NaN (no code stands for it).
 __device__ __forceinline__ float inverse_scale(int e) {
-  return e == kNanExponent ? 0.f : __int_as_float((254 - e) << 23);
+  return e >= 254 ? (e == 254 ? __int_as_float(0x00400000) : 0.f) : __int_as_float((254 - e) << 23);
 }
 __device__ __forceinline__ float scale_of(int e) {
   return e == 0 ? __int_as_float(0x00400000) : __int_as_float(e == kNanExponent ? 0x7fffffff : e << 23);
