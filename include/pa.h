@@ -73,7 +73,7 @@ enum {
   PA_ERR_SCRATCH_LIMIT = -7 /* needs more than the library's static scratch   */
 };
 
-enum { PA_BLOCK_SIZE = 16, PA_HEAD_DIM = 128, PA_MAX_GROUP = 8 };
+enum { PA_BLOCK_SIZE = 16, PA_HEAD_DIM = 128, PA_MAX_GROUP = 8, PA_MAX_KV_HEADS = (1 << 19) - 1 };
 
 typedef struct pa_pool* pa_pool_t;
 
@@ -94,7 +94,8 @@ size_t pa_pool_bytes(int num_blocks, int block_size, int n_kv_heads, int d_head,
 /* Allocates K and V pools (cudaMalloc on the current device, zero-filled) and
  * the device error word.  dtype is PA_FP16 or PA_BF16.  *out receives the
  * handle.  Errors: INVALID (num_blocks <= 0, n_kv_heads <= 0, out null),
- * UNSUPPORTED (block_size != 16, d_head != 128, dtype not 16-bit, or
+ * UNSUPPORTED (block_size != 16, d_head != 128, dtype not 16-bit, n_kv_heads >
+ * PA_MAX_KV_HEADS (a block of an array has fewer than 2^31 bytes), or
  * num_blocks * n_kv_heads * 16 >= 2^31 token rows: a 512 GiB array), OOM. */
 int pa_pool_create(int num_blocks, int block_size, int n_kv_heads, int d_head,
                    int dtype, pa_pool_t* out);

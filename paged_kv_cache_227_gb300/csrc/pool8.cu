@@ -196,6 +196,8 @@ int pa_pool8_create(int num_blocks, int block_size, int n_kv_heads, int d_head, 
   if (!out || num_blocks <= 0 || n_kv_heads <= 0) return PA_ERR_INVALID;
   if (block_size != kBlock || d_head != kHeadDim) return PA_ERR_UNSUPPORTED;
   if (dtype != PA_E4M3 && dtype != PA_INT8) return PA_ERR_UNSUPPORTED;
+  // (offsets inside a block are 32-bit ints)
+  if (n_kv_heads > PA_MAX_KV_HEADS) return PA_ERR_UNSUPPORTED;
   if (static_cast<long long>(num_blocks) * n_kv_heads * kBlock > 0x7fffffffll) return PA_ERR_UNSUPPORTED;
   *out = nullptr;
   pa_pool8* p = new (std::nothrow) pa_pool8();

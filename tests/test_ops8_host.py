@@ -130,3 +130,11 @@ def test_write_of_the_definition_grows_and_restarts():
     assert exps[0, 0] == need8(1.0, "int8") and codes[0, 0, :3, 0].tolist() == [64, 1, 75], "started afresh"
     codes, exps = write8(codes, exps, row(np.nan), [1], "int8")
     assert exps[0, 0] == 255
+
+
+def test_pools_whose_blocks_pass_32_bits_are_refused():
+    """Offsets inside a block are 32-bit: 2^19 heads are a block of 2^31 bytes."""
+    h = ctypes.c_void_p()
+    for create, dtype in ((pa.lib.pa_pool_create, pa.PA_BF16), (pa.lib.pa_pool8_create, pa.PA_INT8)):
+        for heads in (1 << 19, (1 << 24) + 3, (1 << 27) - 1):
+            assert create(1, 16, heads, 128, dtype, ctypes.byref(h)) == pa.PA_ERR_UNSUPPORTED
