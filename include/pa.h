@@ -412,11 +412,14 @@ int pa_evict(pa_pool_t pool, const float* weights, float* weights_out, const int
  * V, of each (block, kv head) on end), PA_E4M3 or PA_INT8, and an exponent
  * byte [num_blocks][n_kv_heads][2] for each such tile: a code c stands for
  *   c * 2^(exponent - 127), for NaN where the exponent is 255.
- * Scales are powers of two, so scaling is exact and a value is rounded once.  The
- * calls below that write a tile give it the smallest exponent >= 1 whose largest
- * code (448, 127) holds the tile's largest magnitude: e4m3 is then off by at most
- * 2^-4 of a value (or 2^-10 of the scale), int8 by half a scale, at most 2^-7 of
- * the tile's largest magnitude.  A row with an infinity or a NaN makes the
+ * Scales are powers of two, so scaling is exact.  The calls below give a tile that they
+ * write afresh the smallest exponent >= 1 whose largest code (448, 127) holds its largest
+ * magnitude, and round a value once: e4m3 is off by at most 2^-4 of the value or
+ * 2^-10 of the scale, int8 by half a scale, at most 1/127 of the tile's largest
+ * magnitude.  A write into a block that is started only ever raises its exponent (one
+ * that rows since dropped have left stays), and rounds the block's other codes to it:
+ * all roundings of a value together are below 2^-4 of it + 2^-9 of the scale (e4m3),
+ * below one scale (int8).  A row with an infinity or a NaN makes the
  * tile's exponent 255.  The other calls of this library take 16-bit pools only.
  * ------------------------------------------------------------------------- */
 typedef struct pa_pool8* pa_pool8_t;

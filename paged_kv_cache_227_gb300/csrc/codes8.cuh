@@ -2,9 +2,10 @@
 //
 // A tile is the 16 x 128 codes of one (block, kv head, K or V), e4m3 or int8,
 // with one exponent byte e: a code c stands for c * 2^(e - 127), 255 for NaN
-// (the e8m0 format).  Powers of two make every scaling exact, so a value is
-// rounded once, and a scale that grows moves e4m3 codes without rounding them
-// again (but for their subnormals).  For int8 an exact amax / 127 would gain
+// (the e8m0 format).  Powers of two make every scaling exact, so a value that is
+// written is rounded once, and a scale that grows moves e4m3 codes without rounding
+// them again (but for their subnormals; int8 codes are: below one step of the last
+// scale in all).  For int8 an exact amax / 127 would gain
 // half a bit on average at the first write; a growing scale would then round
 // the block's earlier rows again at every new maximum (about three times in a
 // block written token by token) instead of only when the maximum doubles.
