@@ -58,10 +58,16 @@ constexpr int kMinUnits8 = 8;  // smallest range of a CTA (8, 16, 24: four short
 // Widest tables of the plan with a CTA a segment, which needs no second kernel but
 // waits for its longest segment: for few segments, and for at least kManyWhole8 (the
 // balanced split then leaves records in every CTA).  us a call with it and with the
-// balanced split: 8 segments of 300, 500, 800 tokens 6.7, 7.6, 9.2 and 7.4, 7.8, 8.6;
-// 72 of 500, 1,100, 1,500 tokens 8.1, 10.6, 12.4 and 10.2, 11.8, 12.8; 128 of 1,500
-// tokens 14.8 and 18.0.
-constexpr int kFewBlocks8 = 32, kManyBlocks8 = 96, kManyWhole8 = 64;
+// balanced split, lengths alike: 8 segments of 300, 500, 800 tokens 7.3, 8.2, 10.1 and 8.1,
+// 8.2, 8.3; 32 of them 7.8, 8.8, 10.6 and 8.5, 8.7, 9.8; 63 of 300, 800, 1,500 8.3, 11.2,
+// 14.6 and 10.4, 11.8, 14.7; 72 of 500, 800, 1,500, 2,500 9.0, 10.9, 14.5, 20.3 and 10.6,
+// 12.0, 14.7, 17.6; 128 of 500, 1,500, 4,000 9.8, 15.8, 28.3 and 12.9, 18.3, 29.0.
+// Ragged (the longest one in brackets): 32 (376), (753) 8.0, 10.3 and 8.4, 8.7; 72 (537),
+// (1,073), (1,530) 9.0, 12.0, 14.7 and 8.9, 10.1, 11.1; 128 (666), (1,331), (1,530) 9.8,
+// 13.7, 14.9 and 10.5, 11.5, 13.0.  Batches are ragged, so the limit of many is theirs.
+// It is the table's width that a launch knows: a table far wider than its sequences
+// gets the balanced split.
+constexpr int kFewBlocks8 = 32, kManyBlocks8 = 48, kManyWhole8 = 64;
 constexpr float kLog2e8 = 1.4426950408889634f;
 // The running maximum moves when a score passes it by 2^4; weights are carried
 // at 2^11 times their size, below 2^15, so that the low half's smallest step
