@@ -128,12 +128,16 @@ static int rope_append(pa_pool_t p, const void* q, int64_t q_stride, int n_q_hea
   const bool few = quads <= 32ll * sm_count(p->device), bf16 = p->dtype == PA_BF16;
   const bool norm = q_weight || k_weight;
   cudaStream_t st = as_stream(stream);
-  // with norms: 4 rows a warp, or 16 that wait in shared memory; those pay only for
-  // tokens of many rows.  us with 4 and with 16, captured calls: 48 rows a token
-  // (the switch is at 405 tokens) 200 tokens 2.96 and 3.84, 400 4.25 and 4.15, 800
-  // 6.30 and 5.06, 4,000 27.1 and 21.5; 16 rows a token 1,531 tokens 4.73 and 5.92,
-  // 6,000 15.1 and 16.5
-  const bool few_norm = few || A.rows < 32;
+  // with norms: 4 rows a warp, or 16 that wait in shared memory, from the same number of
+  // rows on for tokens of many rows, from twice as many for small ones.  us with 4 and with
+  // 16, captured calls: 48 rows a token (the switch is at 405 tokens) 200 tokens 3.1 and
+  // 3.7, 400 4.6 and 4.0, 1,531 13.1 and 11.0, 6,000 41 and 28; 40 rows (486) 200 3.1 and
+  // 3.5, 400 3.7 and 3.8, 800 6.0 and 4.6, 6,000 35 and 24; 28 rows (1,389) 400 3.2 and 3.9,
+  // 1,531 7.6 and 5.6; 20 rows (1,945) 800 4.0 and 4.0, 3,000 10.4 and 8.0; 16 rows (2,432)
+  // in halves 800 3.4 and 4.3, 1,531 5.1 and 4.6, 3,000 8.5 and 6.0, 6,000 17.8 and 13.8,
+  // adjacent pairs 1,531 4.7 and 5.5, 3,000 7.6 and 7.5, 6,000 16.6 and 15.8; 7 rows (4,864)
+  // 1,531 3.6 and 4.0, 6,000 8.7 and 7.9
+  const bool few_norm = quads <= (A.rows < 32 ? 64ll : 32ll) * sm_count(p->device);
   if (norm) return few_norm ? launch_rope<1, true>(A, bf16, st) : launch_rope<4, true>(A, bf16, st);
   return few ? launch_rope<1, false>(A, bf16, st) : launch_rope<3, false>(A, bf16, st);
 }

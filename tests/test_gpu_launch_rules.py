@@ -1,10 +1,12 @@
-"""Both sides of the launch rules of the 8-bit decode: the rule chooses the plan, not the result."""
+"""Both sides of the launch rules of the 8-bit decode and of the norms: a rule chooses the kernel, not the result."""
 import numpy as np
 import pytest
+import torch
 
-from ._ops import BS
+from ._ops import BS, D, ok, to64
 from ._ops8 import ok8
 from .test_gpu_decode8 import Case
+from .test_gpu_norm_rope import EPS, Tokens, check, weight
 
 pytestmark = pytest.mark.gpu
 
@@ -25,3 +27,24 @@ def test_tables_at_the_limit_of_many_segments(pa, Hq, Hkv, B, width):
         c = Case(pa, lens.tolist(), Hq, Hkv, "int8" if alike else "e4m3", seed=B, width=width)
         c.check(c.call())
         ok8(pa, c.pool)
+
+
+@pytest.mark.parametrize("Hq,Hkv,dtype,rot,interleaved,n", [
+    (12, 2, torch.float16, 64, True, 2432), (12, 2, torch.float16, 64, True, 2433), (5, 1, torch.bfloat16, 96, False, 4864),
+    (5, 1, torch.bfloat16, 96, False, 4865), (20, 4, torch.bfloat16, 128, False, 1389), (20, 4, torch.bfloat16, 128, False, 1390),
+    (32, 4, torch.float16, 128, True, 486), (32, 4, torch.float16, 128, True, 487)])
+def test_norms_at_the_switch_to_rows_that_wait(pa, Hq, Hkv, dtype, rot, interleaved, n):
+    rng = np.random.default_rng(n)
+    nb = -(-n // BS)
+    pool = pa.Pool(nb, Hkv, dtype)
+    t = Tokens(rng, n, Hq, Hkv, dtype, rot, 2, interleaved, fused=True)
+    wq, wk = weight(rng, dtype), weight(rng, dtype)
+    slots = rng.permutation(nb * BS)[:n].astype(np.int64)
+    pa.pa_norm_rope_append(pool, *t.args(wq, wk, slots), eps=EPS, interleaved=interleaved)
+    ok(pa, pool)
+    ref, normed = t.want(t.q, wq)
+    check(to64(t.q_out), ref, normed, dtype, rot, interleaved)
+    rows = to64(pool.k).transpose(0, 2, 1, 3).reshape(-1, Hkv, D)
+    ref, normed = t.want(t.k, wk)
+    check(rows[slots], ref, normed, dtype, rot, interleaved)
+    pool.close()
