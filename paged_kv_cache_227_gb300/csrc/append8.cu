@@ -16,9 +16,10 @@
 // has 16 rows of four (kv head, K|V), whose angles are computed once.  Query rows
 // go as in the 16-bit appends, in the same launch, with the same bits.
 //
-// Measured: 7,900 tokens of 32 / 8 / 8 heads in 24 chunks (183 MB) 42.5 us, 0.63 of
-// the copy rate; one token of 64 sequences 5.4 us: three memory latencies (slots,
-// rows and scales, codes) and the reduction between them.
+// Measured: 7,900 tokens of 32 / 8 / 8 heads in 24 chunks (183 MB) 45 us, 0.60 of the
+// copy rate (K and V rows as they are, without query rows, 20); one token of 64 sequences
+// 5.7 us: three memory latencies (slots, rows and scales, codes) and the reduction
+// between them.  int8 codes: 1 us more for the chunks, 0.4 for a token.
 #include "codes8.cuh"
 #include "device_utils.cuh"
 #include "rope_rows.cuh"
@@ -316,10 +317,18 @@ static int launch8(pa_pool8_t p, Append8Args& A, bool bf16, void* stream) {
   const bool e4m3 = p->dtype == PA_E4M3;
   cudaStream_t st = as_stream(stream);
   const long long quads = A.R.n_tok * ((A.R.rows + 3) / 4);
-  // query rows a warp with norms, 4 or 16.  us, captured calls: 32 query heads, 480
-  // tokens (the switch is at 760) 6.6 and 7.3, 960 9.6 and 8.4, 3,840 39.0 and
-  // 24.0; 12 heads (2,027) 1,920 tokens 6.9 and 7.9, 4,000 13.0 and 11.5
-  const bool few = quads <= 40ll * sm_count(p->device);
+  const long long windows = (A.R.n_tok + kTok8 - 1) / kTok8 * claim_groups(A.R.Hkv);
+  // few query rows a warp and 2 CTAs an SM, or 12 (with norms 16) and 3: by the row quads of
+  // queries, and by the K and V rows' CTAs, which a call has without query rows too.  us
+  // with the one and the other, captured calls, norms: 32 / 8 heads (the switch is at 304
+  // tokens) 256 tokens 4.3 and 4.4, 480 5.8 and 5.2, 1,920 20.0 and 13.9; 12 / 2 (810) 480
+  // tokens 3.9 and 4.1, 960 4.7 and 4.8, 1,920 7.0 and 5.7; 8 / 8 (1,216) 960 5.3 and 5.7,
+  // 1,920 9.0 and 8.0; without norms 32 / 8 256 tokens 4.1 and 4.0, 480 5.3 and 4.1; 12 / 2
+  // 480 3.6 and 3.6, 1,920 6.5 and 4.6.  K and V rows alone: 8 heads (3,040) 1,920 tokens
+  // 5.6 and 5.7, 3,840 9.8 and 9.0, 7,680 22.5 and 18.5; 40 heads (608) 480 5.9 and 6.1,
+  // 960 11.8 and 10.3, 7,680 95 and 74
+  const long long sms = sm_count(p->device);
+  const bool few = quads <= 16 * sms && windows <= 5 * sms;
   if (A.R.q_weight || A.R.k_weight)
     return few ? launch_append8<1, true>(A, bf16, e4m3, st) : launch_append8<4, true>(A, bf16, e4m3, st);
   return few ? launch_append8<1, false>(A, bf16, e4m3, st) : launch_append8<3, false>(A, bf16, e4m3, st);

@@ -1,10 +1,11 @@
-"""Both sides of the launch rules of the 8-bit decode and of the norms: a rule chooses the kernel, not the result."""
+"""Both sides of the launch rules of the 8-bit decode, the 8-bit write and the norms: a rule chooses the kernel, not the result."""
 import numpy as np
 import pytest
 import torch
 
 from ._ops import BS, D, ok, to64
-from ._ops8 import ok8
+from ._ops8 import KINDS, ok8, raw, write8
+from .test_gpu_append8 import write_and_compare
 from .test_gpu_decode8 import Case
 from .test_gpu_norm_rope import EPS, Tokens, check, weight
 
@@ -48,3 +49,35 @@ def test_norms_at_the_switch_to_rows_that_wait(pa, Hq, Hkv, dtype, rot, interlea
     ref, normed = t.want(t.k, wk)
     check(rows[slots], ref, normed, dtype, rot, interleaved)
     pool.close()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("hkv,n", [(8, 3040), (8, 3041), (5, 4048), (5, 4065)])
+def test_prompts_into_8_bits_at_the_switch_by_k_and_v_rows(pa, kind, hkv, n):
+    """760 CTAs and 764, 759 and 765: one prompt that starts inside a block."""
+    rng = np.random.default_rng(n)
+    nb = n // BS + 2
+    table = rng.permutation(nb)
+    p = 5 + np.arange(n)
+    ok8(pa, write_and_compare(pa, kind, torch.bfloat16, hkv, table[p // BS] * BS + p % BS, nb, n))
+
+
+@pytest.mark.parametrize("Hq,Hkv,n,norms", [(32, 8, 304, True), (32, 8, 305, True), (12, 2, 810, False), (12, 2, 811, False),
+                                            (7, 7, 1216, True), (7, 7, 1217, False)])
+def test_prompts_into_8_bits_at_the_switch_by_query_rows(pa, Hq, Hkv, n, norms):
+    """Query rows are the 16-bit append's, bit for bit, on both sides; V codes the definition's."""
+    rng = np.random.default_rng(n)
+    nb = n // BS + 2
+    t = Tokens(rng, n, Hq, Hkv, torch.bfloat16, 128, 1, False, fused=True)
+    w = weight(rng, torch.bfloat16) if norms else None
+    slots = 3 + np.arange(n)
+    p8, p16 = pa.Pool8(nb, Hkv, torch.int8), pa.Pool(nb, Hkv, torch.bfloat16)
+    _, v, _, ev = raw(p8)
+    pa.pa_norm_rope_append8(p8, *t.args(w, w, slots))
+    ok8(pa, p8)
+    first = t.q_out.clone()
+    pa.pa_norm_rope_append(p16, *t.args(w, w, slots))
+    assert torch.equal(first, t.q_out)
+    v, ev = write8(v, ev, to64(t.v), slots, "int8")
+    got = raw(p8)
+    assert np.array_equal(got[1], v) and np.array_equal(got[3], ev)
