@@ -15,11 +15,12 @@
 // one CTA to the next, and a second kernel joins those, by log-sum-exp, always in
 // the order of their tiles.  Few or short segments get a CTA each instead.
 //
-// Measured (captured calls, three inputs in turn): batch 64 of chats (108 MB) 26.4 us,
-// 0.61 of the copy rate (a call alone from a cold L2, with its launch, 35 us): 3 us
-// are lengths, tables and first tiles, 17 the stream, 6 the joins and what the SMs'
-// ends lie apart; 16 multi-head sequences (276 MB) 49 us, 0.83; four documents of 8 to
-// 32 thousand tokens (161 MB) 33 us, 0.72; four short requests 7.7-8.1 us.
+// Measured (captured calls, three inputs in turn; behind a flush of L2): batch 64 of
+// chats (108 MB) 26.8 us, 0.60 of the copy rate (29.2); 16 multi-head sequences (276 MB)
+// 49.2, 0.83 (51.3); four documents of 8 to 32 thousand tokens (161 MB) 33.2, 0.72 (35);
+// four short requests 8.2 (10.3).  Groups of 8 query heads, 64 chats (109 MB) 28.8, 0.56
+// (31.7).  Of the 64 chats' 26.8 us 3 are lengths, tables and first tiles, 16 the stream, 5
+// what the SMs' ends lie apart and the joins inside them, 3 the second kernel.
 //
 // A tile is one TMA box, 32 rows of 128 bytes in the 128-byte swizzle, so that the
 // operand loads below meet no bank conflict.  Per tile, with mma.sync m16n8k16 (16
@@ -47,14 +48,16 @@
 namespace pa {
 
 // One CTA an SM, 12 warps with 3 tiles (4 KiB) in flight each.  us for 64 chats, 16
-// multi-head sequences and four documents: 29.2, 52.2, 35.1; 10 warps of 4 tiles 30.5,
-// 56.4, 37.9; 8 of 5 31.9, 57.9, 39.5; 11 of 3 30.0, 52.6, 35.9; 13 of 3 (fewer
-// registers, spills) 31.9, 55.2, 38.0.
+// multi-head sequences and four documents: 26.7, 49.5, 33.1; 10 warps of 4 tiles 29.1,
+// 55.7, 36.4; 8 of 5 29.6, 56.5, 37.9; 11 of 3 27.7, 51.5, 34.4; 13 of 3 (fewer
+// registers, spills) 28.1, 52.9, 35.6.
 constexpr int kWarps8 = 12;
 constexpr int kStages8 = 3;
 static_assert(2 * kWarps8 <= 32, "a lane a chain of pieces");
 constexpr int kSeqs8 = 4096;   // sequences of a call (their prefix lives in shared memory)
-constexpr int kMinUnits8 = 8;  // smallest range of a CTA (8, 16, 24: four short requests, 7.7, 8.5, 9.1 us)
+// Smallest range of a CTA.  us with 4, 8, 16, 24: 16 segments of 100 tokens 7.6, 7.0, 7.5,
+// 8.3; 16 of about 400 10.6, 10.0, 9.7, 10.4; 80 of about 300 10.9, 10.9, 10.0, 10.6.
+constexpr int kMinUnits8 = 8;
 // Widest tables of the plan with a CTA a segment, which needs no second kernel but
 // waits for its longest segment: for few segments, and for at least kManyWhole8 (the
 // balanced split then leaves records in every CTA).  us a call with it and with the
@@ -197,10 +200,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The K and V tile number `tile` of the pool into shared memory.  Tiles are read once,
-// so they leave L2 first and push out neither records nor tables nor what the
-// caller's next kernels read (captured calls over three inputs in turn: 29.2 -> 26.6
-// us for 64 chats; from a cold L2 the same time with and without).
+// The K and V tile number `tile` of the pool into shared memory.  A tile is read once
+// for each sequence that holds it, nearly always one, so tiles leave L2 first and push out
+// neither records nor tables nor what other kernels read.  With the hint and without, us:
+// three inputs in turn, 64 chats 26.9 and 29.2, multi-head 50.0 and 52.4, documents 33.1
+// and 35.1; behind a flush 29.2 and 29.3, 51.1 and 51.3, 35.0 and 35.1.  Forks over one
+// prefix: 256 behind 1,024 tokens in turn 91.6 and 91.8, behind a flush 93.6 and 92.6; 64
+// behind 2,048 51.0 and 51.1, 52.5 and 52.1; 16 behind 8,192 49.0 and 49.2, 51.2 and 50.1.
 __device__ __forceinline__ void load_tile8(uint32_t to, const CUtensorMap* map, int tile, uint32_t bar) {
   const int z = 0;
   uint64_t policy;
@@ -372,7 +378,9 @@ __global__ void __launch_bounds__(kWarps8 * 32, 1) decode8_kernel(const __grid_c
   if (threadIdx.x == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&A.tmap)) : "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // the tables and the exponents on their way into L2 while the lengths are read
+  // the tables and the exponents on their way into L2 while the lengths are read: of small
+  // pools all (a line a thread; of a pool 10 or 50 times the batch's 7.5 MB that it
+  // partly does not need: 64 chats 26.9 us, then 27.5)
   {
     const long long at = 128ll * (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x);
     if (at < 4ll * A.B * A.max_blocks) prefetch_l2(reinterpret_cast<const uint8_t*>(A.tables) + at);

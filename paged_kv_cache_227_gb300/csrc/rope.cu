@@ -16,7 +16,7 @@
 // computed by the lanes of a warp together (two each) and shared by all of
 // the warp's rows through shared memory.  Measured: 8,192 tokens of 48 heads
 // (201 MB) 32.8 us, 6.1 TB/s, 0.90 of this GPU's copy rate; 64 tokens 2.3 us.
-// With norms 36.4 us, 0.82 of the copy rate, and 2.7 us: half of the issue slots go
+// With norms 35.9 us, 0.83 of the copy rate, and 2.7 us: half of the issue slots go
 // to the norms' arithmetic, and its registers leave room for fewer warps.
 #include "device_utils.cuh"
 #include "rope_rows.cuh"
