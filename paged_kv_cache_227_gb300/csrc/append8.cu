@@ -161,6 +161,7 @@ __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_ang
         if (any_far) {
 #pragma unroll
           for (int p = p0; p < p0 + kTogether; ++p) {
+            if (!RowPart::far(mean[p])) continue;
             const FarRow there = far_row(y[p], R.eps);
             y[p] = there.y;
             mean[p] = there.mean;

@@ -111,3 +111,31 @@ def test_rows_that_are_not_finite_or_zero(pa):
     for i, h in ((1, 2), (2, 3), (4, 0)):
         t.q_out[i, h] = clean[i, h]
     assert torch.equal(t.q_out, clean)
+
+
+@pytest.mark.parametrize("n", [40, 1200])
+def test_a_row_out_of_range_leaves_its_neighbours_alone(pa, n):
+    """Rows that share a warp with one that has to be scaled keep their bits."""
+    rng = np.random.default_rng(8)
+    dtype = torch.bfloat16
+    t = tokens(rng, n, 8, 3, dtype, [1.0])
+    w = weight(rng, dtype)
+    results = []
+    for _ in range(2):
+        p8, p16 = pa.Pool8(n, 3, type8("e4m3")), pa.Pool(n, 3, dtype)
+        pa.pa_norm_rope_append8(p8, *t.args(w, w, np.arange(n) * BS))
+        q = t.q_out.clone()
+        pa.pa_norm_rope_append(p16, *t.args(w, w, np.arange(n) * BS))
+        assert torch.equal(q, t.q_out)
+        results.append((raw(p8), p16.k.clone(), q))
+        t.k[3, 1] *= 2.0 ** 80
+        t.q[7, 5] *= 2.0 ** -90
+    (a, ka, qa), (b, kb, qb) = results
+    for x in (a, b):
+        for y in x:
+            y[3, 1] = 0
+    for x, y in zip(a, b):
+        assert np.array_equal(x, y)
+    ka[3, 1], kb[3, 1] = 0.0, 0.0
+    qa[7, 5], qb[7, 5] = 0.0, 0.0
+    assert torch.equal(ka, kb) and torch.equal(qa, qb)
