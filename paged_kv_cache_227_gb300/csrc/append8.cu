@@ -16,9 +16,9 @@
 // has 16 rows of four (kv head, K|V), whose angles are computed once.  Query rows
 // go as in the 16-bit appends, in the same launch, with the same bits.
 //
-// Measured: 7,900 tokens of 32 / 8 / 8 heads in 24 chunks (183 MB) 45 us, 0.60 of the
+// Measured: 7,900 tokens of 32 / 8 / 8 heads in 24 chunks (183 MB) 44 us, 0.61 of the
 // copy rate (K and V rows as they are, without query rows, 20); one token of 64 sequences
-// 5.7 us: three memory latencies (slots, rows and scales, codes) and the reduction
+// 5.6 us: three memory latencies (slots, rows and scales, codes) and the reduction
 // between them.  int8 codes: 1 us more for the chunks, 0.4 for a token.
 #include "codes8.cuh"
 #include "device_utils.cuh"
@@ -64,8 +64,8 @@ __device__ __forceinline__ bool another_run(const RopeArgs& R, uint32_t claim, u
 }
 
 // kTogether: rows of a lane whose norms are made side by side, 2 where latency counts and
-// registers are free, 1 where warps are many (us with 1 and 2: 64 tokens 5.97 and 5.68,
-// 7,900 tokens 43.7 and 44.9).
+// registers are free, 1 where warps are many (us with 1 and 2: 64 tokens 5.75 and 5.43,
+// 7,900 tokens 44.6 and 45.4).
 template <bool kBf16, bool kE4M3, bool kNorm, int kTogether>
 __device__ __forceinline__ void write_window(const Append8Args& A, Angles* s_angles) {
   __shared__ uint32_t s_top[2][kTasks8][kTok8], s_clash[2];
@@ -272,9 +272,10 @@ template <bool kBf16, bool kE4M3, int U, bool kNorm>
 __global__ void __launch_bounds__(kThreads8, U > 1 ? 3 : 2) append8_kernel(const __grid_constant__ Append8Args A) {
   constexpr int kWarps = kThreads8 / 32;
   constexpr int kRows = kNorm && U > 1 ? kWarps * 64 * U : 0;  // vectors of query rows that wait
-  // angles of a window, or the query rows' and the rows
+  // angles of a window, or the query rows' and the rows (128: what a row's lanes read
+  // together lies in one line; at 16 the chunks take 44.6 us instead of 43.7)
   constexpr int kQueries = kWarps * sizeof(Angles) + 16 * kRows, kKeys = kAngleRows * sizeof(Angles);
-  __shared__ __align__(16) uint8_t s_space[kQueries > kKeys ? kQueries : kKeys];
+  __shared__ __align__(128) uint8_t s_space[kQueries > kKeys ? kQueries : kKeys];
   Angles* const s_angles = reinterpret_cast<Angles*>(s_space);
   if (blockIdx.x < A.kv_ctas) {
     write_window<kBf16, kE4M3, kNorm, U == 1 ? 2 : 1>(A, s_angles);
